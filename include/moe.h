@@ -86,6 +86,8 @@ typedef enum { MOE_ACT_SILU = 0, MOE_ACT_SWIGLU = 1 } moe_act;
  *   layer   N, D, E, K, Dff (every intermediate of moe_layer_forward)
  *   layer_e4m3  the same for moe_layer_forward_e4m3 (0 unless D and Dff are
  *           multiples of 128)
+ *   rmsnorm_backward N, D; gated_linear, linear, gated_linear_backward,
+ *           linear_backward N, D, Dff (the dense operators below)
  * The sizes do not depend on the device. */
 size_t moe_workspace_size(const char* op, int N, int D, int E, int K, int Dff);
 
@@ -399,6 +401,88 @@ int moe_layer_launches_e4m3(int N, int D, int E, int K, int Dff, int act);
  * NULL.  Needs no workspace; enqueues one kernel on `stream`. */
 moe_status moe_routing_stats(const int32_t* expert_offsets, int E, float decay, float bias_step,
                              float* ema, float* bias, float* kl_out, void* stream);
+
+/* ---- The dense operators of a pre-norm feed-forward block around the layer:
+ * the norm in front of it, a dense gated expert beside the routed ones (a
+ * shared expert) and the projection onto the residual stream, each with its
+ * gradient.  bf16 tensors, fp32 sums; widths are positive multiples of 8 (rows
+ * start on 16-byte boundaries), any number of rows.  The pages describe the
+ * layer's inside only, so there is no passage to cite: the formulas below are
+ * the definitions.  The gradient entry points compute each output whose pointer
+ * is not NULL; with N = 0 the weight gradients are set to zero.
+ * Workspaces: moe_workspace_size(op, N, D, 0, 0, F) with op "gated_linear",
+ * "linear" (header only), "gated_linear_backward", "linear_backward",
+ * "rmsnorm_backward" (N, D). */
+
+/* Activations of the dense products.  GELU is z Phi(z); GELU_TANH its form
+ * z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+typedef enum {
+    MOE_FN_NONE = 0,
+    MOE_FN_RELU = 1,
+    MOE_FN_SILU = 2,
+    MOE_FN_GELU = 3,
+    MOE_FN_GELU_TANH = 4
+} moe_fn;
+
+/* Root-mean-square norm of the sum of x and the residual stream:
+ *   s = x + residual (s = x with residual NULL)
+ *   y = s * weight / sqrt(mean(s^2) + eps)
+ *   x, residual  [N,D] bf16, weight [D] bf16, eps >= 0, D <= 32768
+ *   y            [N,D] bf16 out, or NULL
+ *   yq, y_scale  [N,D] e4m3 codes and [N] fp32 scales out (together), or NULL:
+ *                y quantised per row by moe_quantize_e4m3's rule, from the fp32
+ *                y, so each code is rounded once (a code may differ by one step
+ *                from quantising the bf16 y).  They feed moe_permute_e4m3.  As
+ *                in moe_quantize_e4m3 an infinity saturates at +-448 and a NaN
+ *                stays one.
+ *   residual_out [N,D] bf16 out, or NULL: s.  May be x or residual itself;
+ *                other outputs overlap no input.
+ * Sums, statistics and y before its rounding are fp32.  Needs no workspace. */
+moe_status moe_rmsnorm(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int N, int D, float eps,
+                       moe_bf16* y, uint8_t* yq, float* y_scale, moe_bf16* residual_out, void* stream);
+
+/* Gradient of moe_rmsnorm.  With r = 1/sqrt(mean(s^2) + eps), v = dy * weight:
+ *   dx = r v - s r^3 mean(v s) + dresidual     (the gradient of x and of the
+ *                                              residual alike)
+ *   dweight = sum over rows of dy s r
+ *   dy [N,D] bf16; s [N,D] bf16: what moe_rmsnorm wrote to residual_out (or x);
+ *   dresidual [N,D] bf16 or NULL: the gradient that reached residual_out;
+ *   dx [N,D] bf16 out; dweight [D] fp32 out or NULL (summed in a fixed order). */
+moe_status moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* s, const moe_bf16* weight,
+                                const moe_bf16* dresidual, int N, int D, float eps, moe_bf16* dx, float* dweight,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* Gated product, the up half of a dense expert, in one launch:
+ *   g = x w1^T, u = x w3^T, h = fn(g) * u
+ *   x [N,D], w1 and w3 [F,D] bf16; h [N,F] bf16 out, from the fp32 g and u;
+ *   g, u [N,F] bf16 out or NULL: kept for the backward pass. */
+moe_status moe_gated_linear(const moe_bf16* x, const moe_bf16* w1, const moe_bf16* w3, int N, int D, int F, int fn,
+                            moe_bf16* h, moe_bf16* g, moe_bf16* u, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_gated_linear from dh [N,F] and what it kept:
+ *   dg = dh u fn'(g), du = dh fn(g)   (rounded to bf16: operands of products)
+ *   dx [N,D] = dg w1 + du w3;  dw1 [F,D] = dg^T x;  dw3 [F,D] = du^T x
+ * dx, or dw1 and dw3 together, may be NULL. */
+moe_status moe_gated_linear_backward(const moe_bf16* dh, const moe_bf16* x, const moe_bf16* w1, const moe_bf16* w3,
+                                     const moe_bf16* g, const moe_bf16* u, int N, int D, int F, int fn, moe_bf16* dx,
+                                     moe_bf16* dw1, moe_bf16* dw3, void* ws, size_t ws_bytes, void* stream);
+
+/* Linear product with bias, activation and residual in its epilogue:
+ *   z = x w^T + bias,  y = residual + fn(z)
+ *   x [N,D], w [F,D], residual [N,F] (or NULL) bf16; bias [F] fp32 or NULL;
+ *   y [N,F] bf16 out (may be residual itself); z [N,F] bf16 out or NULL: kept
+ *   for the backward pass. */
+moe_status moe_linear(const moe_bf16* x, const moe_bf16* w, const float* bias, const moe_bf16* residual, int N, int D,
+                      int F, int fn, moe_bf16* y, moe_bf16* z, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_linear from dy [N,F] (also the residual's gradient):
+ *   dz = dy fn'(z) (rounded to bf16 where fn is not MOE_FN_NONE; z is not read
+ *   and may be NULL where it is)
+ *   dx [N,D] = dz w;  dw [F,D] = dz^T x;  dbias [F] fp32 = sum over rows of dz,
+ *   from the unrounded dz in a fixed order.  Each may be NULL. */
+moe_status moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, const moe_bf16* w, const moe_bf16* z, int N,
+                               int D, int F, int fn, moe_bf16* dx, moe_bf16* dw, float* dbias, void* ws,
+                               size_t ws_bytes, void* stream);
 
 /* Number of kernels moe_layer_forward (capacity < 0) or
  * moe_layer_forward_padded (capacity >= 0) launches for these sizes on the

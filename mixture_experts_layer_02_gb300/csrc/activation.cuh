@@ -1,0 +1,86 @@
+// activation.cuh -- the activation functions of the dense products and their
+// slopes, in fp32.  One definition for the forward epilogues and the backward
+// kernels.
+#pragma once
+
+#include "device.cuh"
+
+namespace moe {
+
+// moe_fn of include/moe.h
+enum { FN_NONE = 0, FN_RELU = 1, FN_SILU = 2, FN_GELU = 3, FN_GELU_TANH = 4 };
+
+// The tanh form of GELU is z * sigmoid(2 q), q = sqrt(2/pi) (z + 0.044715 z^3):
+// (1 + tanh q) / 2 is the sigmoid of 2 q, so no difference of near-equal
+// numbers is formed for negative z.  kGeluTanh2 = 2 sqrt(2/pi).
+constexpr float kGeluTanh2 = 1.5957691216057308f;
+constexpr float kGeluCubic = 0.044715f;
+
+// The normal distribution function by erfc: 1 + erf would cancel for negative z.
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
+
+// fn is the same for every thread of a launch.  A NaN comes out a NaN.
+__device__ __forceinline__ float act_value(int fn, float z) {
+    switch (fn) {
+        case FN_RELU: return z <= 0.0f ? 0.0f : z;
+        case FN_SILU: return silu_f32(z);
+        case FN_GELU: return z * normal_cdf(z);
+        case FN_GELU_TANH: return __fdividef(z, 1.0f + __expf(-kGeluTanh2 * (z + kGeluCubic * z * z * z)));
+        default: return z;
+    }
+}
+
+// Value and slope together (the gated backward needs both).  The exponential
+// is taken of -|q|, so neither e^-|q| nor the sum 1 + e^-|q| can overflow.
+__device__ __forceinline__ float sigmoid_f32(float q, float& one_minus) {
+    const float e = __expf(-fabsf(q));
+    const float r = __fdividef(1.0f, 1.0f + e);
+    const float small = e * r;  // the sigmoid of -|q|
+    one_minus = q >= 0.0f ? small : r;
+    return q >= 0.0f ? r : small;
+}
+
+__device__ __forceinline__ float act_slope(int fn, float z, float& value) {
+    switch (fn) {
+        case FN_RELU:
+            value = z <= 0.0f ? 0.0f : z;
+            return z <= 0.0f ? 0.0f : (z > 0.0f ? 1.0f : z);
+        case FN_SILU: {
+            float m;
+            const float p = sigmoid_f32(z, m);
+            value = z * p;
+            return p * (1.0f + z * m);
+        }
+        case FN_GELU: {
+            const float c = normal_cdf(z);
+            value = z * c;
+            return c + z * 0.3989422804014327f * __expf(-0.5f * z * z);  // 1/sqrt(2 pi)
+        }
+        case FN_GELU_TANH: {
+            float m;
+            const float p = sigmoid_f32(kGeluTanh2 * (z + kGeluCubic * z * z * z), m);
+            value = z * p;
+            return p * (1.0f + z * m * kGeluTanh2 * (1.0f + 3.0f * kGeluCubic * z * z));
+        }
+        default:
+            value = z;
+            return 1.0f;
+    }
+}
+
+// Eight bf16 values in 16 bytes, to and from fp32.
+__device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
+}  // namespace moe

@@ -1,0 +1,344 @@
+// dense_api.cu -- the C entry points of the dense operators (include/moe.h):
+// argument checks, workspace carving, the choice of kernel and the launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+
+#include "../../include/moe.h"
+#include "common.h"
+#include "dense.h"
+
+using namespace moe;
+
+namespace {
+
+moe_status refuse(moe_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_error_detail(buf);
+    return s;
+}
+
+moe_status launched(cudaError_t e, const char* where) {
+    if (e == cudaSuccess) return MOE_OK;
+    return refuse(MOE_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+#define NEED(p)                                                                            \
+    do {                                                                                   \
+        if ((p) == nullptr) return refuse(MOE_ERR_INVALID_ARG, "%s is NULL", #p);          \
+        if (misaligned(p)) return refuse(MOE_ERR_INVALID_ARG, "%s not 16-byte aligned", #p); \
+    } while (0)
+
+#define MAY(p)                                                                             \
+    do {                                                                                   \
+        if ((p) != nullptr && misaligned(p))                                               \
+            return refuse(MOE_ERR_INVALID_ARG, "%s not 16-byte aligned", #p);              \
+    } while (0)
+
+#define NEED_WS(bytes)                                                                     \
+    do {                                                                                   \
+        NEED(ws);                                                                          \
+        const size_t need_ = (bytes);                                                      \
+        if (ws_bytes < need_)                                                              \
+            return refuse(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need_); \
+    } while (0)
+
+// rows * width stays below 2^40, tile counts below 2^31
+moe_status check_widths(int N, int D, int F) {
+    if (N < 0) return refuse(MOE_ERR_INVALID_ARG, "N=%d < 0", N);
+    if (D < 8 || D % 8) return refuse(MOE_ERR_INVALID_ARG, "D=%d not a positive multiple of 8", D);
+    if (F < 8 || F % 8) return refuse(MOE_ERR_INVALID_ARG, "F=%d not a positive multiple of 8", F);
+    if (static_cast<long long>(N) * std::max(D, F) >= (1LL << 40) || static_cast<long long>(D) * F >= (1LL << 40))
+        return refuse(MOE_ERR_INVALID_ARG, "N=%d, D=%d, F=%d too large", N, D, F);
+    return MOE_OK;
+}
+
+moe_status check_fn(int fn) {
+    return fn < MOE_FN_NONE || fn > MOE_FN_GELU_TANH ? refuse(MOE_ERR_INVALID_ARG, "fn=%d outside 0..4", fn) : MOE_OK;
+}
+
+moe_status check_norm(int N, int D, float eps) {
+    if (N < 0) return refuse(MOE_ERR_INVALID_ARG, "N=%d < 0", N);
+    if (D < 8 || D % 8) return refuse(MOE_ERR_INVALID_ARG, "D=%d not a positive multiple of 8", D);
+    if (D > kNormMaxD) return refuse(MOE_ERR_UNSUPPORTED, "D=%d above %d", D, kNormMaxD);
+    if (!(eps >= 0.0f) || eps > 1e30f) return refuse(MOE_ERR_INVALID_ARG, "eps=%g is not a finite number >= 0", eps);
+    return MOE_OK;
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// byte offsets of the backward workspaces (the header first)
+struct BackwardLayout {
+    size_t d0, d1, partial, total;
+};
+
+BackwardLayout backward_layout(int N, int F, int grads, int parts) {
+    BackwardLayout l;
+    const size_t one = up256(static_cast<size_t>(N) * F * 2);
+    l.d0 = kWsHeaderBytes;
+    l.d1 = l.d0 + one;
+    l.partial = l.d0 + one * grads;
+    l.total = l.partial + up256(static_cast<size_t>(parts) * F * sizeof(float));
+    return l;
+}
+
+uint8_t* at(void* ws, size_t off) { return static_cast<uint8_t*>(ws) + off; }
+
+int device_sms() {
+    int dev = 0, n = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
+
+// Cluster size of the one-CTA tiles: the S of 1, 2, 4, 8 with the least time in
+// k-blocks, ceil(tiles S / SMs) rounds of total / S blocks each, plus about four
+// blocks of fill and join per round.
+int plan_cluster(long long tiles, int kblocks) {
+    if (const char* f = getenv("MOE_DENSE_SPLITS")) {
+        const int s = atoi(f);
+        if (s == 1 || s == 2 || s == 4 || s == 8) return std::min(s, kblocks < 2 ? 1 : (kblocks < 4 ? 2 : (kblocks < 8 ? 4 : 8)));
+    }
+    const int n = device_sms();
+    int best = 1;
+    double best_cost = 1e30;
+    for (int s = 1; s <= 8 && s <= kblocks; s *= 2) {
+        const double rounds = static_cast<double>((tiles * s + n - 1) / n);
+        const double cost = rounds * (static_cast<double>(kblocks) / s + 4.0);
+        if (cost < best_cost - 1e-9) {
+            best_cost = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+// One product: tensor maps, the choice of kernel, the launch.
+moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
+    const bool a_mn = kind == DENSE_WGRAD, b_mn = kind == DENSE_DGRAD || kind == DENSE_WGRAD;
+    CUtensorMap m[4];
+    auto map_a = [&](CUtensorMap* t, const uint16_t* p) {
+        return a_mn ? make_bf16_map(t, p, a.K, a.M, 64) : make_bf16_map(t, p, a.M, a.K, kBM);
+    };
+    auto map_b = [&](CUtensorMap* t, const uint16_t* p) {
+        return b_mn ? make_bf16_map(t, p, a.K, a.N, 64)
+                    : make_bf16_map(t, p, a.N, a.K, kind == DENSE_GATED ? 64 : 128);
+    };
+    int s = map_a(&m[0], o.a0);
+    if (s == 0 && o.a1) s = map_a(&m[1], o.a1);
+    if (s == 0) s = map_b(&m[2], o.b0);
+    if (s == 0 && o.b1) s = map_b(&m[3], o.b1);
+    if (s != 0) return static_cast<moe_status>(s);
+    if (!o.a1) m[1] = m[0];
+    if (!o.b1) m[3] = m[2];
+    const int n_tile = kind == DENSE_GATED ? 64 : 128;
+    const long long tiles = static_cast<long long>((a.M + kBM - 1) / kBM) * ((a.N + n_tile - 1) / n_tile) * a.mats;
+    const int kblocks = (a.K + kBK - 1) / kBK * a.segs;
+    return launched(launch_dense_split(kind, m, a, plan_cluster(tiles, kblocks), st), "dense product launch");
+}
+
+DenseArgs args_of(int M, int N, int K, void* ws) {
+    DenseArgs a = {};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.segs = a.mats = 1;
+    a.err = static_cast<uint32_t*>(ws);
+    a.dbg = static_cast<const uint32_t*>(ws) + 1;
+    return a;
+}
+
+// A gradient of no rows is zero.
+moe_status zero(void* p, size_t bytes, cudaStream_t st) {
+    return p ? launched(cudaMemsetAsync(p, 0, bytes, st), "zero gradient") : MOE_OK;
+}
+
+}  // namespace
+
+// Workspace bytes of a dense operation, 0 for another name or invalid sizes.
+size_t moe::dense_workspace_size(const char* op, int N, int D, int F) {
+    if (!strcmp(op, "rmsnorm_backward")) {
+        if (check_norm(N, D, 0.0f) != MOE_OK) return 0;
+        return kWsHeaderBytes + up256(static_cast<size_t>(rmsnorm_bwd_parts(N)) * D * sizeof(float));
+    }
+    const bool gated = !strcmp(op, "gated_linear_backward");
+    if (!strcmp(op, "gated_linear") || !strcmp(op, "linear"))
+        return check_widths(N, D, F) == MOE_OK ? kWsHeaderBytes : 0;
+    if (!gated && strcmp(op, "linear_backward")) return 0;
+    if (check_widths(N, D, F) != MOE_OK) return 0;
+    return backward_layout(N, F, gated ? 2 : 1, gated ? 0 : linear_grad_parts(N)).total;
+}
+
+extern "C" {
+
+moe_status moe_rmsnorm(const moe_bf16* x, const moe_bf16* residual, const moe_bf16* weight, int N, int D, float eps,
+                       moe_bf16* y, uint8_t* yq, float* y_scale, moe_bf16* residual_out, void* stream) {
+    moe_status s = check_norm(N, D, eps);
+    if (s != MOE_OK) return s;
+    if (N == 0) return MOE_OK;
+    NEED(x);
+    MAY(residual);
+    NEED(weight);
+    MAY(y);
+    MAY(yq);
+    MAY(y_scale);
+    MAY(residual_out);
+    if (!y && !yq && !residual_out) return refuse(MOE_ERR_INVALID_ARG, "no output: y, yq and residual_out are NULL");
+    if ((yq == nullptr) != (y_scale == nullptr)) return refuse(MOE_ERR_INVALID_ARG, "yq and y_scale come together");
+    const NormArgs a = {x, residual, weight, y, yq, y_scale, residual_out, N, D, eps};
+    return launched(launch_rmsnorm(a, static_cast<cudaStream_t>(stream)), "rmsnorm launch");
+}
+
+moe_status moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* s_in, const moe_bf16* weight,
+                                const moe_bf16* dresidual, int N, int D, float eps, moe_bf16* dx, float* dweight,
+                                void* ws, size_t ws_bytes, void* stream) {
+    moe_status s = check_norm(N, D, eps);
+    if (s != MOE_OK) return s;
+    MAY(dweight);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N == 0) return zero(dweight, static_cast<size_t>(D) * sizeof(float), st);
+    NEED(dy);
+    NEED(s_in);
+    NEED(weight);
+    MAY(dresidual);
+    NEED(dx);
+    NEED_WS(dense_workspace_size("rmsnorm_backward", N, D, 0));
+    const NormBwdArgs a = {dy, s_in, weight, dresidual, dx, dweight, reinterpret_cast<float*>(at(ws, kWsHeaderBytes)),
+                           N, D, eps};
+    return launched(launch_rmsnorm_bwd(a, st), "rmsnorm backward launch");
+}
+
+moe_status moe_gated_linear(const moe_bf16* x, const moe_bf16* w1, const moe_bf16* w3, int N, int D, int F, int fn,
+                            moe_bf16* h, moe_bf16* g, moe_bf16* u, void* ws, size_t ws_bytes, void* stream) {
+    moe_status s = check_widths(N, D, F);
+    if (s == MOE_OK) s = check_fn(fn);
+    if (s != MOE_OK) return s;
+    if (N == 0) return MOE_OK;
+    NEED(x);
+    NEED(w1);
+    NEED(w3);
+    NEED(h);
+    MAY(g);
+    MAY(u);
+    NEED_WS(kWsHeaderBytes);
+    DenseArgs a = args_of(N, F, D, ws);
+    a.fn = fn;
+    a.out0 = h;
+    a.out1 = g;
+    a.out2 = u;
+    return product(DENSE_GATED, {x, nullptr, w1, w3}, a, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_gated_linear_backward(const moe_bf16* dh, const moe_bf16* x, const moe_bf16* w1, const moe_bf16* w3,
+                                     const moe_bf16* g, const moe_bf16* u, int N, int D, int F, int fn, moe_bf16* dx,
+                                     moe_bf16* dw1, moe_bf16* dw3, void* ws, size_t ws_bytes, void* stream) {
+    moe_status s = check_widths(N, D, F);
+    if (s == MOE_OK) s = check_fn(fn);
+    if (s != MOE_OK) return s;
+    MAY(dx);
+    MAY(dw1);
+    MAY(dw3);
+    if ((dw1 == nullptr) != (dw3 == nullptr)) return refuse(MOE_ERR_INVALID_ARG, "dw1 and dw3 come together");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N == 0) {
+        const size_t bytes = static_cast<size_t>(D) * F * 2;
+        s = zero(dw1, bytes, st);
+        return s == MOE_OK ? zero(dw3, bytes, st) : s;
+    }
+    NEED(dh);
+    NEED(x);
+    NEED(w1);
+    NEED(w3);
+    NEED(g);
+    NEED(u);
+    const BackwardLayout l = backward_layout(N, F, 2, 0);
+    NEED_WS(l.total);
+    uint16_t* dg = reinterpret_cast<uint16_t*>(at(ws, l.d0));
+    uint16_t* du = reinterpret_cast<uint16_t*>(at(ws, l.d1));
+    s = launched(launch_gated_grad(dh, g, u, fn, static_cast<long long>(N) * F, dg, du, st), "gated gradient launch");
+    if (s == MOE_OK && dx) {
+        DenseArgs a = args_of(N, D, F, ws);
+        a.segs = 2;
+        a.out0 = dx;
+        s = product(DENSE_DGRAD, {dg, du, w1, w3}, a, st);
+    }
+    if (s == MOE_OK && dw1) {
+        DenseArgs a = args_of(F, D, N, ws);
+        a.mats = 2;
+        a.out0 = dw1;
+        a.out1 = dw3;
+        s = product(DENSE_WGRAD, {dg, du, x, nullptr}, a, st);
+    }
+    return s;
+}
+
+moe_status moe_linear(const moe_bf16* x, const moe_bf16* w, const float* bias, const moe_bf16* residual, int N, int D,
+                      int F, int fn, moe_bf16* y, moe_bf16* z, void* ws, size_t ws_bytes, void* stream) {
+    moe_status s = check_widths(N, D, F);
+    if (s == MOE_OK) s = check_fn(fn);
+    if (s != MOE_OK) return s;
+    if (N == 0) return MOE_OK;
+    NEED(x);
+    NEED(w);
+    MAY(bias);
+    MAY(residual);
+    NEED(y);
+    MAY(z);
+    NEED_WS(kWsHeaderBytes);
+    DenseArgs a = args_of(N, F, D, ws);
+    a.fn = fn;
+    a.bias = bias;
+    a.residual = residual;
+    a.out0 = y;
+    a.out1 = z;
+    return product(DENSE_LINEAR, {x, nullptr, w, nullptr}, a, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, const moe_bf16* w, const moe_bf16* z, int N,
+                               int D, int F, int fn, moe_bf16* dx, moe_bf16* dw, float* dbias, void* ws,
+                               size_t ws_bytes, void* stream) {
+    moe_status s = check_widths(N, D, F);
+    if (s == MOE_OK) s = check_fn(fn);
+    if (s != MOE_OK) return s;
+    MAY(dx);
+    MAY(dw);
+    MAY(dbias);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (N == 0) {
+        s = zero(dw, static_cast<size_t>(D) * F * 2, st);
+        return s == MOE_OK ? zero(dbias, static_cast<size_t>(F) * sizeof(float), st) : s;
+    }
+    NEED(dy);
+    NEED(x);
+    NEED(w);
+    if (fn != MOE_FN_NONE) NEED(z);
+    const BackwardLayout l = backward_layout(N, F, 1, linear_grad_parts(N));
+    NEED_WS(l.total);
+    uint16_t* dz = reinterpret_cast<uint16_t*>(at(ws, l.d0));
+    s = launched(launch_linear_grad(dy, z, fn, N, F, dz, dbias, reinterpret_cast<float*>(at(ws, l.partial)), st),
+                 "linear gradient launch");
+    const uint16_t* grad = fn == MOE_FN_NONE ? dy : dz;
+    if (s == MOE_OK && dx) {
+        DenseArgs a = args_of(N, D, F, ws);
+        a.out0 = dx;
+        s = product(DENSE_DGRAD, {grad, nullptr, w, nullptr}, a, st);
+    }
+    if (s == MOE_OK && dw) {
+        DenseArgs a = args_of(F, D, N, ws);
+        a.out0 = dw;
+        s = product(DENSE_WGRAD, {grad, nullptr, x, nullptr}, a, st);
+    }
+    return s;
+}
+
+}  // extern "C"

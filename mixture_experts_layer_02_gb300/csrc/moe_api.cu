@@ -16,6 +16,7 @@
 
 #include "../../include/moe.h"
 #include "common.h"
+#include "dense.h"
 
 using namespace moe;
 
@@ -152,6 +153,11 @@ moe_status check_sizes(int N, int D, int E, int K, int Dff, bool need_dff) {
 // The size checks of moe_permute, shared with the allocation-free variant in
 // permute.cu so that both reject exactly the same arguments.
 int moe::check_permute_sizes(int N, int D, int E, int K) { return check_sizes(N, D, E, K, 64, false); }
+
+// The tensor map of a bf16 matrix, for the dense products (dense_api.cu).
+int moe::make_bf16_map(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows) {
+    return make_tmap(m, base, rows, cols, box_rows);
+}
 
 namespace {
 
@@ -1000,7 +1006,7 @@ size_t moe_workspace_size(const char* op, int N, int D, int E, int K, int Dff) {
         if (check_sizes(N, D, E, K, Dff, true) != MOE_OK || D % 128 || Dff % 128) return 0;
         return e4m3_layout(N, D, E, K, Dff).total;
     }
-    return 0;
+    return dense_workspace_size(op, N, D, Dff);
 }
 
 int moe_layer_workspace_layout(int N, int D, int E, int K, int Dff, size_t out[8]) {

@@ -34,6 +34,12 @@ SIGMOID_NORM = 1
 ACT_SILU = 0
 ACT_SWIGLU = 1
 
+FN_NONE = 0
+FN_RELU = 1
+FN_SILU = 2
+FN_GELU = 3
+FN_GELU_TANH = 4
+
 EXPORTED = (
     "moe_workspace_size", "moe_route", "moe_permute", "moe_route_permute", "moe_grouped_ffn", "moe_combine",
     "moe_layer_forward", "moe_layer_workspace_layout", "moe_read_device_error",
@@ -44,6 +50,8 @@ EXPORTED = (
     "moe_quantize_e4m3", "moe_permute_e4m3", "moe_grouped_ffn_e4m3", "moe_layer_forward_e4m3",
     "moe_layer_e4m3_workspace_layout", "moe_layer_launches_e4m3", "moe_permute_indices",
     "moe_grouped_ffn_gathered", "moe_grouped_ffn_e4m3_gathered",
+    "moe_rmsnorm", "moe_rmsnorm_backward", "moe_gated_linear", "moe_gated_linear_backward",
+    "moe_linear", "moe_linear_backward",
 )
 
 _lock = threading.Lock()
@@ -120,6 +128,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.moe_grouped_ffn_e4m3_gathered.restype = i
         L.moe_grouped_ffn_e4m3_gathered.argtypes = [p, p, i, p, p, i, p, p, p, p, p, p, i, i, i, i,
                                                     p, p, p, p, p, sz, p]
+        f = ctypes.c_float
+        L.moe_rmsnorm.restype = i
+        L.moe_rmsnorm.argtypes = [p, p, p, i, i, f, p, p, p, p, p]
+        L.moe_rmsnorm_backward.restype = i
+        L.moe_rmsnorm_backward.argtypes = [p, p, p, p, i, i, f, p, p, p, sz, p]
+        L.moe_gated_linear.restype = i
+        L.moe_gated_linear.argtypes = [p, p, p, i, i, i, i, p, p, p, p, sz, p]
+        L.moe_gated_linear_backward.restype = i
+        L.moe_gated_linear_backward.argtypes = [p, p, p, p, p, p, i, i, i, i, p, p, p, p, sz, p]
+        L.moe_linear.restype = i
+        L.moe_linear.argtypes = [p, p, p, p, i, i, i, i, p, p, p, sz, p]
+        L.moe_linear_backward.restype = i
+        L.moe_linear_backward.argtypes = [p, p, p, p, i, i, i, i, p, p, p, p, sz, p]
         L.moe_read_device_error.restype = i
         L.moe_read_device_error.argtypes = [p, p]
         L.moe_clear_device_error.restype = i
@@ -645,3 +666,172 @@ def moe_grouped_ffn_e4m3_gathered(xq, x_scale, perm_src, expert_offsets, w1q, s1
         _ptr(w3q) if sw else None, _ptr(s3) if sw else None, _ptr(w2q), _ptr(s2), E, D, Dff, act,
         _ptr(h), _ptr(hq), _ptr(h_scale), _ptr(y_perm), _ptr(ws), ws.numel(), _stream(stream)))
     return h, hq, h_scale, y_perm
+
+
+# ---------------------------------------------------------------- dense operators (norm, gated and linear products)
+class _on_stream:
+    """Allocations inside belong to the stream the call runs on, so that the
+    allocator does not hand a freed buffer to another stream too early."""
+
+    def __init__(self, stream):
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def _scratch(op, N, D, F, device):
+    """A workspace of one call: only its header is zeroed.  Invalid sizes get a
+    bare header: the entry point then says what is wrong with them."""
+    ws = torch.empty(max(workspace_size(op, N=N, D=D, Dff=F), 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_all(*specs):
+    """(tensor or None, dtype, shape, name) for each argument."""
+    for t, dtype, shape, name in specs:
+        if t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+            continue
+        _need(t, dtype, shape, name)
+
+
+def _rows(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected [rows, width], got {tuple(t.shape)}")
+    return t.shape
+
+
+def moe_rmsnorm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False, y=None, yq=None, y_scale=None,
+                residual_out=None, stream=None):
+    """s = x + residual; y = s / sqrt(mean(s^2) + eps) * weight.  Returns
+    (y, yq, y_scale, s): yq and y_scale (e4m3 codes as uint8 and one scale a
+    row, as moe_permute_e4m3 takes them) with quantize=True or when passed, s
+    (the new residual stream) when a residual is given or residual_out is
+    passed; None for the others."""
+    N, D = _rows(x, "x")
+    with _on_stream(stream):
+        y = torch.empty_like(x) if y is None else y
+        if quantize or yq is not None or y_scale is not None:
+            yq = torch.empty((N, D), dtype=torch.uint8, device=x.device) if yq is None else yq
+            y_scale = torch.empty(N, dtype=torch.float32, device=x.device) if y_scale is None else y_scale
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(x)
+    bf16 = torch.bfloat16
+    _check_all((x, bf16, (N, D), "x"), (weight, bf16, (D,), "weight"), (residual, bf16, (N, D), "residual"),
+               (y, bf16, (N, D), "y"), (yq, torch.uint8, (N, D), "yq"), (y_scale, torch.float32, (N,), "y_scale"),
+               (residual_out, bf16, (N, D), "residual_out"))
+    _check("moe_rmsnorm", load().moe_rmsnorm(
+        _addr(x), _addr(residual), _addr(weight), N, D, eps, _addr(y), _addr(yq), _addr(y_scale), _addr(residual_out),
+        _stream(stream)))
+    return y, yq, y_scale, residual_out
+
+
+def moe_rmsnorm_backward(dy, s, weight, dresidual=None, eps: float = 1e-6, dx=None, dweight=None, ws=None, stream=None):
+    """Gradient of moe_rmsnorm from dy and s (its fourth result, or x without a
+    residual): (dx, dweight), dx for x and the residual alike, dweight fp32.
+    dresidual is the gradient that reached s itself."""
+    N, D = _rows(s, "s")
+    with _on_stream(stream):
+        dx = torch.empty_like(s) if dx is None else dx
+        dweight = torch.empty(D, dtype=torch.float32, device=s.device) if dweight is None else dweight
+        ws = _scratch("rmsnorm_backward", N, D, 0, s.device) if ws is None else ws
+    bf16 = torch.bfloat16
+    _check_all((dy, bf16, (N, D), "dy"), (s, bf16, (N, D), "s"), (weight, bf16, (D,), "weight"),
+               (dresidual, bf16, (N, D), "dresidual"), (dx, bf16, (N, D), "dx"), (dweight, torch.float32, (D,), "dweight"))
+    _check("moe_rmsnorm_backward", load().moe_rmsnorm_backward(
+        _addr(dy), _addr(s), _addr(weight), _addr(dresidual), N, D, eps, _addr(dx), _addr(dweight), _addr(ws), ws.numel(),
+        _stream(stream)))
+    return dx, dweight
+
+
+def moe_gated_linear(x, w1, w3, fn: int = FN_SILU, save: bool = False, h=None, g=None, u=None, ws=None, stream=None):
+    """h = fn(x w1^T) * (x w3^T) for weights [F, D].  Returns (h, g, u); g and u
+    (the two projections, for the backward pass) are None unless save=True or
+    they are passed."""
+    N, D = _rows(x, "x")
+    F = w1.shape[0]
+    bf16 = torch.bfloat16
+    with _on_stream(stream):
+        h = torch.empty((N, F), dtype=bf16, device=x.device) if h is None else h
+        if save:
+            g = torch.empty_like(h) if g is None else g
+            u = torch.empty_like(h) if u is None else u
+        ws = _scratch("gated_linear", N, D, F, x.device) if ws is None else ws
+    _check_all((x, bf16, (N, D), "x"), (w1, bf16, (F, D), "w1"), (w3, bf16, (F, D), "w3"), (h, bf16, (N, F), "h"),
+               (g, bf16, (N, F), "g"), (u, bf16, (N, F), "u"))
+    _check("moe_gated_linear", load().moe_gated_linear(
+        _addr(x), _addr(w1), _addr(w3), N, D, F, fn, _addr(h), _addr(g), _addr(u), _addr(ws), ws.numel(),
+        _stream(stream)))
+    return h, g, u
+
+
+def moe_gated_linear_backward(dh, x, w1, w3, g, u, fn: int = FN_SILU, dx=None, dw1=None, dw3=None, ws=None, stream=None):
+    """Gradient of moe_gated_linear from dh and the g, u it kept: (dx, dw1, dw3)."""
+    N, D = _rows(x, "x")
+    F = w1.shape[0]
+    bf16 = torch.bfloat16
+    with _on_stream(stream):
+        dx = torch.empty_like(x) if dx is None else dx
+        dw1 = torch.empty_like(w1) if dw1 is None else dw1
+        dw3 = torch.empty_like(w3) if dw3 is None else dw3
+        ws = _scratch("gated_linear_backward", N, D, F, x.device) if ws is None else ws
+    _check_all((dh, bf16, (N, F), "dh"), (x, bf16, (N, D), "x"), (w1, bf16, (F, D), "w1"), (w3, bf16, (F, D), "w3"),
+               (g, bf16, (N, F), "g"), (u, bf16, (N, F), "u"), (dx, bf16, (N, D), "dx"), (dw1, bf16, (F, D), "dw1"),
+               (dw3, bf16, (F, D), "dw3"))
+    _check("moe_gated_linear_backward", load().moe_gated_linear_backward(
+        _addr(dh), _addr(x), _addr(w1), _addr(w3), _addr(g), _addr(u), N, D, F, fn, _addr(dx), _addr(dw1), _addr(dw3),
+        _addr(ws), ws.numel(), _stream(stream)))
+    return dx, dw1, dw3
+
+
+def moe_linear(x, w, bias=None, residual=None, fn: int = FN_NONE, save: bool = False, y=None, z=None, ws=None,
+               stream=None):
+    """y = residual + fn(x w^T + bias) for a weight [F, D] and an fp32 bias [F].
+    Returns (y, z); z (the pre-activation, for the backward pass) is None unless
+    save=True or it is passed."""
+    N, D = _rows(x, "x")
+    F = w.shape[0]
+    bf16 = torch.bfloat16
+    with _on_stream(stream):
+        y = torch.empty((N, F), dtype=bf16, device=x.device) if y is None else y
+        if save and z is None:
+            z = torch.empty_like(y)
+        ws = _scratch("linear", N, D, F, x.device) if ws is None else ws
+    _check_all((x, bf16, (N, D), "x"), (w, bf16, (F, D), "w"), (bias, torch.float32, (F,), "bias"),
+               (residual, bf16, (N, F), "residual"), (y, bf16, (N, F), "y"), (z, bf16, (N, F), "z"))
+    _check("moe_linear", load().moe_linear(
+        _addr(x), _addr(w), _addr(bias), _addr(residual), N, D, F, fn, _addr(y), _addr(z), _addr(ws), ws.numel(),
+        _stream(stream)))
+    return y, z
+
+
+def moe_linear_backward(dy, x, w, z=None, fn: int = FN_NONE, need_dbias: bool = False, dx=None, dw=None, dbias=None,
+                        ws=None, stream=None):
+    """Gradient of moe_linear from dy and the z it kept (not needed for
+    FN_NONE): (dx, dw, dbias); dbias is fp32, None unless need_dbias=True or it
+    is passed.  The residual's gradient is dy."""
+    N, D = _rows(x, "x")
+    F = w.shape[0]
+    bf16 = torch.bfloat16
+    with _on_stream(stream):
+        dx = torch.empty_like(x) if dx is None else dx
+        dw = torch.empty_like(w) if dw is None else dw
+        if need_dbias and dbias is None:
+            dbias = torch.empty(F, dtype=torch.float32, device=x.device)
+        ws = _scratch("linear_backward", N, D, F, x.device) if ws is None else ws
+    _check_all((dy, bf16, (N, F), "dy"), (x, bf16, (N, D), "x"), (w, bf16, (F, D), "w"), (z, bf16, (N, F), "z"),
+               (dx, bf16, (N, D), "dx"), (dw, bf16, (F, D), "dw"), (dbias, torch.float32, (F,), "dbias"))
+    _check("moe_linear_backward", load().moe_linear_backward(
+        _addr(dy), _addr(x), _addr(w), _addr(z), N, D, F, fn, _addr(dx), _addr(dw), _addr(dbias), _addr(ws), ws.numel(),
+        _stream(stream)))
+    return dx, dw, dbias
