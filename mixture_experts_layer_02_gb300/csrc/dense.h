@@ -93,7 +93,16 @@ size_t dense_workspace_size(const char* op, int N, int D, int F);
 
 // One CTA per 128 x 128 tile, the reduction over K split over a cluster of
 // `splits` CTAs (1, 2, 4 or 8) and joined through distributed shared memory.
+cudaError_t dense_split_limit(DenseKind kind, int splits, int* clusters);  // clusters the device holds at once
 cudaError_t launch_dense_split(DenseKind kind, const CUtensorMap* maps, const DenseArgs& a, int splits,
                                cudaStream_t st);
+
+// CTA pairs on 256 x 256 tiles, persistent: clusters of one pair (cluster = 2)
+// or of two pairs one above the other (4).
+constexpr int kPairTile = 256;
+// clusters the device holds at once
+cudaError_t dense_pair_limit(DenseKind kind, int cluster, int* clusters);
+cudaError_t launch_dense_pair(DenseKind kind, const CUtensorMap* maps, const DenseArgs& a, int cluster, int clusters,
+                              cudaStream_t st);
 
 }  // namespace moe

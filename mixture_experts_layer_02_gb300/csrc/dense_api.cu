@@ -95,44 +95,76 @@ BackwardLayout backward_layout(int N, int F, int grads, int parts) {
 
 uint8_t* at(void* ws, size_t off) { return static_cast<uint8_t*>(ws) + off; }
 
-int device_sms() {
-    int dev = 0, n = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
+// ---- the choice of kernel ----
+// Estimated microseconds, fitted to measured times (33 to 4096 rows, K 1024 to
+// 14336): a k-block (64 of K) of a one-CTA 128 x 128 tile takes 0.27 us with
+// the GPU full (the SMs' reads from L2 hold it back) and a round of such tiles
+// 5.5 us of first load, join and epilogue; a k-block of a 256 x 256 pair tile
+// 0.36 us, 0.95 of that where two pairs share an operand, and a round 3 us.
+constexpr double kSplitBlock = 0.27, kSplitRound = 5.5;
+constexpr double kPairBlock = 0.36, kPairRound = 3.0, kPairOnce = 3.0, kMulticastRate = 0.95;
+
+struct Plan {
+    int splits;             // split kernel: CTAs over K
+    int cluster, clusters;  // pair kernel (cluster 0: the split kernel)
+};
+
+int env_int(const char* name, int dflt) {
+    const char* f = getenv(name);
+    return f ? atoi(f) : dflt;
 }
 
-// Cluster size of the one-CTA tiles: the S of 1, 2, 4, 8 with the least time in
-// k-blocks, ceil(tiles S / SMs) rounds of total / S blocks each, plus about four
-// blocks of fill and join per round.
-int plan_cluster(long long tiles, int kblocks) {
-    if (const char* f = getenv("MOE_DENSE_SPLITS")) {
-        const int s = atoi(f);
-        if (s == 1 || s == 2 || s == 4 || s == 8) return std::min(s, kblocks < 2 ? 1 : (kblocks < 4 ? 2 : (kblocks < 8 ? 4 : 8)));
-    }
-    const int n = device_sms();
-    int best = 1;
-    double best_cost = 1e30;
+// MOE_DENSE_KERNEL = 1 (split) or 2 (pairs), MOE_DENSE_SPLITS and
+// MOE_DENSE_CLUSTER = 2 or 4 force a choice, for tuning and test coverage.
+moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p) {
+    const int n1 = kind == DENSE_GATED ? 64 : 128, n2 = kind == DENSE_GATED ? 128 : 256;
+    const long long t1 = static_cast<long long>((a.M + kBM - 1) / kBM) * ((a.N + n1 - 1) / n1) * a.mats;
+    const int kernel = env_int("MOE_DENSE_KERNEL", 0), fixed = env_int("MOE_DENSE_SPLITS", 0);
+    *p = {1, 0, 0};
+    double best = 1e30;
     for (int s = 1; s <= 8 && s <= kblocks; s *= 2) {
-        const double rounds = static_cast<double>((tiles * s + n - 1) / n);
-        const double cost = rounds * (static_cast<double>(kblocks) / s + 4.0);
-        if (cost < best_cost - 1e-9) {
-            best_cost = cost;
-            best = s;
+        if (fixed && s > fixed) break;
+        int limit = 0;
+        const moe_status st = launched(dense_split_limit(kind, s, &limit), "dense split limit");
+        if (st != MOE_OK) return st;
+        const double c = static_cast<double>((t1 + limit - 1) / limit) * (kblocks * kSplitBlock / s + kSplitRound);
+        if (fixed || c < best) best = c, p->splits = s;
+    }
+    if (kernel == 1) return MOE_OK;
+    if (kernel == 2) best = 1e30;
+    for (int cl = 2; cl <= 4; cl += 2) {
+        if (env_int("MOE_DENSE_CLUSTER", cl) != cl) continue;
+        int limit = 0;
+        const moe_status st = launched(dense_pair_limit(kind, cl, &limit), "dense pair limit");
+        if (st != MOE_OK) return st;
+        const int rows = kPairTile * cl / 2;
+        const long long tiles = static_cast<long long>((a.M + rows - 1) / rows) * ((a.N + n2 - 1) / n2) * a.mats;
+        const double block = kPairBlock * (cl == 2 ? 1.0 : kMulticastRate);
+        const double c = static_cast<double>((tiles + limit - 1) / limit) * (kblocks * block + kPairRound) + kPairOnce;
+        if (c < best) {
+            best = c;
+            p->cluster = cl;
+            p->clusters = static_cast<int>(std::min<long long>(tiles, limit));
         }
     }
-    return best;
+    return MOE_OK;
 }
 
 // One product: tensor maps, the choice of kernel, the launch.
 moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
     const bool a_mn = kind == DENSE_WGRAD, b_mn = kind == DENSE_DGRAD || kind == DENSE_WGRAD;
+    const int kblocks = (a.K + kBK - 1) / kBK * a.segs;
+    Plan p;
+    const moe_status planned = plan_product(kind, a, kblocks, &p);
+    if (planned != MOE_OK) return planned;
+    // K-major boxes: 128 rows of A; of B what one CTA loads at a time
+    const int b_rows = p.cluster ? 256 / p.cluster : (kind == DENSE_GATED ? 64 : 128);
     CUtensorMap m[4];
-    auto map_a = [&](CUtensorMap* t, const uint16_t* p) {
-        return a_mn ? make_bf16_map(t, p, a.K, a.M, 64) : make_bf16_map(t, p, a.M, a.K, kBM);
+    auto map_a = [&](CUtensorMap* t, const uint16_t* q) {
+        return a_mn ? make_bf16_map(t, q, a.K, a.M, 64) : make_bf16_map(t, q, a.M, a.K, kBM);
     };
-    auto map_b = [&](CUtensorMap* t, const uint16_t* p) {
-        return b_mn ? make_bf16_map(t, p, a.K, a.N, 64)
-                    : make_bf16_map(t, p, a.N, a.K, kind == DENSE_GATED ? 64 : 128);
+    auto map_b = [&](CUtensorMap* t, const uint16_t* q) {
+        return b_mn ? make_bf16_map(t, q, a.K, a.N, 64) : make_bf16_map(t, q, a.N, a.K, b_rows);
     };
     int s = map_a(&m[0], o.a0);
     if (s == 0 && o.a1) s = map_a(&m[1], o.a1);
@@ -141,10 +173,8 @@ moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, c
     if (s != 0) return static_cast<moe_status>(s);
     if (!o.a1) m[1] = m[0];
     if (!o.b1) m[3] = m[2];
-    const int n_tile = kind == DENSE_GATED ? 64 : 128;
-    const long long tiles = static_cast<long long>((a.M + kBM - 1) / kBM) * ((a.N + n_tile - 1) / n_tile) * a.mats;
-    const int kblocks = (a.K + kBK - 1) / kBK * a.segs;
-    return launched(launch_dense_split(kind, m, a, plan_cluster(tiles, kblocks), st), "dense product launch");
+    if (!p.cluster) return launched(launch_dense_split(kind, m, a, p.splits, st), "dense product launch");
+    return launched(launch_dense_pair(kind, m, a, p.cluster, p.clusters, st), "dense pair product launch");
 }
 
 DenseArgs args_of(int M, int N, int K, void* ws) {

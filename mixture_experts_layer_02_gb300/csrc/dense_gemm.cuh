@@ -49,6 +49,50 @@ __host__ __device__ constexpr uint32_t dense_idesc(int M, int N) {
     return idesc_bf16_f32(M, N) | (DenseLayout<KIND>::A_MN ? 1u << 15 : 0u) | (DenseLayout<KIND>::B_MN ? 1u << 16 : 0u);
 }
 
+// tma_load_2d_pair into the CTAs of `mask` at the same offset; each copy's bytes
+// are counted in the destination's pair, on the CTA of bar_cluster's parity.
+__device__ __forceinline__ void tma_load_2d_pair_multicast(const CUtensorMap* map, uint32_t bar_cluster, void* dst, int x,
+                                                           int y, uint16_t mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
+        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "h"(mask)
+        : "memory");
+}
+
+// mbar_wait whose tries may suspend the thread for up to 20 us each: the
+// epilogue warps wait for a whole main loop, and polling costs power that the
+// tensor cores could use.
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            record_error(err, MOE_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// 32 accumulator columns of this thread's row, as floats.
+__device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    tmem_ld_32x32(taddr, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+
 // ---- fused epilogues: eight consecutive columns of one row ----
 // n % 8 == 0 for every width, so an octet is inside or outside as a whole and
 // every access is one aligned 16-byte word.
@@ -71,8 +115,8 @@ __device__ __forceinline__ void gated_octet(const DenseArgs& a, long long row, i
     if (a.out2) *octet(a.out2, row, a.N, col) = pack_bf16x8(u);
 }
 
-// y = residual + act(acc + bias) in fp32, rounded once.
-__device__ __forceinline__ void linear_octet(const DenseArgs& a, long long row, int col, float (&z)[8]) {
+// y = residual + act(acc + bias) in fp32, rounded once; `res` are the residual's eight values.
+__device__ __forceinline__ void linear_octet(const DenseArgs& a, long long row, int col, float (&z)[8], const uint4& res) {
     if (a.bias) {
         const float4 b0 = __ldg(reinterpret_cast<const float4*>(a.bias + col));
         const float4 b1 = __ldg(reinterpret_cast<const float4*>(a.bias + col) + 1);
@@ -86,11 +130,100 @@ __device__ __forceinline__ void linear_octet(const DenseArgs& a, long long row, 
     }
     if (a.residual) {
         float r[8];
-        unpack_bf16x8(*octet(a.residual, row, a.N, col), r);
+        unpack_bf16x8(res, r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) z[j] += r[j];
     }
     *octet(a.out0, row, a.N, col) = pack_bf16x8(z);
+}
+
+// ---- fused epilogues: 32 rows x 32 columns of a warp ----
+// tcgen05.ld leaves one accumulator row in each thread.  Stored as it lies, a
+// warp's 16-byte store touches 32 rows at once, half a sector each; the kernel
+// that keeps g and u was bound by that (656 us against 573 us without them at
+// 4096 x 4096 x 14336).  So a chunk goes through 2 KB of shared memory per warp
+// and leaves (and a residual enters) as 64-byte pieces of eight rows.  The
+// 16-byte pieces of a row are permuted so that both directions use all banks.
+constexpr int kChunkBytes = 32 * 64;
+
+struct RowChunk {
+    uint8_t* smem;   // this warp's kChunkBytes
+    long long row0;
+    int col0, M, N, lane;
+
+    __device__ __forceinline__ uint4* cell(int r, int p) const {
+        return reinterpret_cast<uint4*>(smem + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
+    }
+    // rows i * 8 + lane / 4, piece lane % 4 of a [M, N] matrix (zeros outside)
+    __device__ __forceinline__ void fetch(const uint16_t* base, uint4 (&v)[4]) const {
+        const int col = col0 + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long r = row0 + i * 8 + (lane >> 2);
+            v[i] = r < M && col < N ? *octet(base, r, N, col) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    // what fetch read, as this thread's row
+    __device__ __forceinline__ void to_row(const uint4 (&v)[4], uint4 (&row)[4]) const {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *cell(i * 8 + (lane >> 2), lane & 3) = v[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = *cell(lane, i);
+    }
+    __device__ __forceinline__ void store(uint16_t* base, const float (&v)[32]) const {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *cell(lane, i) = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                        pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+        __syncwarp();
+        const int col = col0 + (lane & 3) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const long long r = row0 + i * 8 + (lane >> 2);
+            if (r < M && col < N) *octet(base, r, N, col) = *cell(i * 8 + (lane >> 2), lane & 3);
+        }
+    }
+};
+
+__device__ __forceinline__ void gated_chunk(const DenseArgs& a, const RowChunk& c, float (&g)[32], float (&u)[32]) {
+    if (a.out1) c.store(a.out1, g);
+    if (a.out2) c.store(a.out2, u);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] = act_value(a.fn, g[j]) * u[j];
+    c.store(a.out0, g);
+}
+
+__device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk& c, float (&z)[32], const uint4 (&res)[4]) {
+    if (a.bias) {
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+            if (c.col0 + o * 8 >= a.N) break;
+            const float4 b0 = __ldg(reinterpret_cast<const float4*>(a.bias + c.col0 + o * 8));
+            const float4 b1 = __ldg(reinterpret_cast<const float4*>(a.bias + c.col0 + o * 8) + 1);
+            z[8 * o] += b0.x, z[8 * o + 1] += b0.y, z[8 * o + 2] += b0.z, z[8 * o + 3] += b0.w;
+            z[8 * o + 4] += b1.x, z[8 * o + 5] += b1.y, z[8 * o + 6] += b1.z, z[8 * o + 7] += b1.w;
+        }
+    }
+    if (a.out1) c.store(a.out1, z);
+    if (a.fn != FN_NONE) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = act_value(a.fn, z[j]);
+    }
+    if (a.residual) {
+        uint4 row[4];
+        c.to_row(res, row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float r[8];
+            unpack_bf16x8(row[i], r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[8 * i + j] += r[j];
+        }
+    }
+    c.store(a.out0, z);
 }
 
 }  // namespace moe

@@ -1,0 +1,322 @@
+// dense_gemm_pair.cu -- the dense products on CTA pairs (tcgen05 cta_group::2),
+// for products with enough tiles to occupy the GPU.
+//
+// A cluster of two CTAs on two SMs owns a 256 x 256 tile: each CTA loads its
+// own 128 rows of A and its own half of B (for the gated product the even CTA
+// holds the W1 rows and the odd one the W3 rows, so an accumulator row has the
+// gate in columns 0..127 and the up projection in 128..255), and the even CTA
+// issues the MMAs for both.  Two 256-column accumulators fill TMEM: the
+// epilogue of a tile runs under the main loop of the next.
+//
+// Sharing an operand.  With two CTAs to a cluster each SM reads 64 bytes a
+// clock from L2 (A and B halves of 16 KB per 512-clock k-block), and that is
+// what holds the main loop back: a prefetch of later k-blocks into L2, which
+// only adds requests, made it 8 to 14 % slower.  With four (CL = 4), two pairs
+// take m-tiles one above the other and the same columns: each CTA loads half of
+// its B half and multicasts it to the CTA of the other pair that needs the same,
+// 48 bytes a clock.  A stage is then free when both pairs' MMAs have read it
+// (two commits on `empty`).  36 clusters of four hold 144 of the 152 SMs.
+//
+// Order of tiles: bands of 8 m-tiles, inside a band n by n, m innermost, so
+// that the pairs working at one time share weight tiles and token rows in L2.
+//
+// Barriers as in grouped_gemm_2sm.cuh: full (even CTA, both CTAs' bytes),
+// empty and tfull (multicast commits), tempty (even CTA, the 16 epilogue warps
+// of both CTAs).  Every wait is bounded.
+#include <algorithm>
+#include <atomic>
+
+#include "dense_gemm.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kOperand = kBM * kRowBytes;        // 16 KB: this CTA's half of an operand
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kBand = 8;
+constexpr int kQuarter = kOperand / 2;           // what a CTA of a cluster of four loads of its B half
+constexpr size_t kPairSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kEpiWarps * kChunkBytes + (2 * kStages + 5) * 8 + 16;
+
+// Row tiles of a cluster's tile: one pair's 256 rows, or two pairs' 512.
+template <int CL>
+constexpr int kTileRows = kPairTile * CL / 2;
+
+// Tile t of the list, as its first row and column; mats products follow one another.
+struct TilePlace {
+    int mat, m0, n0;
+};
+
+template <int CL>
+__device__ __forceinline__ TilePlace place_tile(int t, int mt, int nt, int n_tile) {
+    constexpr int B = kBand * kPairTile / kTileRows<CL>;
+    TilePlace w;
+    w.mat = t / (mt * nt);
+    t -= w.mat * mt * nt;
+    const int band = t / (B * nt), in = t - band * B * nt;
+    const int rows = min(B, mt - band * B);
+    const int n = in / rows;
+    w.m0 = (band * B + in - n * rows) * kTileRows<CL>;
+    w.n0 = n * n_tile;
+    return w;
+}
+
+template <int KIND, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads, 1)
+dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+                  const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                  const DenseArgs a) {
+    using L = DenseLayout<KIND>;
+    constexpr int S = kStages;
+    constexpr int N_TILE = L::GATED ? kPairTile / 2 : kPairTile;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align1024(smem_raw);
+    uint8_t* sA = smem;
+    uint8_t* sB = smem + S * kOperand;
+    uint64_t* full = reinterpret_cast<uint64_t*>(sB + S * kOperand + kEpiWarps * kChunkBytes);
+    uint64_t* empty = full + S;
+    uint64_t* tfull = empty + S;   // [2]
+    uint64_t* tempty = tfull + 2;  // [2]
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t crank = cluster_ctarank();  // in the cluster
+    const uint32_t rank = crank & 1u, lead = crank & ~1u;  // in the pair; the pair's even CTA issues its MMAs
+    const bool leader = rank == 0;
+    const uint16_t both = static_cast<uint16_t>(0x3u << lead), all = static_cast<uint16_t>((1u << CL) - 1u);
+    uint32_t* err = a.err;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], CL / 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 2 * kPairTile);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before any remote arrive
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int kbs = (a.K + kBK - 1) / kBK;
+    const int total_kb = kbs * a.segs;
+    const int mt = (a.M + kTileRows<CL> - 1) / kTileRows<CL>, nt = (a.N + N_TILE - 1) / N_TILE;
+    const int tiles = mt * nt * a.mats, first = blockIdx.x / CL, step = gridDim.x / CL;
+    const uint32_t full_lead = mapa_shared(smem_u32(full), lead);
+    const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), lead);
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool withhold = a.dbg && (*a.dbg & MOE_DBG_WITHHOLD_FIRST_LOAD) && blockIdx.x == 0;
+            uint32_t pending = 0, pend_parity = 0;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += step) {
+                const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
+                const int arow = w.m0 + static_cast<int>(crank) * kBM;
+                const int bcol = w.n0 + (L::GATED ? 0 : static_cast<int>(rank) * (kPairTile / 2));
+                for (int kb = 0; kb < total_kb; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
+                    if (withhold) {
+                        withhold = false;  // test hook: this stage never fills
+                    } else {
+                        const int seg = kb >= kbs ? 1 : 0, k0 = (kb - seg * kbs) * kBK;
+                        const uint32_t bar = full_lead + 8u * stage;
+                        uint8_t* dA = sA + stage * kOperand;
+                        uint8_t* dB = sB + stage * kOperand;
+                        if (leader) {
+                            mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+                            pending |= 1u << stage;
+                            pend_parity = (pend_parity & ~(1u << stage)) | (phase << stage);
+                        }
+                        const CUtensorMap* mA = (seg | w.mat) ? &tmA1 : &tmA0;
+                        if constexpr (L::A_MN) {
+                            tma_load_2d_pair(mA, bar, dA, arow, k0);
+                            tma_load_2d_pair(mA, bar, dA + kMnBlockBytes, arow + 64, k0);
+                        } else {
+                            tma_load_2d_pair(mA, bar, dA, k0, arow);
+                        }
+                        const CUtensorMap* mB = L::GATED ? (rank ? &tmB1 : &tmB0) : (L::B_MN && seg ? &tmB1 : &tmB0);
+                        if constexpr (CL == 4) {  // half of the B half, to both CTAs of this parity
+                            const int part = static_cast<int>(crank >> 1);
+                            const uint16_t mask = static_cast<uint16_t>(0x5u << rank);
+                            const int b64 = bcol + part * 64;
+                            tma_load_2d_pair_multicast(mB, bar, dB + part * kQuarter, L::B_MN ? b64 : k0,
+                                                       L::B_MN ? k0 : b64, mask);
+                        } else if constexpr (L::B_MN) {
+                            tma_load_2d_pair(mB, bar, dB, bcol, k0);
+                            tma_load_2d_pair(mB, bar, dB + kMnBlockBytes, bcol + 64, k0);
+                        } else {
+                            tma_load_2d_pair(mB, bar, dB, k0, bcol);
+                        }
+                    }
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                }
+            }
+            for (int s = 0; s < S; ++s)
+                if (pending & (1u << s)) drain_wait(&full[s], (pend_parity >> s) & 1u, err);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            if (leader) {
+                constexpr uint32_t idesc = dense_idesc<KIND>(kPairTile, kPairTile);
+                int stage = 0, acc = 0;
+                uint32_t phase = 0, acc_phase = 0;
+                bool ok = true;
+                for (int tile = first; ok && tile < tiles; tile += step) {
+                    if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, err)) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kPairTile);
+                    for (int kb = 0; kb < total_kb; ++kb) {
+                        if (!mbar_wait(&full[stage], phase, abort_flag, err)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint64_t ad = operand_desc<L::A_MN>(smem_u32(sA + stage * kOperand));
+                        const uint64_t bd = operand_desc<L::B_MN>(smem_u32(sB + stage * kOperand));
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k)
+                            umma_bf16_pair(d, ad + k * kDescStep<L::A_MN>, bd + k * kDescStep<L::B_MN>, idesc,
+                                           (kb | k) != 0 ? 1u : 0u);
+                        umma_commit_pair_multicast(&empty[stage], all);
+                        if (++stage == S) { stage = 0; phase ^= 1u; }
+                    }
+                    if (!ok) break;
+                    umma_commit_pair_multicast(&tfull[acc], both);
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
+                umma_commit_pair_multicast(drain, both);
+            }
+            drain_wait(drain, 0, err);  // the pair MMAs wrote this CTA's TMEM too
+        }
+    } else {
+        // epilogue warp (q, half): TMEM lanes 32 q .., accumulator columns [0, 128) or [128, 256);
+        // gated: 64 gate columns and the 64 up columns that belong to them
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int col0 = L::GATED ? half * 64 : half * 128;
+        uint8_t* stage_smem = smem + S * kStageBytes + (warp - 2) * kChunkBytes;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int tile = first; tile < tiles; tile += step) {
+            const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
+            const bool ok = lane != 0 || mbar_wait_long(&tfull[acc], acc_phase, abort_flag, err);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kPairTile);
+            const long long row0 = static_cast<long long>(w.m0) + crank * kBM + q * 32;
+#pragma unroll 1
+            for (int c = 0; c < (L::GATED ? 2 : 4); ++c) {
+                float v[32];
+                const RowChunk chunk{stage_smem, row0, w.n0 + col0 + c * 32, a.M, a.N, lane};
+                if constexpr (KIND == DENSE_LINEAR) {
+                    uint4 res[4];
+                    if (a.residual) chunk.fetch(a.residual, res);
+                    tmem_row(t + col0 + c * 32, v);
+                    linear_chunk(a, chunk, v, res);
+                } else if constexpr (L::GATED) {
+                    float u[32];
+                    tmem_row(t + col0 + c * 32, v);
+                    tmem_row(t + 128 + col0 + c * 32, u);
+                    gated_chunk(a, chunk, v, u);
+                } else {
+                    tmem_row(t + col0 + c * 32, v);
+                    chunk.store(w.mat ? a.out1 : a.out0, v);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * acc);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+    }
+
+    __syncwarp();
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // no CTA leaves while another of the cluster may still signal it
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 2 * kPairTile);
+    }
+}
+
+template <int KIND, int CL>
+cudaError_t pair_prepare(int* clusters) {
+    static std::atomic<unsigned long long> done{0};
+    static int limit[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(dense_pair_kernel<KIND, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kPairSmem));
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(CL);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kPairSmem;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<KIND, CL>, &cfg);
+        if (e != cudaSuccess) return e;
+        limit[dev & 63] = n;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    *clusters = limit[dev & 63];
+    return *clusters > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
+template <int KIND, int CL>
+cudaError_t pair_go(const CUtensorMap* m, const DenseArgs& a, int clusters, cudaStream_t st) {
+    int limit = 0;
+    cudaError_t e = pair_prepare<KIND, CL>(&limit);
+    if (e != cudaSuccess) return e;
+    if (clusters > limit) return cudaErrorInvalidConfiguration;
+    return launch_kernel(dense_pair_kernel<KIND, CL>, dim3(CL * clusters), dim3(kThreads), kPairSmem, st, m[0], m[1], m[2],
+                         m[3], a);
+}
+
+}  // namespace
+
+cudaError_t dense_pair_limit(DenseKind kind, int cluster, int* clusters) {
+    const bool two = cluster == 2;
+    switch (kind) {
+        case DENSE_GATED: return two ? pair_prepare<DENSE_GATED, 2>(clusters) : pair_prepare<DENSE_GATED, 4>(clusters);
+        case DENSE_LINEAR: return two ? pair_prepare<DENSE_LINEAR, 2>(clusters) : pair_prepare<DENSE_LINEAR, 4>(clusters);
+        case DENSE_DGRAD: return two ? pair_prepare<DENSE_DGRAD, 2>(clusters) : pair_prepare<DENSE_DGRAD, 4>(clusters);
+        default: return two ? pair_prepare<DENSE_WGRAD, 2>(clusters) : pair_prepare<DENSE_WGRAD, 4>(clusters);
+    }
+}
+
+cudaError_t launch_dense_pair(DenseKind kind, const CUtensorMap* m, const DenseArgs& a, int cluster, int clusters,
+                              cudaStream_t st) {
+    const bool two = cluster == 2;
+    switch (kind) {
+        case DENSE_GATED: return two ? pair_go<DENSE_GATED, 2>(m, a, clusters, st) : pair_go<DENSE_GATED, 4>(m, a, clusters, st);
+        case DENSE_LINEAR: return two ? pair_go<DENSE_LINEAR, 2>(m, a, clusters, st) : pair_go<DENSE_LINEAR, 4>(m, a, clusters, st);
+        case DENSE_DGRAD: return two ? pair_go<DENSE_DGRAD, 2>(m, a, clusters, st) : pair_go<DENSE_DGRAD, 4>(m, a, clusters, st);
+        default: return two ? pair_go<DENSE_WGRAD, 2>(m, a, clusters, st) : pair_go<DENSE_WGRAD, 4>(m, a, clusters, st);
+    }
+}
+
+}  // namespace moe

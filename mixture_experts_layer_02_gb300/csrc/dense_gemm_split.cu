@@ -12,8 +12,14 @@
 //
 // Warp roles: 0 TMA producer, 1 TMEM allocator and MMA issuer, 4..7 park the
 // accumulator (warp q reads TMEM lanes 32 q ..), all eight warps the join and
-// epilogue.  Three 32 KB stages, so that two CTAs fit an SM: a short k-range
-// then overlaps its neighbour's prologue and epilogue.
+// epilogue.
+//
+// These products are latency-bound.  Time stamps at 256 x 4096 x 4096 (S = 2,
+// 32 k-blocks a CTA) showed a TMA round trip of 1.1 us, so three 32 KB stages
+// moved one k-block each 0.37 us; six stages (one CTA an SM) halve that.  The
+// join took 4 us with one row octet after another; now each thread issues all
+// of its sixteen distributed-shared-memory loads at once, and the residual is
+// fetched before the cluster barrier.
 //
 // Every wait is bounded (mbar_wait); whatever a role sees, every thread reaches
 // both cluster barriers, so no CTA waits for one that left.
@@ -27,7 +33,7 @@ namespace moe {
 namespace {
 
 constexpr int kSplitBN = 128;
-constexpr int kSplitStages = 3;
+constexpr int kSplitStages = 6;
 constexpr int kSplitThreads = 256;
 constexpr int kOperandBytes = kBM * kRowBytes;  // 16 KB: 128 rows x 64 K, or two MN-major boxes
 constexpr int kSplitStageBytes = 2 * kOperandBytes;
@@ -44,25 +50,7 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ uint32_t cluster_nctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-
-// Eight consecutive floats of a parked accumulator, summed over the cluster in rank order.
-__device__ __forceinline__ void joined_octet(uint32_t offset, uint32_t splits, float (&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    for (uint32_t s = 0; s < splits; ++s) {
-        const uint32_t p = mapa_shared(offset, s);
-        const float4 a = ld_cluster_v4(p), b = ld_cluster_v4(p + 16);
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-    }
-}
-
-template <int KIND>
+template <int KIND, int SPLITS>
 __global__ void __launch_bounds__(kSplitThreads)
 dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                    const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
@@ -80,7 +68,12 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank(), splits = cluster_nctarank();
+    const uint32_t rank = SPLITS > 1 ? cluster_ctarank() : 0u;
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmA0);
+        tma_prefetch_desc(&tmB0);
+        if (L::GATED) tma_prefetch_desc(&tmB1);
+    }
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -102,14 +95,14 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
 
     // tile: m fastest, so that concurrent CTAs share the weight columns
     const int mt = (a.M + kBM - 1) / kBM, nt = (a.N + N_TILE - 1) / N_TILE;
-    int tile = blockIdx.x / splits;
+    int tile = blockIdx.x / SPLITS;
     const int mat = tile / (mt * nt);
     tile -= mat * mt * nt;
     const int m0 = (tile % mt) * kBM, n0 = (tile / mt) * N_TILE;
     const int kbs = (a.K + kBK - 1) / kBK;  // k-blocks of one segment
     const int total = kbs * a.segs;
-    const int k_lo = static_cast<int>(static_cast<long long>(total) * rank / splits);
-    const int k_hi = static_cast<int>(static_cast<long long>(total) * (rank + 1) / splits);
+    const int k_lo = static_cast<int>(static_cast<long long>(total) * rank / SPLITS);
+    const int k_hi = static_cast<int>(static_cast<long long>(total) * (rank + 1) / SPLITS);
     pdl_wait();
 
     if (warp == 0) {
@@ -191,7 +184,25 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
             }
         }
     }
+    // This CTA's share of the tile's row octets: items of thread t are t, t + 256, ...
+    constexpr int OCTETS = N_TILE / 8;
+    constexpr int ITEMS = kBM * OCTETS / SPLITS;
+    constexpr int PER = (ITEMS + kSplitThreads - 1) / kSplitThreads;
+    int rows[PER], cols[PER];
+    uint4 res[PER];
     __syncwarp();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int it = i * kSplitThreads + static_cast<int>(threadIdx.x);
+        const int item = ITEMS * static_cast<int>(rank) + it, r = item / OCTETS, c = (item - r * OCTETS) * 8;
+        const bool in = it < ITEMS && m0 + r < a.M && n0 + c < a.N;
+        rows[i] = in ? r : -1;
+        cols[i] = c;
+        if constexpr (KIND == DENSE_LINEAR) {
+            res[i] = make_uint4(0, 0, 0, 0);
+            if (in && a.residual) res[i] = *octet(a.residual, m0 + r, a.N, n0 + c);
+        }
+    }
     pdl_trigger();
     tc_fence_before();
     __syncthreads();
@@ -199,77 +210,139 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, kSplitBN);
     }
-    cluster_sync_all();  // every CTA's accumulator is parked
+    if constexpr (SPLITS > 1) cluster_sync_all();  // every CTA's accumulator is parked
 
-    constexpr int OCTETS = N_TILE / 8;
-    constexpr int ITEMS = kBM * OCTETS;
-    const int it_lo = ITEMS * static_cast<int>(rank) / static_cast<int>(splits);
-    const int it_hi = ITEMS * static_cast<int>(rank + 1) / static_cast<int>(splits);
     const uint32_t park0 = smem_u32(park);
-    for (int it = it_lo + threadIdx.x; it < it_hi; it += kSplitThreads) {
-        const int r = it / OCTETS, c = (it - r * OCTETS) * 8;
-        if (m0 + r >= a.M || n0 + c >= a.N) continue;
-        const uint32_t at = park0 + static_cast<uint32_t>(r * kParkLd + c) * 4u;
-        float v[8];
-        joined_octet(at, splits, v);
-        if constexpr (L::GATED) {
-            float u[8];
-            joined_octet(at + 4u * N_TILE, splits, u);
-            gated_octet(a, m0 + r, n0 + c, v, u);
-        } else if constexpr (KIND == DENSE_LINEAR) {
-            linear_octet(a, m0 + r, n0 + c, v);
-        } else {
-            *octet(mat ? a.out1 : a.out0, m0 + r, a.N, n0 + c) = pack_bf16x8(v);
+    constexpr int HALVES = L::GATED ? 2 : 1;
+    float4 parts[PER][HALVES][SPLITS][2];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+            for (int s = 0; s < SPLITS; ++s) {
+                const uint32_t at = park0 + static_cast<uint32_t>(max(rows[i], 0) * kParkLd + h * N_TILE + cols[i]) * 4u;
+                const uint32_t p = SPLITS > 1 ? mapa_shared(at, s) : at;
+                parts[i][h][s][0] = ld_cluster_v4(p);
+                parts[i][h][s][1] = ld_cluster_v4(p + 16);
+            }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        float v[HALVES][8];
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[h][j] = 0.0f;
+#pragma unroll
+            for (int s = 0; s < SPLITS; ++s) {  // in rank order
+                const float4 x = parts[i][h][s][0], y = parts[i][h][s][1];
+                v[h][0] += x.x, v[h][1] += x.y, v[h][2] += x.z, v[h][3] += x.w;
+                v[h][4] += y.x, v[h][5] += y.y, v[h][6] += y.z, v[h][7] += y.w;
+            }
         }
+        if (rows[i] < 0) continue;
+        const long long row = static_cast<long long>(m0) + rows[i];
+        const int col = n0 + cols[i];
+        if constexpr (L::GATED) gated_octet(a, row, col, v[0], v[HALVES - 1]);
+        else if constexpr (KIND == DENSE_LINEAR) linear_octet(a, row, col, v[0], res[i]);
+        else *octet(mat ? a.out1 : a.out0, row, a.N, col) = pack_bf16x8(v[0]);
     }
-    cluster_sync_all();  // no CTA leaves while another reads its shared memory
+    if constexpr (SPLITS > 1) cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
-template <int KIND>
-cudaError_t split_prepare() {
-    static std::atomic<unsigned long long> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(dense_split_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSplitSmem));
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
-    return e;
-}
-
-template <int KIND>
-cudaError_t split_go(const CUtensorMap* m, const DenseArgs& a, int splits, cudaStream_t st) {
-    cudaError_t e = split_prepare<KIND>();
-    if (e != cudaSuccess) return e;
-    constexpr int n_tile = DenseLayout<KIND>::GATED ? kSplitBN / 2 : kSplitBN;
-    const long long tiles = static_cast<long long>((a.M + kBM - 1) / kBM) * ((a.N + n_tile - 1) / n_tile) * a.mats;
-    if (tiles * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+template <int KIND, int SPLITS>
+cudaLaunchConfig_t split_config(cudaLaunchAttribute (&attr)[2], cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+    cfg.gridDim = dim3(SPLITS);
     cfg.blockDim = dim3(kSplitThreads);
     cfg.dynamicSmemBytes = kSplitSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.x = SPLITS;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, dense_split_kernel<KIND>, m[0], m[1], m[2], m[3], a);
+    return cfg;
+}
+
+// Clusters the current device holds at once (kept per device).
+template <int KIND, int SPLITS>
+cudaError_t split_prepare(int* clusters) {
+    static std::atomic<unsigned long long> done{0};
+    static int limit[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(dense_split_kernel<KIND, SPLITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSplitSmem));
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = split_config<KIND, SPLITS>(attr, nullptr);
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, dense_split_kernel<KIND, SPLITS>, &cfg);
+        if (e != cudaSuccess) return e;
+        limit[dev & 63] = n;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    *clusters = limit[dev & 63];
+    return *clusters > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
+template <int KIND, int SPLITS>
+cudaError_t split_go(const CUtensorMap* m, const DenseArgs& a, cudaStream_t st) {
+    int limit = 0;
+    cudaError_t e = split_prepare<KIND, SPLITS>(&limit);
+    if (e != cudaSuccess) return e;
+    constexpr int n_tile = DenseLayout<KIND>::GATED ? kSplitBN / 2 : kSplitBN;
+    const long long tiles = static_cast<long long>((a.M + kBM - 1) / kBM) * ((a.N + n_tile - 1) / n_tile) * a.mats;
+    if (tiles * SPLITS > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = split_config<KIND, SPLITS>(attr, st);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * SPLITS));
+    return cudaLaunchKernelEx(&cfg, dense_split_kernel<KIND, SPLITS>, m[0], m[1], m[2], m[3], a);
+}
+
+template <int KIND>
+cudaError_t split_pick(const CUtensorMap* m, const DenseArgs& a, int splits, cudaStream_t st) {
+    switch (splits) {
+        case 1: return split_go<KIND, 1>(m, a, st);
+        case 2: return split_go<KIND, 2>(m, a, st);
+        case 4: return split_go<KIND, 4>(m, a, st);
+        default: return split_go<KIND, 8>(m, a, st);
+    }
+}
+
+template <int KIND>
+cudaError_t split_limit(int splits, int* clusters) {
+    switch (splits) {
+        case 1: return split_prepare<KIND, 1>(clusters);
+        case 2: return split_prepare<KIND, 2>(clusters);
+        case 4: return split_prepare<KIND, 4>(clusters);
+        default: return split_prepare<KIND, 8>(clusters);
+    }
 }
 
 }  // namespace
 
+cudaError_t dense_split_limit(DenseKind kind, int splits, int* clusters) {
+    switch (kind) {
+        case DENSE_GATED: return split_limit<DENSE_GATED>(splits, clusters);
+        case DENSE_LINEAR: return split_limit<DENSE_LINEAR>(splits, clusters);
+        case DENSE_DGRAD: return split_limit<DENSE_DGRAD>(splits, clusters);
+        default: return split_limit<DENSE_WGRAD>(splits, clusters);
+    }
+}
+
 cudaError_t launch_dense_split(DenseKind kind, const CUtensorMap* m, const DenseArgs& a, int splits, cudaStream_t st) {
     switch (kind) {
-        case DENSE_GATED: return split_go<DENSE_GATED>(m, a, splits, st);
-        case DENSE_LINEAR: return split_go<DENSE_LINEAR>(m, a, splits, st);
-        case DENSE_DGRAD: return split_go<DENSE_DGRAD>(m, a, splits, st);
-        default: return split_go<DENSE_WGRAD>(m, a, splits, st);
+        case DENSE_GATED: return split_pick<DENSE_GATED>(m, a, splits, st);
+        case DENSE_LINEAR: return split_pick<DENSE_LINEAR>(m, a, splits, st);
+        case DENSE_DGRAD: return split_pick<DENSE_DGRAD>(m, a, splits, st);
+        default: return split_pick<DENSE_WGRAD>(m, a, splits, st);
     }
 }
 

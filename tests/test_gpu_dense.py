@@ -137,13 +137,18 @@ def test_norm_backward(moe, n, d, down):
 # ------------------------------------------------------------------ products
 #: rows, in, out: one row, tails of every dimension, widths below a tile, several tiles
 SHAPES = [(1, 8, 8), (1, 2048, 768), (3, 72, 200), (8, 1000, 264), (9, 1024, 40), (17, 264, 1032), (33, 520, 72), (64, 512, 512),
-          (127, 64, 136), (128, 1024, 256), (129, 2056, 328), (300, 776, 520), (513, 136, 1288)]
+          (127, 64, 136), (128, 1024, 256), (129, 2056, 328), (300, 776, 520), (513, 136, 1288), (700, 4104, 400)]
 
 
-@pytest.fixture(params=["", "1", "2", "8"])
+#: the plan's choice; one-CTA tiles with 1, 2 or 8 CTAs over K; CTA pairs; two pairs that share an operand
+KERNELS = {"plan": {}, "split1": dict(KERNEL="1", SPLITS="1"), "split2": dict(KERNEL="1", SPLITS="2"),
+           "split8": dict(KERNEL="1", SPLITS="8"), "pair": dict(KERNEL="2", CLUSTER="2"), "pairs4": dict(KERNEL="2", CLUSTER="4")}
+
+
+@pytest.fixture(params=list(KERNELS))
 def splits(request, monkeypatch):
-    if request.param:
-        monkeypatch.setenv("MOE_DENSE_SPLITS", request.param)
+    for k, v in KERNELS[request.param].items():
+        monkeypatch.setenv("MOE_DENSE_" + k, v)
     return request.param
 
 
@@ -380,8 +385,27 @@ def test_gradients_against_differences(moe, fn):
         assert abs((grad.double() * v).sum() - want) <= 8 * R.H * grad.double().norm() * v.norm() / grad.numel() ** 0.5 * 4
 
 
-def test_withheld_load_times_out_and_recovers(moe):
+@pytest.mark.parametrize("n,d,f", [(5000, 512, 2600), (2050, 1544, 4400), (257, 2048, 8200)])
+def test_more_tiles_than_pairs(moe, n, d, f):
+    """Several rounds of tiles, ragged in every dimension."""
+    x, w = randn(n, d, seed=1), randn(f, d, seed=2, scale=d ** -0.5)
+    res, dy = randn(n, f, seed=3), randn(n, f, seed=4, scale=0.1)
+    ws = moe.workspace("linear_backward", N=n, D=d, Dff=f)
+    y, _ = moe.moe_linear(x, w, residual=res, ws=ws)
+    (ry, ey), _ = R.linear(x, w, None, res, "none")
+    assert_within(y, ry, ey, "y")
+    got = moe.moe_linear_backward(dy, x, w, ws=ws)
+    for t, (ref, bound), name in zip(got, R.linear_backward(dy, x, w, None, "none"), ("dx", "dw")):
+        assert_within(t, ref, bound, name)
+    again = moe.moe_linear_backward(dy, x, w, ws=ws)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    assert moe.read_device_error(ws) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("kernel", ["1", "2"])
+def test_withheld_load_times_out_and_recovers(moe, kernel, monkeypatch):
     """A load that never lands: the call ends, says so, and the next one is right."""
+    monkeypatch.setenv("MOE_DENSE_KERNEL", kernel)
     x, w = randn(70, 264, seed=1), randn(136, 264, seed=2, scale=0.1)
     ws = moe.workspace("linear", N=70, D=264, Dff=136)
     want = moe.moe_linear(x, w, ws=ws)[0].clone()
