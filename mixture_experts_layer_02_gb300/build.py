@@ -26,7 +26,7 @@ SOURCES = ["grouped_gemm.cu", "grouped_gemm_e4m3.cu", "grouped_gemm_2sm.cu", "gr
            "grouped_gemm_swap.cu", "grouped_gemm_swap_e4m3.cu", "grouped_gemm_gather.cu",
            "grouped_gemm_gather_e4m3.cu", "grouped_gemm_gather_small.cu", "ffn_fused_decode.cu", "layer_decode.cu", "quant.cu", "route_reduce.cu",
            "permute.cu", "combine.cu", "rmsnorm.cu", "dense_grad.cu", "dense_gemm_split.cu",
-           "dense_gemm_pair.cu", "dense_api.cu",
+           "dense_gemm_pair.cu", "dense_gemv.cu", "dense_api.cu",
            "moe_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -97,6 +97,10 @@ cudaError_t dense_split_limit(DenseKind kind, int splits, int* clusters);  // cl
 cudaError_t launch_dense_split(DenseKind kind, const CUtensorMap* maps, const DenseArgs& a, int splits,
                                cudaStream_t st);
 
+// A few rows (DENSE_GATED, DENSE_LINEAR; M <= kGemvMaxRows): one pass over the weights.
+constexpr int kGemvMaxRows = 16;
+cudaError_t launch_dense_gemv(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st);
+
 // CTA pairs on 256 x 256 tiles, persistent: clusters of one pair (cluster = 2)
 // or of two pairs one above the other (4).
 constexpr int kPairTile = 256;

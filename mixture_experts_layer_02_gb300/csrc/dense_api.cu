@@ -114,7 +114,7 @@ int env_int(const char* name, int dflt) {
     return f ? atoi(f) : dflt;
 }
 
-// MOE_DENSE_KERNEL = 1 (split) or 2 (pairs), MOE_DENSE_SPLITS and
+// MOE_DENSE_KERNEL = 1 (split), 2 (pairs) or 3 (streamed weights, where M allows), MOE_DENSE_SPLITS and
 // MOE_DENSE_CLUSTER = 2 or 4 force a choice, for tuning and test coverage.
 moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p) {
     const int n1 = kind == DENSE_GATED ? 64 : 128, n2 = kind == DENSE_GATED ? 128 : 256;
@@ -152,6 +152,9 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
 
 // One product: tensor maps, the choice of kernel, the launch.
 moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
+    const int kernel = env_int("MOE_DENSE_KERNEL", 0);
+    if ((kind == DENSE_GATED || kind == DENSE_LINEAR) && a.M <= kGemvMaxRows && (kernel == 0 || kernel == 3))
+        return launched(launch_dense_gemv(kind, o, a, st), "dense product launch");
     const bool a_mn = kind == DENSE_WGRAD, b_mn = kind == DENSE_DGRAD || kind == DENSE_WGRAD;
     const int kblocks = (a.K + kBK - 1) / kBK * a.segs;
     Plan p;

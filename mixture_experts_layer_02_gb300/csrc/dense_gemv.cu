@@ -1,0 +1,156 @@
+// dense_gemv.cu -- the gated and linear products of a few tokens: a stream of
+// weight rows.
+//
+// At up to 16 rows of x the weights are read once and everything else is small,
+// so the time is the weights' bytes over the HBM rate plus a fixed latency.  A
+// 128-row tensor-core tile spends that latency on shared memory, barriers and
+// clusters (20.8 us at one token, 7168 x 2 x 2048, where the bytes take 8.7).
+// Here the weights go from global memory straight into registers as the 16-row
+// operand of mma.sync.m16n8k16 and the tokens are its 8 columns:
+//
+//   - a block owns 16 weight rows (gated: 8 rows of W1 and the same 8 of W3, so
+//     a thread holds the gate and the up sum of one output in one fragment) and
+//     its 8 warps take 64-wide steps of K in turn;
+//   - lane (g, t) = (lane / 4, lane % 4) loads the 16-byte pieces at columns
+//     32 j + 8 t of rows g and g + 8: every load instruction covers whole
+//     sectors, and any K that is a multiple of 8 will do.  Which K element sits
+//     in which fragment slot does not matter as long as x is loaded the same
+//     way, so no element is ever moved between lanes;
+//   - the loads of four steps are issued before the first is used: two blocks
+//     an SM keep about 128 KB in flight.
+//
+// The 8 warps' sums are added in warp order through shared memory and run
+// through the epilogue, so results do not change from run to run.
+#include <algorithm>
+
+#include "dense_gemm.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kGemvWarps = 8;
+constexpr int kGemvRows = 16;
+constexpr int kGemvBatch = 4;  // steps of 64 K loaded ahead
+
+__device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Read once: not kept in L1.
+__device__ __forceinline__ uint4 ld_once(const uint16_t* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// NT: groups of eight tokens.
+template <bool GATED, int NT>
+__global__ void __launch_bounds__(kGemvWarps * 32, 2)
+dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w, const uint16_t* __restrict__ w3,
+                  const DenseArgs a) {
+    __shared__ float sums[kGemvWarps][NT * 8][kGemvRows + 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int K = a.K;
+    // rows past the last are read as the last one and not stored
+    const int n0 = blockIdx.x * (GATED ? 8 : kGemvRows);
+    const uint16_t* lo = w + static_cast<long long>(min(n0 + g, a.N - 1)) * K;
+    const uint16_t* hi = GATED ? w3 + static_cast<long long>(min(n0 + g, a.N - 1)) * K
+                               : w + static_cast<long long>(min(n0 + g + 8, a.N - 1)) * K;
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    pdl_wait();
+    pdl_trigger();
+
+    const int steps = (K + 63) >> 6;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int s0 = warp; s0 < steps; s0 += kGemvWarps * kGemvBatch) {
+        uint4 wl[kGemvBatch][2], wh[kGemvBatch][2], xv[kGemvBatch][NT][2];
+#pragma unroll
+        for (int b = 0; b < kGemvBatch; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int k = (s0 + b * kGemvWarps) * 64 + j * 32 + t * 8;
+                const bool in = k < K;
+                wl[b][j] = in ? ld_once(lo + k) : zero;
+                wh[b][j] = in ? ld_once(hi + k) : zero;
+            }
+#pragma unroll
+        for (int b = 0; b < kGemvBatch; ++b)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int k = (s0 + b * kGemvWarps) * 64 + j * 32 + t * 8, tok = i * 8 + g;
+                    xv[b][i][j] = k < K && tok < a.M
+                                      ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<long long>(tok) * K + k))
+                                      : zero;
+                }
+#pragma unroll
+        for (int b = 0; b < kGemvBatch; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    mma_16x8x16(acc[i], wl[b][j].x, wh[b][j].x, wl[b][j].y, wh[b][j].y, xv[b][i][j].x, xv[b][i][j].y);
+                    mma_16x8x16(acc[i], wl[b][j].z, wh[b][j].z, wl[b][j].w, wh[b][j].w, xv[b][i][j].z, xv[b][i][j].w);
+                }
+    }
+    // acc[i]: rows g (0, 1) and g + 8 (2, 3), tokens 8 i + 2 t and the next
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[warp][i * 8 + 2 * t + (j & 1)][g + (j >> 1) * 8] = acc[i][j];
+    __syncthreads();
+
+    constexpr int COLS = GATED ? 8 : kGemvRows;
+    for (int it = threadIdx.x; it < NT * 8 * COLS; it += kGemvWarps * 32) {
+        const int tok = it / COLS, c = it - tok * COLS, col = n0 + c;
+        if (tok >= a.M || col >= a.N) continue;
+        const long long at = static_cast<long long>(tok) * a.N + col;
+        float z = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kGemvWarps; ++v) {
+            z += sums[v][tok][c];
+            if (GATED) u += sums[v][tok][c + 8];
+        }
+        auto put = [&](uint16_t* p, float f) { p[at] = static_cast<uint16_t>(pack_bf16x2(f, 0.0f)); };
+        if constexpr (GATED) {
+            if (a.out1) put(a.out1, z);
+            if (a.out2) put(a.out2, u);
+            put(a.out0, act_value(a.fn, z) * u);
+        } else {
+            if (a.bias) z += a.bias[col];
+            if (a.out1) put(a.out1, z);
+            z = act_value(a.fn, z);
+            if (a.residual) z += __uint_as_float(static_cast<uint32_t>(a.residual[at]) << 16);
+            put(a.out0, z);
+        }
+    }
+}
+
+template <bool GATED, int NT>
+cudaError_t gemv_go(const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
+    const int rows = GATED ? 8 : kGemvRows;
+    return launch_kernel(dense_gemv_kernel<GATED, NT>, dim3((a.N + rows - 1) / rows), dim3(kGemvWarps * 32), 0, st, o.a0,
+                         o.b0, o.b1, a);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_gemv(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
+    if (kind == DENSE_GATED) return a.M <= 8 ? gemv_go<true, 1>(o, a, st) : gemv_go<true, 2>(o, a, st);
+    return a.M <= 8 ? gemv_go<false, 1>(o, a, st) : gemv_go<false, 2>(o, a, st);
+}
+
+}  // namespace moe

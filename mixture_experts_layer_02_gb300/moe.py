@@ -669,46 +669,61 @@ def moe_grouped_ffn_e4m3_gathered(xq, x_scale, perm_src, expert_offsets, w1q, s1
 
 
 # ---------------------------------------------------------------- dense operators (norm, gated and linear products)
-class _on_stream:
-    """Allocations inside belong to the stream the call runs on, so that the
-    allocator does not hand a freed buffer to another stream too early."""
-
-    def __init__(self, stream):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+# Small calls run in a few microseconds on the GPU, so the host side counts:
+# each function tests its arguments in one expression and goes through _explain
+# only to say what is wrong, and the stream handle is read without a Stream
+# object (3 us).
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _scratch(op, N, D, F, device):
+def _stream_of(t, stream):
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
+
+
+def _new(stream, *specs):
+    """Empty tensors (shape, dtype, device), each None where the spec is None,
+    that belong to the stream the call runs on: the allocator then does not hand
+    a freed one to another stream too early."""
+    if stream is None:
+        return [None if s is None else torch.empty(s[0], dtype=s[1], device=s[2]) for s in specs]
+    with torch.cuda.stream(stream):
+        return _new(None, *specs)
+
+
+def _scratch(stream, op, N, D, F, device):
     """A workspace of one call: only its header is zeroed.  Invalid sizes get a
     bare header: the entry point then says what is wrong with them."""
-    ws = torch.empty(max(workspace_size(op, N=N, D=D, Dff=F), 256), dtype=torch.uint8, device=device)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _scratch(None, op, N, D, F, device)
+    ws = torch.empty(max(workspace_size(op, N=N, D=D, Dff=F), 256), dtype=_U8, device=device)
     ws[:256].zero_()
     return ws
+
+
+def _fits(t, dtype, shape):
+    return t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+
+
+def _explain(ws, *specs):
+    """Raise for the first (tensor or None, dtype, shape, name) that does not fit, or a workspace off the GPU."""
+    for t, dtype, shape, name in specs:
+        if t is not None:
+            _need(t, dtype, shape, name)
+    if ws is not None and not ws.is_cuda:
+        raise ValueError("ws: must be a CUDA tensor")
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _check_all(*specs):
-    """(tensor or None, dtype, shape, name) for each argument."""
-    for t, dtype, shape, name in specs:
-        if t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
-            continue
-        _need(t, dtype, shape, name)
-
-
 def _rows(t, name):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected [rows, width], got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected [rows, width], got {tuple(shape)}")
+    return shape
 
 
 def moe_rmsnorm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = False, y=None, yq=None, y_scale=None,
@@ -718,21 +733,27 @@ def moe_rmsnorm(x, weight, residual=None, eps: float = 1e-6, quantize: bool = Fa
     row, as moe_permute_e4m3 takes them) with quantize=True or when passed, s
     (the new residual stream) when a residual is given or residual_out is
     passed; None for the others."""
-    N, D = _rows(x, "x")
-    with _on_stream(stream):
-        y = torch.empty_like(x) if y is None else y
-        if quantize or yq is not None or y_scale is not None:
-            yq = torch.empty((N, D), dtype=torch.uint8, device=x.device) if yq is None else yq
-            y_scale = torch.empty(N, dtype=torch.float32, device=x.device) if y_scale is None else y_scale
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(x)
-    bf16 = torch.bfloat16
-    _check_all((x, bf16, (N, D), "x"), (weight, bf16, (D,), "weight"), (residual, bf16, (N, D), "residual"),
-               (y, bf16, (N, D), "y"), (yq, torch.uint8, (N, D), "yq"), (y_scale, torch.float32, (N,), "y_scale"),
-               (residual_out, bf16, (N, D), "residual_out"))
-    _check("moe_rmsnorm", load().moe_rmsnorm(
-        _addr(x), _addr(residual), _addr(weight), N, D, eps, _addr(y), _addr(yq), _addr(y_scale), _addr(residual_out),
-        _stream(stream)))
+    shape = _rows(x, "x")
+    N, D = shape
+    codes = quantize or yq is not None or y_scale is not None
+    if y is None:
+        y, = _new(stream, (shape, _BF16, x.device))
+    if codes and (yq is None or y_scale is None):
+        q, sc = _new(stream, (shape, _U8, x.device), ((N,), _F32, x.device))
+        yq, y_scale = q if yq is None else yq, sc if y_scale is None else y_scale
+    if residual is not None and residual_out is None:
+        residual_out, = _new(stream, (shape, _BF16, x.device))
+    if not (_fits(x, _BF16, shape) and _fits(weight, _BF16, (D,)) and _fits(y, _BF16, shape)
+            and (residual is None or _fits(residual, _BF16, shape))
+            and (residual_out is None or _fits(residual_out, _BF16, shape))
+            and (not codes or (_fits(yq, _U8, shape) and _fits(y_scale, _F32, (N,))))):
+        _explain(None, (x, _BF16, shape, "x"), (weight, _BF16, (D,), "weight"), (residual, _BF16, shape, "residual"),
+                 (y, _BF16, shape, "y"), (yq, _U8, shape, "yq"), (y_scale, _F32, (N,), "y_scale"),
+                 (residual_out, _BF16, shape, "residual_out"))
+    s = (_lib or load()).moe_rmsnorm(_addr(x), _addr(residual), _addr(weight), N, D, eps, _addr(y), _addr(yq),
+                                     _addr(y_scale), _addr(residual_out), _stream_of(x, stream))
+    if s:
+        _check("moe_rmsnorm", s)
     return y, yq, y_scale, residual_out
 
 
@@ -740,17 +761,22 @@ def moe_rmsnorm_backward(dy, s, weight, dresidual=None, eps: float = 1e-6, dx=No
     """Gradient of moe_rmsnorm from dy and s (its fourth result, or x without a
     residual): (dx, dweight), dx for x and the residual alike, dweight fp32.
     dresidual is the gradient that reached s itself."""
-    N, D = _rows(s, "s")
-    with _on_stream(stream):
-        dx = torch.empty_like(s) if dx is None else dx
-        dweight = torch.empty(D, dtype=torch.float32, device=s.device) if dweight is None else dweight
-        ws = _scratch("rmsnorm_backward", N, D, 0, s.device) if ws is None else ws
-    bf16 = torch.bfloat16
-    _check_all((dy, bf16, (N, D), "dy"), (s, bf16, (N, D), "s"), (weight, bf16, (D,), "weight"),
-               (dresidual, bf16, (N, D), "dresidual"), (dx, bf16, (N, D), "dx"), (dweight, torch.float32, (D,), "dweight"))
-    _check("moe_rmsnorm_backward", load().moe_rmsnorm_backward(
-        _addr(dy), _addr(s), _addr(weight), _addr(dresidual), N, D, eps, _addr(dx), _addr(dweight), _addr(ws), ws.numel(),
-        _stream(stream)))
+    shape = _rows(s, "s")
+    N, D = shape
+    if dx is None:
+        dx, = _new(stream, (shape, _BF16, s.device))
+    if dweight is None:
+        dweight, = _new(stream, ((D,), _F32, s.device))
+    if ws is None:
+        ws = _scratch(stream, "rmsnorm_backward", N, D, 0, s.device)
+    if not (_fits(dy, _BF16, shape) and _fits(s, _BF16, shape) and _fits(weight, _BF16, (D,)) and _fits(dx, _BF16, shape)
+            and _fits(dweight, _F32, (D,)) and ws.is_cuda and (dresidual is None or _fits(dresidual, _BF16, shape))):
+        _explain(ws, (dy, _BF16, shape, "dy"), (s, _BF16, shape, "s"), (weight, _BF16, (D,), "weight"),
+                 (dresidual, _BF16, shape, "dresidual"), (dx, _BF16, shape, "dx"), (dweight, _F32, (D,), "dweight"))
+    st = (_lib or load()).moe_rmsnorm_backward(_addr(dy), _addr(s), _addr(weight), _addr(dresidual), N, D, eps, _addr(dx),
+                                               _addr(dweight), _addr(ws), ws.numel(), _stream_of(s, stream))
+    if st:
+        _check("moe_rmsnorm_backward", st)
     return dx, dweight
 
 
@@ -759,38 +785,47 @@ def moe_gated_linear(x, w1, w3, fn: int = FN_SILU, save: bool = False, h=None, g
     (the two projections, for the backward pass) are None unless save=True or
     they are passed."""
     N, D = _rows(x, "x")
-    F = w1.shape[0]
-    bf16 = torch.bfloat16
-    with _on_stream(stream):
-        h = torch.empty((N, F), dtype=bf16, device=x.device) if h is None else h
-        if save:
-            g = torch.empty_like(h) if g is None else g
-            u = torch.empty_like(h) if u is None else u
-        ws = _scratch("gated_linear", N, D, F, x.device) if ws is None else ws
-    _check_all((x, bf16, (N, D), "x"), (w1, bf16, (F, D), "w1"), (w3, bf16, (F, D), "w3"), (h, bf16, (N, F), "h"),
-               (g, bf16, (N, F), "g"), (u, bf16, (N, F), "u"))
-    _check("moe_gated_linear", load().moe_gated_linear(
-        _addr(x), _addr(w1), _addr(w3), N, D, F, fn, _addr(h), _addr(g), _addr(u), _addr(ws), ws.numel(),
-        _stream(stream)))
+    wide = _rows(w1, "w1")
+    F = wide[0]
+    if h is None:
+        h, = _new(stream, ((N, F), _BF16, x.device))
+    if save and (g is None or u is None):
+        g2, u2 = _new(stream, ((N, F), _BF16, x.device), ((N, F), _BF16, x.device))
+        g, u = g2 if g is None else g, u2 if u is None else u
+    if ws is None:
+        ws = _scratch(stream, "gated_linear", N, D, F, x.device)
+    if not (_fits(x, _BF16, (N, D)) and _fits(w1, _BF16, (F, D)) and _fits(w3, _BF16, (F, D)) and _fits(h, _BF16, (N, F)) and ws.is_cuda
+            and (g is None or _fits(g, _BF16, (N, F))) and (u is None or _fits(u, _BF16, (N, F)))):
+        _explain(ws, (x, _BF16, (N, D), "x"), (w1, _BF16, (F, D), "w1"), (w3, _BF16, (F, D), "w3"), (h, _BF16, (N, F), "h"),
+                 (g, _BF16, (N, F), "g"), (u, _BF16, (N, F), "u"))
+    s = (_lib or load()).moe_gated_linear(_addr(x), _addr(w1), _addr(w3), N, D, F, fn, _addr(h), _addr(g), _addr(u),
+                                          _addr(ws), ws.numel(), _stream_of(x, stream))
+    if s:
+        _check("moe_gated_linear", s)
     return h, g, u
 
 
 def moe_gated_linear_backward(dh, x, w1, w3, g, u, fn: int = FN_SILU, dx=None, dw1=None, dw3=None, ws=None, stream=None):
     """Gradient of moe_gated_linear from dh and the g, u it kept: (dx, dw1, dw3)."""
     N, D = _rows(x, "x")
-    F = w1.shape[0]
-    bf16 = torch.bfloat16
-    with _on_stream(stream):
-        dx = torch.empty_like(x) if dx is None else dx
-        dw1 = torch.empty_like(w1) if dw1 is None else dw1
-        dw3 = torch.empty_like(w3) if dw3 is None else dw3
-        ws = _scratch("gated_linear_backward", N, D, F, x.device) if ws is None else ws
-    _check_all((dh, bf16, (N, F), "dh"), (x, bf16, (N, D), "x"), (w1, bf16, (F, D), "w1"), (w3, bf16, (F, D), "w3"),
-               (g, bf16, (N, F), "g"), (u, bf16, (N, F), "u"), (dx, bf16, (N, D), "dx"), (dw1, bf16, (F, D), "dw1"),
-               (dw3, bf16, (F, D), "dw3"))
-    _check("moe_gated_linear_backward", load().moe_gated_linear_backward(
-        _addr(dh), _addr(x), _addr(w1), _addr(w3), _addr(g), _addr(u), N, D, F, fn, _addr(dx), _addr(dw1), _addr(dw3),
-        _addr(ws), ws.numel(), _stream(stream)))
+    F = _rows(w1, "w1")[0]
+    dev = x.device
+    if dx is None:
+        dx, = _new(stream, ((N, D), _BF16, dev))
+    if dw1 is None:
+        dw1, = _new(stream, ((F, D), _BF16, dev))
+    if dw3 is None:
+        dw3, = _new(stream, ((F, D), _BF16, dev))
+    if ws is None:
+        ws = _scratch(stream, "gated_linear_backward", N, D, F, dev)
+    _explain(ws, (dh, _BF16, (N, F), "dh"), (x, _BF16, (N, D), "x"), (w1, _BF16, (F, D), "w1"), (w3, _BF16, (F, D), "w3"),
+             (g, _BF16, (N, F), "g"), (u, _BF16, (N, F), "u"), (dx, _BF16, (N, D), "dx"), (dw1, _BF16, (F, D), "dw1"),
+             (dw3, _BF16, (F, D), "dw3"))
+    s = (_lib or load()).moe_gated_linear_backward(_addr(dh), _addr(x), _addr(w1), _addr(w3), _addr(g), _addr(u), N, D, F,
+                                                   fn, _addr(dx), _addr(dw1), _addr(dw3), _addr(ws), ws.numel(),
+                                                   _stream_of(x, stream))
+    if s:
+        _check("moe_gated_linear_backward", s)
     return dx, dw1, dw3
 
 
@@ -800,18 +835,22 @@ def moe_linear(x, w, bias=None, residual=None, fn: int = FN_NONE, save: bool = F
     Returns (y, z); z (the pre-activation, for the backward pass) is None unless
     save=True or it is passed."""
     N, D = _rows(x, "x")
-    F = w.shape[0]
-    bf16 = torch.bfloat16
-    with _on_stream(stream):
-        y = torch.empty((N, F), dtype=bf16, device=x.device) if y is None else y
-        if save and z is None:
-            z = torch.empty_like(y)
-        ws = _scratch("linear", N, D, F, x.device) if ws is None else ws
-    _check_all((x, bf16, (N, D), "x"), (w, bf16, (F, D), "w"), (bias, torch.float32, (F,), "bias"),
-               (residual, bf16, (N, F), "residual"), (y, bf16, (N, F), "y"), (z, bf16, (N, F), "z"))
-    _check("moe_linear", load().moe_linear(
-        _addr(x), _addr(w), _addr(bias), _addr(residual), N, D, F, fn, _addr(y), _addr(z), _addr(ws), ws.numel(),
-        _stream(stream)))
+    F = _rows(w, "w")[0]
+    if y is None:
+        y, = _new(stream, ((N, F), _BF16, x.device))
+    if save and z is None:
+        z, = _new(stream, ((N, F), _BF16, x.device))
+    if ws is None:
+        ws = _scratch(stream, "linear", N, D, F, x.device)
+    if not (_fits(x, _BF16, (N, D)) and _fits(w, _BF16, (F, D)) and _fits(y, _BF16, (N, F)) and ws.is_cuda
+            and (bias is None or _fits(bias, _F32, (F,))) and (residual is None or _fits(residual, _BF16, (N, F)))
+            and (z is None or _fits(z, _BF16, (N, F)))):
+        _explain(ws, (x, _BF16, (N, D), "x"), (w, _BF16, (F, D), "w"), (bias, _F32, (F,), "bias"),
+                 (residual, _BF16, (N, F), "residual"), (y, _BF16, (N, F), "y"), (z, _BF16, (N, F), "z"))
+    s = (_lib or load()).moe_linear(_addr(x), _addr(w), _addr(bias), _addr(residual), N, D, F, fn, _addr(y), _addr(z),
+                                    _addr(ws), ws.numel(), _stream_of(x, stream))
+    if s:
+        _check("moe_linear", s)
     return y, z
 
 
@@ -821,17 +860,20 @@ def moe_linear_backward(dy, x, w, z=None, fn: int = FN_NONE, need_dbias: bool = 
     FN_NONE): (dx, dw, dbias); dbias is fp32, None unless need_dbias=True or it
     is passed.  The residual's gradient is dy."""
     N, D = _rows(x, "x")
-    F = w.shape[0]
-    bf16 = torch.bfloat16
-    with _on_stream(stream):
-        dx = torch.empty_like(x) if dx is None else dx
-        dw = torch.empty_like(w) if dw is None else dw
-        if need_dbias and dbias is None:
-            dbias = torch.empty(F, dtype=torch.float32, device=x.device)
-        ws = _scratch("linear_backward", N, D, F, x.device) if ws is None else ws
-    _check_all((dy, bf16, (N, F), "dy"), (x, bf16, (N, D), "x"), (w, bf16, (F, D), "w"), (z, bf16, (N, F), "z"),
-               (dx, bf16, (N, D), "dx"), (dw, bf16, (F, D), "dw"), (dbias, torch.float32, (F,), "dbias"))
-    _check("moe_linear_backward", load().moe_linear_backward(
-        _addr(dy), _addr(x), _addr(w), _addr(z), N, D, F, fn, _addr(dx), _addr(dw), _addr(dbias), _addr(ws), ws.numel(),
-        _stream(stream)))
+    F = _rows(w, "w")[0]
+    dev = x.device
+    if dx is None:
+        dx, = _new(stream, ((N, D), _BF16, dev))
+    if dw is None:
+        dw, = _new(stream, ((F, D), _BF16, dev))
+    if need_dbias and dbias is None:
+        dbias, = _new(stream, ((F,), _F32, dev))
+    if ws is None:
+        ws = _scratch(stream, "linear_backward", N, D, F, dev)
+    _explain(ws, (dy, _BF16, (N, F), "dy"), (x, _BF16, (N, D), "x"), (w, _BF16, (F, D), "w"), (z, _BF16, (N, F), "z"),
+             (dx, _BF16, (N, D), "dx"), (dw, _BF16, (F, D), "dw"), (dbias, _F32, (F,), "dbias"))
+    s = (_lib or load()).moe_linear_backward(_addr(dy), _addr(x), _addr(w), _addr(z), N, D, F, fn, _addr(dx), _addr(dw),
+                                             _addr(dbias), _addr(ws), ws.numel(), _stream_of(x, stream))
+    if s:
+        _check("moe_linear_backward", s)
     return dx, dw, dbias
