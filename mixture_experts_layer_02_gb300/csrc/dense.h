@@ -33,13 +33,14 @@ struct NormBwdArgs {
     const uint16_t* dresidual;  // [rows, D] or NULL
     uint16_t* dx;               // [rows, D]
     float* dweight;             // [D] or NULL
-    float* partial;             // [rmsnorm_bwd_parts(rows)][D]
+    float* partial;             // [rmsnorm_bwd_parts(rows, D)][D]
     long long rows;
     int D;
     float eps;
+    uint32_t* err;              // workspace error word
 };
 // Row groups whose dweight sums are kept apart (the workspace's size; the same on every device).
-int rmsnorm_bwd_parts(long long rows);
+int rmsnorm_bwd_parts(long long rows, int D);
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t st);
 
 // out[c] = sum over p (in order) of partial[p][c].

@@ -202,7 +202,7 @@ moe_status zero(void* p, size_t bytes, cudaStream_t st) {
 size_t moe::dense_workspace_size(const char* op, int N, int D, int F) {
     if (!strcmp(op, "rmsnorm_backward")) {
         if (check_norm(N, D, 0.0f) != MOE_OK) return 0;
-        return kWsHeaderBytes + up256(static_cast<size_t>(rmsnorm_bwd_parts(N)) * D * sizeof(float));
+        return kWsHeaderBytes + up256(static_cast<size_t>(rmsnorm_bwd_parts(N, D)) * D * sizeof(float));
     }
     const bool gated = !strcmp(op, "gated_linear_backward");
     if (!strcmp(op, "gated_linear") || !strcmp(op, "linear"))
@@ -247,7 +247,7 @@ moe_status moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* s_in, const 
     NEED(dx);
     NEED_WS(dense_workspace_size("rmsnorm_backward", N, D, 0));
     const NormBwdArgs a = {dy, s_in, weight, dresidual, dx, dweight, reinterpret_cast<float*>(at(ws, kWsHeaderBytes)),
-                           N, D, eps};
+                           N, D, eps, static_cast<uint32_t*>(ws)};
     return launched(launch_rmsnorm_bwd(a, st), "rmsnorm backward launch");
 }
 
