@@ -25,7 +25,10 @@ SOURCES = ["grouped_gemm.cu", "grouped_gemm_e4m3.cu", "grouped_gemm_2sm.cu", "gr
            "grouped_gemm_2sm_mixed.cu",
            "grouped_gemm_swap.cu", "grouped_gemm_swap_e4m3.cu", "grouped_gemm_gather.cu",
            "grouped_gemm_gather_e4m3.cu", "grouped_gemm_gather_small.cu", "ffn_fused_decode.cu", "layer_decode.cu", "quant.cu", "route_reduce.cu",
-           "permute.cu", "combine.cu", "rmsnorm.cu", "dense_grad.cu", "dense_gemm_split.cu",
+           "permute.cu", "combine.cu", "rmsnorm.cu", "dense_grad.cu", "dense_gemm_split_gated.cu",
+           "dense_gemm_split_linear.cu", "dense_gemm_split_dgrad.cu", "dense_gemm_split_wgrad.cu",
+           "dense_gemm_pairsplit_gated.cu", "dense_gemm_pairsplit_linear.cu", "dense_gemm_pairsplit_dgrad.cu",
+           "dense_gemm_pairsplit_wgrad.cu",
            "dense_gemm_pair.cu", "dense_gemv.cu", "dense_api.cu",
            "moe_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

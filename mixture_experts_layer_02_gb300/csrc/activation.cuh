@@ -16,15 +16,39 @@ enum { FN_NONE = 0, FN_RELU = 1, FN_SILU = 2, FN_GELU = 3, FN_GELU_TANH = 4 };
 constexpr float kGeluTanh2 = 1.5957691216057308f;
 constexpr float kGeluCubic = 0.044715f;
 
-// The normal distribution function by erfc: 1 + erf would cancel for negative z.
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
+// The normal distribution function Phi(z); `e` gets exp(-z^2 / 2) (its density
+// times sqrt(2 pi)).  For x = |z| / sqrt 2, erfc(x) = exp(-x^2) erfcx(x), and
+// erfcx(x) is t P(t) with t = 1 / (1 + 0.4 x): P is the polynomial of degree 8
+// with the least relative error over 0 <= x <= 14 (reweighted least squares on
+// 4000 Chebyshev points): 9e-8, 4e-7 evaluated in fp32.  The relative error
+// holds far into the negative tail, where 1 + erf would cancel, and one
+// exponential serves the value and the slope.  erfcf took 2.5 times the
+// instructions, and a gelu epilogue or gradient was bound by them.
+__device__ __forceinline__ float normal_cdf(float z, float& e) {
+    const float t = __fdividef(1.0f, fmaf(0.28284271247461903f, fabsf(z), 1.0f));
+    float p = 0.0459682680666447f;
+    p = fmaf(p, t, -0.1630595624446869f);
+    p = fmaf(p, t, 0.1304987967014313f);
+    p = fmaf(p, t, 0.0354329086840153f);
+    p = fmaf(p, t, 0.1154701560735703f);
+    p = fmaf(p, t, 0.1784794181585312f);
+    p = fmaf(p, t, 0.2056105583906174f);
+    p = fmaf(p, t, 0.2259367406368256f);
+    p = fmaf(p, t, 0.2256629019975662f);
+    e = __expf(-0.5f * z * z);
+    const float tail = 0.5f * e * (p * t);
+    return z >= 0.0f ? 1.0f - tail : tail;
+}
 
 // fn is the same for every thread of a launch.  A NaN comes out a NaN.
 __device__ __forceinline__ float act_value(int fn, float z) {
     switch (fn) {
         case FN_RELU: return z <= 0.0f ? 0.0f : z;
         case FN_SILU: return silu_f32(z);
-        case FN_GELU: return z * normal_cdf(z);
+        case FN_GELU: {
+            float e;
+            return z * normal_cdf(z, e);
+        }
         case FN_GELU_TANH: return __fdividef(z, 1.0f + __expf(-kGeluTanh2 * (z + kGeluCubic * z * z * z)));
         default: return z;
     }
@@ -52,9 +76,10 @@ __device__ __forceinline__ float act_slope(int fn, float z, float& value) {
             return p * (1.0f + z * m);
         }
         case FN_GELU: {
-            const float c = normal_cdf(z);
+            float e;
+            const float c = normal_cdf(z, e);
             value = z * c;
-            return c + z * 0.3989422804014327f * __expf(-0.5f * z * z);  // 1/sqrt(2 pi)
+            return c + z * 0.3989422804014327f * e;  // 1/sqrt(2 pi)
         }
         case FN_GELU_TANH: {
             float m;

@@ -92,11 +92,31 @@ int make_bf16_map(CUtensorMap* m, const void* base, long long rows, long long co
 // moe_workspace_size of the dense operations (dense_api.cu); 0 for another name or invalid sizes.
 size_t dense_workspace_size(const char* op, int N, int D, int F);
 
-// One CTA per 128 x 128 tile, the reduction over K split over a cluster of
-// `splits` CTAs (1, 2, 4 or 8) and joined through distributed shared memory.
-cudaError_t dense_split_limit(DenseKind kind, int splits, int* clusters);  // clusters the device holds at once
-cudaError_t launch_dense_split(DenseKind kind, const CUtensorMap* maps, const DenseArgs& a, int splits,
-                               cudaStream_t st);
+// Tiles with the reduction over K split over a cluster: bn = 0: one CTA per
+// 128 x 128 tile and part of K (splits 1, 2, 4 or 8); bn = 128 or 256: a CTA pair
+// per 256 x bn tile and part (splits 1, 2 or 4).  clusters != NULL: launch
+// nothing, tell how many clusters the device holds at once.
+cudaError_t dense_split_gated(const CUtensorMap*, const DenseArgs&, int splits, cudaStream_t, int* clusters);
+cudaError_t dense_pairsplit_gated(const CUtensorMap*, const DenseArgs&, int bn, int splits, cudaStream_t, int* clusters);
+cudaError_t dense_split_linear(const CUtensorMap*, const DenseArgs&, int splits, cudaStream_t, int* clusters);
+cudaError_t dense_pairsplit_linear(const CUtensorMap*, const DenseArgs&, int bn, int splits, cudaStream_t, int* clusters);
+cudaError_t dense_split_dgrad(const CUtensorMap*, const DenseArgs&, int splits, cudaStream_t, int* clusters);
+cudaError_t dense_pairsplit_dgrad(const CUtensorMap*, const DenseArgs&, int bn, int splits, cudaStream_t, int* clusters);
+cudaError_t dense_split_wgrad(const CUtensorMap*, const DenseArgs&, int splits, cudaStream_t, int* clusters);
+cudaError_t dense_pairsplit_wgrad(const CUtensorMap*, const DenseArgs&, int bn, int splits, cudaStream_t, int* clusters);
+inline cudaError_t dense_split(DenseKind kind, const CUtensorMap* m, const DenseArgs& a, int bn, int splits,
+                               cudaStream_t st, int* clusters = nullptr) {
+    switch (kind) {
+        case DENSE_GATED:
+            return bn ? dense_pairsplit_gated(m, a, bn, splits, st, clusters) : dense_split_gated(m, a, splits, st, clusters);
+        case DENSE_LINEAR:
+            return bn ? dense_pairsplit_linear(m, a, bn, splits, st, clusters) : dense_split_linear(m, a, splits, st, clusters);
+        case DENSE_DGRAD:
+            return bn ? dense_pairsplit_dgrad(m, a, bn, splits, st, clusters) : dense_split_dgrad(m, a, splits, st, clusters);
+        default:
+            return bn ? dense_pairsplit_wgrad(m, a, bn, splits, st, clusters) : dense_split_wgrad(m, a, splits, st, clusters);
+    }
+}
 
 // A few rows (DENSE_GATED, DENSE_LINEAR; M <= kGemvMaxRows): one pass over the weights.
 constexpr int kGemvMaxRows = 16;

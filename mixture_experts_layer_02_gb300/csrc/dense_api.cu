@@ -97,16 +97,19 @@ uint8_t* at(void* ws, size_t off) { return static_cast<uint8_t*>(ws) + off; }
 
 // ---- the choice of kernel ----
 // Estimated microseconds, fitted to measured times (33 to 4096 rows, K 1024 to
-// 14336): a k-block (64 of K) of a one-CTA 128 x 128 tile takes 0.27 us with
-// the GPU full (the SMs' reads from L2 hold it back) and a round of such tiles
-// 5.5 us of first load, join and epilogue; a k-block of a 256 x 256 pair tile
-// 0.36 us, 0.95 of that where two pairs share an operand, and a round 3 us.
-constexpr double kSplitBlock = 0.27, kSplitRound = 5.5;
-constexpr double kPairBlock = 0.36, kPairRound = 3.0, kPairOnce = 3.0, kMulticastRate = 0.95;
+// 14336): k-blocks (64 of K) a round times the time of one, plus the round's
+// first load, join and epilogue.
+struct TileKind {
+    int bn;          // 0: one CTA, 128 x 128; else a pair, 256 x bn
+    double block, round;
+};
+constexpr TileKind kSplitTiles[3] = {{0, 0.25, 5.0}, {128, 0.20, 5.5}, {256, 0.30, 6.0}};
+// persistent pairs: 0.97 of the block where two pairs share an operand
+constexpr double kPairBlock = 0.34, kPairRound = 3.0, kPairOnce = 3.0, kMulticastRate = 0.97;
 
 struct Plan {
-    int splits;             // split kernel: CTAs over K
-    int cluster, clusters;  // pair kernel (cluster 0: the split kernel)
+    int bn, splits;         // split tiles
+    int cluster, clusters;  // persistent pairs (cluster 0: split tiles)
 };
 
 int env_int(const char* name, int dflt) {
@@ -114,21 +117,30 @@ int env_int(const char* name, int dflt) {
     return f ? atoi(f) : dflt;
 }
 
-// MOE_DENSE_KERNEL = 1 (split), 2 (pairs) or 3 (streamed weights, where M allows), MOE_DENSE_SPLITS and
-// MOE_DENSE_CLUSTER = 2 or 4 force a choice, for tuning and test coverage.
+// MOE_DENSE_KERNEL = 1 (split tiles), 2 (persistent pairs) or 3 (streamed weights,
+// where M allows), MOE_DENSE_SPLIT = 10 * bn + splits and MOE_DENSE_CLUSTER = 2 or
+// 4 force a choice, for tuning and test coverage.
 moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p) {
-    const int n1 = kind == DENSE_GATED ? 64 : 128, n2 = kind == DENSE_GATED ? 128 : 256;
-    const long long t1 = static_cast<long long>((a.M + kBM - 1) / kBM) * ((a.N + n1 - 1) / n1) * a.mats;
-    const int kernel = env_int("MOE_DENSE_KERNEL", 0), fixed = env_int("MOE_DENSE_SPLITS", 0);
-    *p = {1, 0, 0};
+    const int n2 = kind == DENSE_GATED ? 128 : 256;
+    const int kernel = env_int("MOE_DENSE_KERNEL", 0), fixed = env_int("MOE_DENSE_SPLIT", -1);
+    *p = {0, 1, 0, 0};
     double best = 1e30;
-    for (int s = 1; s <= 8 && s <= kblocks; s *= 2) {
-        if (fixed && s > fixed) break;
-        int limit = 0;
-        const moe_status st = launched(dense_split_limit(kind, s, &limit), "dense split limit");
-        if (st != MOE_OK) return st;
-        const double c = static_cast<double>((t1 + limit - 1) / limit) * (kblocks * kSplitBlock / s + kSplitRound);
-        if (fixed || c < best) best = c, p->splits = s;
+    for (const TileKind& t : kSplitTiles) {
+        const int rows = t.bn ? 2 * kBM : kBM, width = (t.bn ? t.bn : 128) / (kind == DENSE_GATED ? 2 : 1);
+        const long long tiles = static_cast<long long>((a.M + rows - 1) / rows) * ((a.N + width - 1) / width) * a.mats;
+        // every part of K has work: an empty one would add what its accumulator held before
+        for (int s = 1; s <= (t.bn ? 4 : 8) && s <= kblocks; s *= 2) {
+            if (fixed >= 0 && fixed != 10 * t.bn + s) continue;
+            int limit = 0;
+            const moe_status st = launched(dense_split(kind, nullptr, a, t.bn, s, nullptr, &limit), "dense split limit");
+            if (st != MOE_OK) return st;
+            const double c = static_cast<double>((tiles + limit - 1) / limit) * (kblocks * t.block / s + t.round);
+            if (c < best) {
+                best = c;
+                p->bn = t.bn;
+                p->splits = s;
+            }
+        }
     }
     if (kernel == 1) return MOE_OK;
     if (kernel == 2) best = 1e30;
@@ -161,7 +173,7 @@ moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, c
     const moe_status planned = plan_product(kind, a, kblocks, &p);
     if (planned != MOE_OK) return planned;
     // K-major boxes: 128 rows of A; of B what one CTA loads at a time
-    const int b_rows = p.cluster ? 256 / p.cluster : (kind == DENSE_GATED ? 64 : 128);
+    const int b_rows = p.cluster ? 256 / p.cluster : (p.bn ? p.bn / 2 : (kind == DENSE_GATED ? 64 : 128));
     CUtensorMap m[4];
     auto map_a = [&](CUtensorMap* t, const uint16_t* q) {
         return a_mn ? make_bf16_map(t, q, a.K, a.M, 64) : make_bf16_map(t, q, a.M, a.K, kBM);
@@ -176,7 +188,7 @@ moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, c
     if (s != 0) return static_cast<moe_status>(s);
     if (!o.a1) m[1] = m[0];
     if (!o.b1) m[3] = m[2];
-    if (!p.cluster) return launched(launch_dense_split(kind, m, a, p.splits, st), "dense product launch");
+    if (!p.cluster) return launched(dense_split(kind, m, a, p.bn, p.splits, st), "dense product launch");
     return launched(launch_dense_pair(kind, m, a, p.cluster, p.clusters, st), "dense pair product launch");
 }
 

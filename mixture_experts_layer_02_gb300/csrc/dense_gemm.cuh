@@ -60,29 +60,72 @@ __device__ __forceinline__ void tma_load_2d_pair_multicast(const CUtensorMap* ma
         : "memory");
 }
 
-// mbar_wait whose tries may suspend the thread for up to 20 us each: the
-// epilogue warps wait for a whole main loop, and polling costs power that the
-// tensor cores could use.
-__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+// ---- waiting ----
+// Waits on an mbarrier are polls, and polls of one SM queue up behind one
+// another: with six to eight warps polling for the end of a main loop, each wait
+// and each copy of its producer took about 370 clocks (time stamps), 730 a
+// k-block of 256 to 512 clocks of MMA.  So during a main loop only its producer
+// and its MMA issuer poll (pipe_wait); one thread waits for the accumulator,
+// asleep between polls (idle_wait), and everybody else stands at a hardware
+// barrier.  Both end after kWaitLimitNs.
+__device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+    return mbar_wait(bar, parity, abort, err);
+}
+
+__device__ __forceinline__ bool idle_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
     const uint64_t t0 = globaltimer_ns();
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-            : "memory");
-        if (ok) return true;
+    while (!mbar_test_wait(bar, parity)) {
         if (*abort) return false;
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;
             record_error(err, MOE_DEVERR_TIMEOUT);
             return false;
         }
+        __nanosleep(128);
     }
+    return true;
 }
+
+// ---- issuing MMAs ----
+// One lane of a converged warp, as a predicate the compiler knows to hold for a
+// single thread: what the others compute alike stays in uniform registers, which
+// the MMA instructions take their descriptors from.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// The MMA warp's walk over the stages, executed by all of its lanes.  A wait on
+// an mbarrier that is complete still takes about 200 clocks to answer, so the
+// next stage's barrier is asked before this stage's MMAs are issued.
+struct StageWalk {
+    uint64_t* full;
+    int stages, stage;
+    uint32_t phase;
+    bool ready;  // the barrier of `stage` has been seen complete
+
+    __device__ __forceinline__ StageWalk(uint64_t* f, int n) : full(f), stages(n), stage(0), phase(0), ready(false) {}
+    // false: given up, by all lanes
+    __device__ __forceinline__ bool wait(volatile int* abort, uint32_t* err) {
+        const bool ok = ready || pipe_wait(&full[stage], phase, abort, err);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        __syncwarp();
+        const int next = stage + 1 == stages ? 0 : stage + 1;
+        ready = mbar_test_wait(&full[next], next == 0 ? phase ^ 1u : phase);
+        return true;
+    }
+    __device__ __forceinline__ void advance() {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
 
 // 32 accumulator columns of this thread's row, as floats.
 __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[32]) {

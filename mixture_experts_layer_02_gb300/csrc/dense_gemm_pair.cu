@@ -36,7 +36,7 @@ constexpr int kStages = 6;
 constexpr int kOperand = kBM * kRowBytes;        // 16 KB: this CTA's half of an operand
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kThreads = (3 + kEpiWarps) * 32;  // A copies, MMA issuer, epilogue, B copies
 constexpr int kBand = 8;
 constexpr int kQuarter = kOperand / 2;           // what a CTA of a cluster of four loads of its B half
 constexpr size_t kPairSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kEpiWarps * kChunkBytes + (2 * kStages + 5) * 8 + 16;
@@ -121,7 +121,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), lead);
     pdl_wait();
 
-    if (warp == 0) {
+    if (warp == 0) {  // copies of A; the even CTA's also announces the stage's bytes
         if (lane == 0) {
             bool withhold = a.dbg && (*a.dbg & MOE_DBG_WITHHOLD_FIRST_LOAD) && blockIdx.x == 0;
             uint32_t pending = 0, pend_parity = 0;
@@ -131,16 +131,14 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             for (int tile = first; ok && tile < tiles; tile += step) {
                 const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
                 const int arow = w.m0 + static_cast<int>(crank) * kBM;
-                const int bcol = w.n0 + (L::GATED ? 0 : static_cast<int>(rank) * (kPairTile / 2));
                 for (int kb = 0; kb < total_kb; ++kb) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
+                    if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
                     if (withhold) {
                         withhold = false;  // test hook: this stage never fills
                     } else {
                         const int seg = kb >= kbs ? 1 : 0, k0 = (kb - seg * kbs) * kBK;
                         const uint32_t bar = full_lead + 8u * stage;
                         uint8_t* dA = sA + stage * kOperand;
-                        uint8_t* dB = sB + stage * kOperand;
                         if (leader) {
                             mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
                             pending |= 1u << stage;
@@ -153,19 +151,6 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                         } else {
                             tma_load_2d_pair(mA, bar, dA, k0, arow);
                         }
-                        const CUtensorMap* mB = L::GATED ? (rank ? &tmB1 : &tmB0) : (L::B_MN && seg ? &tmB1 : &tmB0);
-                        if constexpr (CL == 4) {  // half of the B half, to both CTAs of this parity
-                            const int part = static_cast<int>(crank >> 1);
-                            const uint16_t mask = static_cast<uint16_t>(0x5u << rank);
-                            const int b64 = bcol + part * 64;
-                            tma_load_2d_pair_multicast(mB, bar, dB + part * kQuarter, L::B_MN ? b64 : k0,
-                                                       L::B_MN ? k0 : b64, mask);
-                        } else if constexpr (L::B_MN) {
-                            tma_load_2d_pair(mB, bar, dB, bcol, k0);
-                            tma_load_2d_pair(mB, bar, dB + kMnBlockBytes, bcol + 64, k0);
-                        } else {
-                            tma_load_2d_pair(mB, bar, dB, k0, bcol);
-                        }
                     }
                     if (++stage == S) { stage = 0; phase ^= 1u; }
                 }
@@ -173,38 +158,74 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             for (int s = 0; s < S; ++s)
                 if (pending & (1u << s)) drain_wait(&full[s], (pend_parity >> s) & 1u, err);
         }
-    } else if (warp == 1) {
+    } else if (warp == 2 + kEpiWarps) {  // copies of B
         if (lane == 0) {
-            if (leader) {
-                constexpr uint32_t idesc = dense_idesc<KIND>(kPairTile, kPairTile);
-                int stage = 0, acc = 0;
-                uint32_t phase = 0, acc_phase = 0;
-                bool ok = true;
-                for (int tile = first; ok && tile < tiles; tile += step) {
-                    if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, err)) break;
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += step) {
+                const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
+                const int bcol = w.n0 + (L::GATED ? 0 : static_cast<int>(rank) * (kPairTile / 2));
+                for (int kb = 0; kb < total_kb; ++kb) {
+                    if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
+                    const int seg = kb >= kbs ? 1 : 0, k0 = (kb - seg * kbs) * kBK;
+                    const uint32_t bar = full_lead + 8u * stage;
+                    uint8_t* dB = sB + stage * kOperand;
+                    const CUtensorMap* mB = L::GATED ? (rank ? &tmB1 : &tmB0) : (L::B_MN && seg ? &tmB1 : &tmB0);
+                    if constexpr (CL == 4) {  // half of the B half, to both CTAs of this parity
+                        const int part = static_cast<int>(crank >> 1);
+                        const uint16_t mask = static_cast<uint16_t>(0x5u << rank);
+                        const int b64 = bcol + part * 64;
+                        tma_load_2d_pair_multicast(mB, bar, dB + part * kQuarter, L::B_MN ? b64 : k0, L::B_MN ? k0 : b64,
+                                                   mask);
+                    } else if constexpr (L::B_MN) {
+                        tma_load_2d_pair(mB, bar, dB, bcol, k0);
+                        tma_load_2d_pair(mB, bar, dB + kMnBlockBytes, bcol + 64, k0);
+                    } else {
+                        tma_load_2d_pair(mB, bar, dB, k0, bcol);
+                    }
+                    if (++stage == S) { stage = 0; phase ^= 1u; }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (leader) {
+            constexpr uint32_t idesc = dense_idesc<KIND>(kPairTile, kPairTile);
+            StageWalk w(full, S);
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int tile = first; ok && tile < tiles; tile += step) {
+                ok = __all_sync(0xffffffffu, pipe_wait(&tempty[acc], acc_phase ^ 1u, abort_flag, err));
+                if (!ok) break;
+                __syncwarp();
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kPairTile);
+                for (int kb = 0; kb < total_kb; ++kb) {
+                    if (!w.wait(abort_flag, err)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kPairTile);
-                    for (int kb = 0; kb < total_kb; ++kb) {
-                        if (!mbar_wait(&full[stage], phase, abort_flag, err)) { ok = false; break; }
-                        tc_fence_after();
-                        const uint64_t ad = operand_desc<L::A_MN>(smem_u32(sA + stage * kOperand));
-                        const uint64_t bd = operand_desc<L::B_MN>(smem_u32(sB + stage * kOperand));
+                    const uint64_t ad = operand_desc<L::A_MN>(smem_u32(sA + w.stage * kOperand));
+                    const uint64_t bd = operand_desc<L::B_MN>(smem_u32(sB + w.stage * kOperand));
+                    if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kBK / 16; ++k)
                             umma_bf16_pair(d, ad + k * kDescStep<L::A_MN>, bd + k * kDescStep<L::B_MN>, idesc,
                                            (kb | k) != 0 ? 1u : 0u);
-                        umma_commit_pair_multicast(&empty[stage], all);
-                        if (++stage == S) { stage = 0; phase ^= 1u; }
+                        umma_commit_pair_multicast(&empty[w.stage], all);
                     }
-                    if (!ok) break;
-                    umma_commit_pair_multicast(&tfull[acc], both);
-                    acc ^= 1;
-                    if (acc == 0) acc_phase ^= 1u;
+                    __syncwarp();
+                    w.advance();
                 }
-                umma_commit_pair_multicast(drain, both);
+                if (!ok) break;
+                if (elect_one()) umma_commit_pair_multicast(&tfull[acc], both);
+                __syncwarp();
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
             }
-            drain_wait(drain, 0, err);  // the pair MMAs wrote this CTA's TMEM too
+            if (elect_one()) umma_commit_pair_multicast(drain, both);
+            __syncwarp();
         }
+        if (lane == 0) drain_wait(drain, 0, err);  // the pair MMAs wrote this CTA's TMEM too
     } else {
         // epilogue warp (q, half): TMEM lanes 32 q .., accumulator columns [0, 128) or [128, 256);
         // gated: 64 gate columns and the 64 up columns that belong to them
@@ -215,9 +236,9 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         uint32_t acc_phase = 0;
         for (int tile = first; tile < tiles; tile += step) {
             const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
-            const bool ok = lane != 0 || mbar_wait_long(&tfull[acc], acc_phase, abort_flag, err);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            const bool ok = warp != 2 || lane != 0 || idle_wait(&tfull[acc], acc_phase, abort_flag, err);
             __syncwarp();
+            if (!named_barrier_and(1, kEpiWarps * 32, ok)) break;  // given up: by all of them
             tc_fence_after();
             const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kPairTile);
             const long long row0 = static_cast<long long>(w.m0) + crank * kBM + q * 32;

@@ -1,4 +1,4 @@
-// dense_gemm_split.cu -- the dense products on one-CTA 128 x 128 tiles with the
+// dense_gemm_split.cuh -- the dense products on one-CTA 128 x 128 tiles with the
 // reduction over K split over a cluster.
 //
 // A product with few tiles (few tokens, or a small weight gradient) leaves most
@@ -10,19 +10,27 @@
 // epilogue on the sums.  No fp32 partials reach HBM, there is no second launch,
 // and the order of the additions is fixed.
 //
-// Warp roles: 0 TMA producer, 1 TMEM allocator and MMA issuer, 4..7 park the
+// For at most 128 rows (more: dense_gemm_pairsplit.cuh), where the weights come
+// from HBM once and latency is the rest.
+//   - Time stamps at 256 x 4096 x 4096 (S = 2, 32 k-blocks a CTA) showed a TMA
+//     round trip of 1.1 us: three 32 KB stages moved a k-block each 0.37 us,
+//     six (one CTA an SM) each 0.25 us.  That is what an SM takes in (64 bytes a
+//     clock), so sharing operand tiles over a cluster by multicast, which was
+//     built and measured, changed nothing here.
+//   - The join took 4 us with one octet of a row after another; every thread now
+//     issues all its distributed-shared-memory loads at once, of rows that exist,
+//     and rows are dealt to the CTAs in turn (a 33-row product would otherwise
+//     leave the join to one of them).
+//
+// Warp roles: 0 copies A, 2 copies B (one thread issuing both took longer than a
+// k-block's MMAs), 1 allocates TMEM and issues the MMAs, 4..7 park the
 // accumulator (warp q reads TMEM lanes 32 q ..), all eight warps the join and
 // epilogue.
 //
-// These products are latency-bound.  Time stamps at 256 x 4096 x 4096 (S = 2,
-// 32 k-blocks a CTA) showed a TMA round trip of 1.1 us, so three 32 KB stages
-// moved one k-block each 0.37 us; six stages (one CTA an SM) halve that.  The
-// join took 4 us with one row octet after another; now each thread issues all
-// of its sixteen distributed-shared-memory loads at once, and the residual is
-// fetched before the cluster barrier.
-//
 // Every wait is bounded (mbar_wait); whatever a role sees, every thread reaches
 // both cluster barriers, so no CTA waits for one that left.
+#pragma once
+
 #include <algorithm>
 #include <atomic>
 
@@ -66,9 +74,10 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
     uint64_t* done = empty + S;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int never = 0;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = SPLITS > 1 ? cluster_ctarank() : 0u;
+    const uint32_t rank = SPLITS > 1 ? cluster_ctarank() : 0u;  // the k-part
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmA0);
         tma_prefetch_desc(&tmB0);
@@ -105,69 +114,84 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
     const int k_hi = static_cast<int>(static_cast<long long>(total) * (rank + 1) / SPLITS);
     pdl_wait();
 
-    if (warp == 0) {
+    if (warp == 0) {  // copies of A, and the announcement of the stage's bytes
         if (lane == 0) {
             bool withhold = a.dbg && (*a.dbg & MOE_DBG_WITHHOLD_FIRST_LOAD) && blockIdx.x == 0;
             uint32_t pending = 0, pend_parity = 0;
-            int stage = 0;
+            int stage = 0, seg = k_lo / kbs, kb = k_lo - seg * kbs;
             uint32_t phase = 0;
-            for (int kb = k_lo; kb < k_hi; ++kb) {
-                if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) break;
+            for (int n = k_hi - k_lo; n > 0; --n) {
+                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) break;
                 if (withhold) {
                     withhold = false;  // test hook: this stage never fills
                 } else {
-                    const int seg = kb / kbs, k0 = (kb - seg * kbs) * kBK;
                     uint8_t* sA = smem + stage * kSplitStageBytes;
-                    uint8_t* sB = sA + kOperandBytes;
                     const CUtensorMap* mA = (seg | mat) ? &tmA1 : &tmA0;
                     mbar_arrive_expect_tx(&full[stage], kSplitStageBytes);
                     pending |= 1u << stage;
                     pend_parity = (pend_parity & ~(1u << stage)) | (phase << stage);
                     if constexpr (L::A_MN) {
-                        tma_load_2d(mA, &full[stage], sA, m0, k0);
-                        tma_load_2d(mA, &full[stage], sA + kMnBlockBytes, m0 + 64, k0);
+                        tma_load_2d(mA, &full[stage], sA, m0, kb * kBK);
+                        tma_load_2d(mA, &full[stage], sA + kMnBlockBytes, m0 + 64, kb * kBK);
                     } else {
-                        tma_load_2d(mA, &full[stage], sA, k0, m0);
-                    }
-                    if constexpr (L::GATED) {
-                        tma_load_2d(&tmB0, &full[stage], sB, k0, n0);
-                        tma_load_2d(&tmB1, &full[stage], sB + kOperandBytes / 2, k0, n0);
-                    } else if constexpr (L::B_MN) {
-                        const CUtensorMap* mB = seg ? &tmB1 : &tmB0;
-                        tma_load_2d(mB, &full[stage], sB, n0, k0);
-                        tma_load_2d(mB, &full[stage], sB + kMnBlockBytes, n0 + 64, k0);
-                    } else {
-                        tma_load_2d(&tmB0, &full[stage], sB, k0, n0);
+                        tma_load_2d(mA, &full[stage], sA, kb * kBK, m0);
                     }
                 }
+                if (++kb == kbs) { kb = 0; ++seg; }
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
             for (int s = 0; s < S; ++s)
                 if (pending & (1u << s)) drain_wait(&full[s], (pend_parity >> s) & 1u, a.err);
         }
-    } else if (warp == 1) {
+    } else if (warp == 2) {  // copies of B
         if (lane == 0) {
-            constexpr uint32_t idesc = dense_idesc<KIND>(kBM, kSplitBN);
-            int stage = 0;
+            int stage = 0, seg = k_lo / kbs, kb = k_lo - seg * kbs;
             uint32_t phase = 0;
-            for (int kb = k_lo; kb < k_hi; ++kb) {
-                if (!mbar_wait(&full[stage], phase, abort_flag, a.err)) break;
-                tc_fence_after();
-                const uint32_t sA = smem_u32(smem + stage * kSplitStageBytes);
-                const uint64_t ad = operand_desc<L::A_MN>(sA), bd = operand_desc<L::B_MN>(sA + kOperandBytes);
-#pragma unroll
-                for (int k = 0; k < kBK / 16; ++k)
-                    umma_bf16(tmem, ad + k * kDescStep<L::A_MN>, bd + k * kDescStep<L::B_MN>, idesc,
-                              (kb != k_lo || k != 0) ? 1u : 0u);
-                umma_commit(&empty[stage]);
+            for (int n = k_hi - k_lo; n > 0; --n) {
+                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) break;
+                uint8_t* sB = smem + stage * kSplitStageBytes + kOperandBytes;
+                if constexpr (L::GATED) {
+                    tma_load_2d(&tmB0, &full[stage], sB, kb * kBK, n0);
+                    tma_load_2d(&tmB1, &full[stage], sB + kOperandBytes / 2, kb * kBK, n0);
+                } else if constexpr (L::B_MN) {
+                    const CUtensorMap* mB = seg ? &tmB1 : &tmB0;
+                    tma_load_2d(mB, &full[stage], sB, n0, kb * kBK);
+                    tma_load_2d(mB, &full[stage], sB + kMnBlockBytes, n0 + 64, kb * kBK);
+                } else {
+                    tma_load_2d(&tmB0, &full[stage], sB, kb * kBK, n0);
+                }
+                if (++kb == kbs) { kb = 0; ++seg; }
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
-            umma_commit(done);
-            drain_wait(done, 0, a.err);  // TMEM is released below: nothing may be in flight
         }
-    } else if (warp >= 4) {
-        bool ok = mbar_wait(done, 0, abort_flag, a.err);
-        ok = __all_sync(0xffffffffu, ok);
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = dense_idesc<KIND>(kBM, kSplitBN);
+        StageWalk w(full, S);
+        for (int n = 0; n < k_hi - k_lo; ++n) {
+            if (!w.wait(abort_flag, a.err)) break;
+            tc_fence_after();
+            const uint32_t sA = smem_u32(smem + w.stage * kSplitStageBytes);
+            const uint64_t ad = operand_desc<L::A_MN>(sA), bd = operand_desc<L::B_MN>(sA + kOperandBytes);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k)
+                    umma_bf16(tmem, ad + k * kDescStep<L::A_MN>, bd + k * kDescStep<L::B_MN>, idesc, (n | k) != 0 ? 1u : 0u);
+                umma_commit(&empty[w.stage]);
+            }
+            __syncwarp();
+            w.advance();
+        }
+        if (elect_one()) umma_commit(done);
+        __syncwarp();
+        if (lane == 0) {
+            // to the end whatever happened: TMEM is released below, nothing may be in flight
+            idle_wait(done, 0, &never, a.err);
+        }
+    }
+    __syncwarp();
+    __syncthreads();  // the accumulator is complete (or the product was given up)
+    if (warp >= 4) {
+        const bool ok = *abort_flag == 0;
         tc_fence_after();
         if (ok) {
             const int q = warp & 3;
@@ -184,7 +208,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
             }
         }
     }
-    // This CTA's share of the tile's row octets: items of thread t are t, t + 256, ...
+    // This CTA's share of the join: every SPLITS-th row, 16 (gated: 8) octets a row
     constexpr int OCTETS = N_TILE / 8;
     constexpr int ITEMS = kBM * OCTETS / SPLITS;
     constexpr int PER = (ITEMS + kSplitThreads - 1) / kSplitThreads;
@@ -194,7 +218,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int it = i * kSplitThreads + static_cast<int>(threadIdx.x);
-        const int item = ITEMS * static_cast<int>(rank) + it, r = item / OCTETS, c = (item - r * OCTETS) * 8;
+        const int r = it / OCTETS * SPLITS + static_cast<int>(rank), c = it % OCTETS * 8;
         const bool in = it < ITEMS && m0 + r < a.M && n0 + c < a.N;
         rows[i] = in ? r : -1;
         cols[i] = c;
@@ -221,13 +245,15 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         for (int h = 0; h < HALVES; ++h)
 #pragma unroll
             for (int s = 0; s < SPLITS; ++s) {
-                const uint32_t at = park0 + static_cast<uint32_t>(max(rows[i], 0) * kParkLd + h * N_TILE + cols[i]) * 4u;
+                if (rows[i] < 0) continue;
+                const uint32_t at = park0 + static_cast<uint32_t>(rows[i] * kParkLd + h * N_TILE + cols[i]) * 4u;
                 const uint32_t p = SPLITS > 1 ? mapa_shared(at, s) : at;
                 parts[i][h][s][0] = ld_cluster_v4(p);
                 parts[i][h][s][1] = ld_cluster_v4(p + 16);
             }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
+        if (rows[i] < 0) continue;
         float v[HALVES][8];
 #pragma unroll
         for (int h = 0; h < HALVES; ++h) {
@@ -240,7 +266,6 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
                 v[h][4] += y.x, v[h][5] += y.y, v[h][6] += y.z, v[h][7] += y.w;
             }
         }
-        if (rows[i] < 0) continue;
         const long long row = static_cast<long long>(m0) + rows[i];
         const int col = n0 + cols[i];
         if constexpr (L::GATED) gated_octet(a, row, col, v[0], v[HALVES - 1]);
@@ -293,7 +318,8 @@ cudaError_t split_prepare(int* clusters) {
 }
 
 template <int KIND, int SPLITS>
-cudaError_t split_go(const CUtensorMap* m, const DenseArgs& a, cudaStream_t st) {
+cudaError_t split_go(const CUtensorMap* m, const DenseArgs& a, cudaStream_t st, int* clusters) {
+    if (clusters) return split_prepare<KIND, SPLITS>(clusters);
     int limit = 0;
     cudaError_t e = split_prepare<KIND, SPLITS>(&limit);
     if (e != cudaSuccess) return e;
@@ -306,43 +332,17 @@ cudaError_t split_go(const CUtensorMap* m, const DenseArgs& a, cudaStream_t st) 
     return cudaLaunchKernelEx(&cfg, dense_split_kernel<KIND, SPLITS>, m[0], m[1], m[2], m[3], a);
 }
 
-template <int KIND>
-cudaError_t split_pick(const CUtensorMap* m, const DenseArgs& a, int splits, cudaStream_t st) {
-    switch (splits) {
-        case 1: return split_go<KIND, 1>(m, a, st);
-        case 2: return split_go<KIND, 2>(m, a, st);
-        case 4: return split_go<KIND, 4>(m, a, st);
-        default: return split_go<KIND, 8>(m, a, st);
-    }
-}
-
-template <int KIND>
-cudaError_t split_limit(int splits, int* clusters) {
-    switch (splits) {
-        case 1: return split_prepare<KIND, 1>(clusters);
-        case 2: return split_prepare<KIND, 2>(clusters);
-        case 4: return split_prepare<KIND, 4>(clusters);
-        default: return split_prepare<KIND, 8>(clusters);
-    }
-}
-
 }  // namespace
 
-cudaError_t dense_split_limit(DenseKind kind, int splits, int* clusters) {
-    switch (kind) {
-        case DENSE_GATED: return split_limit<DENSE_GATED>(splits, clusters);
-        case DENSE_LINEAR: return split_limit<DENSE_LINEAR>(splits, clusters);
-        case DENSE_DGRAD: return split_limit<DENSE_DGRAD>(splits, clusters);
-        default: return split_limit<DENSE_WGRAD>(splits, clusters);
-    }
-}
-
-cudaError_t launch_dense_split(DenseKind kind, const CUtensorMap* m, const DenseArgs& a, int splits, cudaStream_t st) {
-    switch (kind) {
-        case DENSE_GATED: return split_pick<DENSE_GATED>(m, a, splits, st);
-        case DENSE_LINEAR: return split_pick<DENSE_LINEAR>(m, a, splits, st);
-        case DENSE_DGRAD: return split_pick<DENSE_DGRAD>(m, a, splits, st);
-        default: return split_pick<DENSE_WGRAD>(m, a, splits, st);
+// clusters != NULL asks only for how many the device holds at once.
+template <int KIND>
+cudaError_t dense_split_pick(const CUtensorMap* m, const DenseArgs& a, int splits, cudaStream_t st, int* clusters) {
+    switch (splits) {
+        case 1: return split_go<KIND, 1>(m, a, st, clusters);
+        case 2: return split_go<KIND, 2>(m, a, st, clusters);
+        case 4: return split_go<KIND, 4>(m, a, st, clusters);
+        case 8: return split_go<KIND, 8>(m, a, st, clusters);
+        default: return cudaErrorInvalidConfiguration;
     }
 }
 

@@ -1,0 +1,10 @@
+// dense_gemm_split_wgrad.cu -- the weight gradients on split one-CTA tiles (dense_gemm_split.cuh).
+#include "dense_gemm_split.cuh"
+
+namespace moe {
+
+cudaError_t dense_split_wgrad(const CUtensorMap* m, const DenseArgs& a, int splits, cudaStream_t st, int* clusters) {
+    return dense_split_pick<DENSE_WGRAD>(m, a, splits, st, clusters);
+}
+
+}  // namespace moe

@@ -140,9 +140,9 @@ SHAPES = [(1, 8, 8), (1, 2048, 768), (3, 72, 200), (8, 1000, 264), (9, 1024, 40)
           (127, 64, 136), (128, 1024, 256), (129, 2056, 328), (300, 776, 520), (513, 136, 1288), (700, 4104, 400)]
 
 
-#: the plan's choice; one-CTA tiles with 1, 2 or 8 CTAs over K; CTA pairs; two pairs that share an operand
-KERNELS = {"plan": {}, "split1": dict(KERNEL="1", SPLITS="1"), "split2": dict(KERNEL="1", SPLITS="2"),
-           "split8": dict(KERNEL="1", SPLITS="8"), "pair": dict(KERNEL="2", CLUSTER="2"), "pairs4": dict(KERNEL="2", CLUSTER="4")}
+#: the plan's choice; one-CTA tiles and pair tiles (bn * 10) with parts of K; persistent pairs; two pairs that share an operand
+KERNELS = {"plan": {}} | {f"split{c}": dict(KERNEL="1", SPLIT=c) for c in ("1", "2", "8", "1281", "1282", "1284", "2561", "2562", "2564")} | {
+           "pair": dict(KERNEL="2", CLUSTER="2"), "pairs4": dict(KERNEL="2", CLUSTER="4")}
 
 
 @pytest.fixture(params=list(KERNELS))
@@ -245,6 +245,20 @@ def test_activation_slopes(moe, fn):
     got = moe.moe_gated_linear_backward(dy, x, w, w3, z, u, fn=R.FNS[fn])
     for t, (ref, bound), name in zip(got, R.gated_backward(dy, x, w, w3, z, u, fn), ("dx", "dw1", "dw3")):
         assert_within(t, ref, bound, name)
+
+
+@pytest.mark.parametrize("fn", sorted(R.FNS))
+def test_slopes_in_fp32(moe, fn):
+    """One row: dbias is the fp32 slope itself, over the whole range of z."""
+    z = torch.linspace(-18, 18, 16384, device="cuda").to(BF16)[None]
+    f = z.shape[1]
+    x, w, dy = torch.ones(1, 8, device="cuda", dtype=BF16), torch.zeros(f, 8, device="cuda", dtype=BF16), torch.ones_like(z)
+    _, _, db = moe.moe_linear_backward(dy, x, w, z=z, fn=R.FNS[fn], need_dbias=True)
+    assert_within(db, R.slope(z.double(), fn)[0], R.ACT_EPS * (1 + z.double().abs())[0], fn)
+    # the value, through the gated product's gradient du = dh fn(g), whose sums over one row are the values in bf16
+    got = moe.moe_gated_linear_backward(dy, x, w, w, z, torch.zeros_like(z), R.FNS[fn])[2]
+    ref = R.act(z.double(), fn)[0][:, None].expand(f, 8)
+    assert_within(got, ref, 4 * R.H * ref.abs() + R.ACT_EPS * z.double().abs()[0][:, None], fn)
 
 
 def test_extreme_pre_activations(moe):
