@@ -96,16 +96,18 @@ BackwardLayout backward_layout(int N, int F, int grads, int parts) {
 uint8_t* at(void* ws, size_t off) { return static_cast<uint8_t*>(ws) + off; }
 
 // ---- the choice of kernel ----
-// Estimated microseconds, fitted to measured times (33 to 4096 rows, K 1024 to
-// 14336): k-blocks (64 of K) a round times the time of one, plus the round's
-// first load, join and epilogue.
+// Estimated microseconds, fitted to times measured on GB300 over 33 to 4096 rows
+// and K of 768 to 16384 (within about 10 % of each): rounds over the clusters
+// that fit the device, each k-blocks (64 of K) times the time of one, plus first
+// load, join and epilogue.
 struct TileKind {
-    int bn;          // 0: one CTA, 128 x 128; else a pair, 256 x bn
-    double block, round;
+    int bn;                        // 0: one CTA, 128 x 128; else a pair, 256 x bn
+    double block, whole, joined;   // a k-block; the rest of a round with K whole or in parts
 };
-constexpr TileKind kSplitTiles[3] = {{0, 0.25, 5.0}, {128, 0.20, 5.5}, {256, 0.30, 6.0}};
-// persistent pairs: 0.97 of the block where two pairs share an operand
-constexpr double kPairBlock = 0.34, kPairRound = 3.0, kPairOnce = 3.0, kMulticastRate = 0.97;
+constexpr TileKind kSplitTiles[3] = {{0, 0.244, 4.2, 4.5}, {128, 0.206, 6.4, 7.2}, {256, 0.294, 8.0, 10.3}};
+constexpr double kJoinRows = 2.5, kJoinEight = 1.0;  // one-CTA tiles: a join of all 128 rows, of eight parts
+constexpr double kPairBlock = 0.32, kPairRound = 1.5, kPairOnce = 4.5;  // persistent pairs
+constexpr double kMulticastRate = 0.97;              // of the block, where two pairs share an operand
 
 struct Plan {
     int bn, splits;         // split tiles
@@ -134,7 +136,9 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
             int limit = 0;
             const moe_status st = launched(dense_split(kind, nullptr, a, t.bn, s, nullptr, &limit), "dense split limit");
             if (st != MOE_OK) return st;
-            const double c = static_cast<double>((tiles + limit - 1) / limit) * (kblocks * t.block / s + t.round);
+            double rest = s == 1 ? t.whole : t.joined;
+            if (s > 1 && t.bn == 0) rest += kJoinRows * std::min(a.M, kBM) / kBM + (s == 8 ? kJoinEight : 0.0);
+            const double c = static_cast<double>((tiles + limit - 1) / limit) * (kblocks * t.block / s + rest);
             if (c < best) {
                 best = c;
                 p->bn = t.bn;

@@ -152,7 +152,10 @@ __device__ __forceinline__ void gated_octet(const DenseArgs& a, long long row, i
                                             const float (&u)[8]) {
     float h[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = act_value(a.fn, g[j]) * u[j];
+    for (int j = 0; j < 8; ++j) h[j] = g[j];
+    act_values(a.fn, h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] *= u[j];
     *octet(a.out0, row, a.N, col) = pack_bf16x8(h);
     if (a.out1) *octet(a.out1, row, a.N, col) = pack_bf16x8(g);
     if (a.out2) *octet(a.out2, row, a.N, col) = pack_bf16x8(u);
@@ -167,10 +170,7 @@ __device__ __forceinline__ void linear_octet(const DenseArgs& a, long long row, 
         z[4] += b1.x, z[5] += b1.y, z[6] += b1.z, z[7] += b1.w;
     }
     if (a.out1) *octet(a.out1, row, a.N, col) = pack_bf16x8(z);
-    if (a.fn != FN_NONE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] = act_value(a.fn, z[j]);
-    }
+    act_values(a.fn, z);
     if (a.residual) {
         float r[8];
         unpack_bf16x8(res, r);
@@ -234,8 +234,9 @@ struct RowChunk {
 __device__ __forceinline__ void gated_chunk(const DenseArgs& a, const RowChunk& c, float (&g)[32], float (&u)[32]) {
     if (a.out1) c.store(a.out1, g);
     if (a.out2) c.store(a.out2, u);
+    act_values(a.fn, g);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) g[j] = act_value(a.fn, g[j]) * u[j];
+    for (int j = 0; j < 32; ++j) g[j] *= u[j];
     c.store(a.out0, g);
 }
 
@@ -251,10 +252,7 @@ __device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk&
         }
     }
     if (a.out1) c.store(a.out1, z);
-    if (a.fn != FN_NONE) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) z[j] = act_value(a.fn, z[j]);
-    }
+    act_values(a.fn, z);
     if (a.residual) {
         uint4 row[4];
         c.to_row(res, row);
@@ -267,6 +265,35 @@ __device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk&
         }
     }
     c.store(a.out0, z);
+}
+
+// The epilogue of a whole accumulator of 128 rows x BN columns by eight warps:
+// warp (q, half) takes lanes 32 q .. and half of the output columns.
+template <int KIND, int BN>
+__device__ __forceinline__ void whole_epilogue(const DenseArgs& a, int mat, uint32_t tmem, uint8_t* chunk_smem, int m0,
+                                               int n0, int q, int half, int lane) {
+    constexpr bool GATED = DenseLayout<KIND>::GATED;
+    constexpr int COLS = GATED ? BN / 4 : BN / 2;  // output columns of a warp
+    const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * COLS);
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += 32) {
+        float v[32];
+        const RowChunk chunk{chunk_smem, static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M, a.N, lane};
+        if constexpr (KIND == DENSE_LINEAR) {
+            uint4 res[4];
+            if (a.residual) chunk.fetch(a.residual, res);
+            tmem_row(t + c, v);
+            linear_chunk(a, chunk, v, res);
+        } else if constexpr (GATED) {
+            float u[32];
+            tmem_row(t + c, v);
+            tmem_row(t + BN / 2 + c, u);
+            gated_chunk(a, chunk, v, u);
+        } else {
+            tmem_row(t + c, v);
+            chunk.store(mat ? a.out1 : a.out0, v);
+        }
+    }
 }
 
 }  // namespace moe

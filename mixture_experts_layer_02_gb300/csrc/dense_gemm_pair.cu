@@ -230,7 +230,6 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         // epilogue warp (q, half): TMEM lanes 32 q .., accumulator columns [0, 128) or [128, 256);
         // gated: 64 gate columns and the 64 up columns that belong to them
         const int q = warp & 3, half = (warp - 2) >> 2;
-        const int col0 = L::GATED ? half * 64 : half * 128;
         uint8_t* stage_smem = smem + S * kStageBytes + (warp - 2) * kChunkBytes;
         int acc = 0;
         uint32_t acc_phase = 0;
@@ -240,27 +239,8 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             __syncwarp();
             if (!named_barrier_and(1, kEpiWarps * 32, ok)) break;  // given up: by all of them
             tc_fence_after();
-            const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * kPairTile);
-            const long long row0 = static_cast<long long>(w.m0) + crank * kBM + q * 32;
-#pragma unroll 1
-            for (int c = 0; c < (L::GATED ? 2 : 4); ++c) {
-                float v[32];
-                const RowChunk chunk{stage_smem, row0, w.n0 + col0 + c * 32, a.M, a.N, lane};
-                if constexpr (KIND == DENSE_LINEAR) {
-                    uint4 res[4];
-                    if (a.residual) chunk.fetch(a.residual, res);
-                    tmem_row(t + col0 + c * 32, v);
-                    linear_chunk(a, chunk, v, res);
-                } else if constexpr (L::GATED) {
-                    float u[32];
-                    tmem_row(t + col0 + c * 32, v);
-                    tmem_row(t + 128 + col0 + c * 32, u);
-                    gated_chunk(a, chunk, v, u);
-                } else {
-                    tmem_row(t + col0 + c * 32, v);
-                    chunk.store(w.mat ? a.out1 : a.out0, v);
-                }
-            }
+            whole_epilogue<KIND, kPairTile>(a, w.mat, tmem_base + static_cast<uint32_t>(acc * kPairTile), stage_smem,
+                                            w.m0 + static_cast<int>(crank) * kBM, w.n0, q, half, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * acc);

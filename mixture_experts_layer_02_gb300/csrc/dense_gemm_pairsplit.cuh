@@ -11,8 +11,7 @@
 // a cluster barrier each CTA adds every S-th of its 128 rows over the S parked
 // copies, in order, through distributed shared memory, and runs the epilogue.
 //
-// Roles and bounded waits as in dense_gemm_split.cuh, but all eight warps park
-// (0..3 the second half of the columns); full is the even CTA's and counts
+// Roles and bounded waits as in dense_gemm_split.cuh, with BN columns; full is the even CTA's and counts
 // both CTAs' bytes, empty and done are multicast commits to both.
 #pragma once
 
@@ -185,22 +184,34 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
     }
     __syncwarp();
     __syncthreads();  // the accumulator is complete (or the product was given up)
-    {
-        const bool ok = *abort_flag == 0;
-        tc_fence_after();
-        if (ok) {
-            const int q = warp & 3, c0 = warp < 4 ? BN / 2 : 0;
-            float* row = park + (q * 32 + lane) * C::PARK_LD + c0;
-            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c0);
+    const bool ok = *abort_flag == 0;
+    tc_fence_after();
+    const int q = warp & 3, half = warp >> 2;  // TMEM lanes 32 q .., columns of this half
+    if constexpr (SPLITS == 1) {
+        // nothing to join: from TMEM through the epilogue, 32 x 32 at a time
+        if (ok) whole_epilogue<KIND, BN>(a, mat, tmem, smem + warp * kChunkBytes, m0, n0, q, half, lane);
+        __syncwarp();
+        pdl_trigger();
+        tc_fence_before();
+        __syncthreads();
+        cluster_sync_all();  // neither CTA leaves while the other may still signal it
+        if (warp == 1) {
+            tc_fence_after();
+            tmem_dealloc_pair(tmem, BN);
+        }
+        return;
+    }
+    if (ok) {
+        float* row = park + (q * 32 + lane) * C::PARK_LD + half * (BN / 2);
+        const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * (BN / 2));
 #pragma unroll
-            for (int c = 0; c < BN / 2; c += 32) {
-                uint32_t r[32];
-                tmem_ld_32x32(t + c, r);
-                tmem_ld_wait();
+        for (int c = 0; c < BN / 2; c += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32(t + c, r);
+            tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<uint4*>(row + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-            }
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<uint4*>(row + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
         }
     }
     __syncwarp();

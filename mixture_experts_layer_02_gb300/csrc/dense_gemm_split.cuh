@@ -23,9 +23,9 @@
 //     leave the join to one of them).
 //
 // Warp roles: 0 copies A, 2 copies B (one thread issuing both took longer than a
-// k-block's MMAs), 1 allocates TMEM and issues the MMAs, 4..7 park the
-// accumulator (warp q reads TMEM lanes 32 q ..), all eight warps the join and
-// epilogue.
+// k-block's MMAs), 1 allocates TMEM and issues the MMAs; all eight
+// park the accumulator (warp w reads TMEM lanes 32 (w % 4) .. and columns 64
+// (w / 4) ..), join and run the epilogue.
 //
 // Every wait is bounded (mbar_wait); whatever a role sees, every thread reaches
 // both cluster barriers, so no CTA waits for one that left.
@@ -190,22 +190,33 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
     }
     __syncwarp();
     __syncthreads();  // the accumulator is complete (or the product was given up)
-    if (warp >= 4) {
-        const bool ok = *abort_flag == 0;
-        tc_fence_after();
-        if (ok) {
-            const int q = warp & 3;
-            float* row = park + (q * 32 + lane) * kParkLd;
-            const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const bool ok = *abort_flag == 0;
+    tc_fence_after();
+    const int q = warp & 3, half = warp >> 2;  // TMEM lanes 32 q .., columns of this half
+    if constexpr (SPLITS == 1) {
+        // nothing to join: from TMEM through the epilogue, 32 x 32 at a time
+        if (ok) whole_epilogue<KIND, kSplitBN>(a, mat, tmem, smem + warp * kChunkBytes, m0, n0, q, half, lane);
+        __syncwarp();
+        pdl_trigger();
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 1) {
+            tc_fence_after();
+            tmem_dealloc(tmem, kSplitBN);
+        }
+        return;
+    }
+    if (ok) {
+        float* row = park + (q * 32 + lane) * kParkLd + half * (kSplitBN / 2);
+        const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * (kSplitBN / 2));
 #pragma unroll
-            for (int c = 0; c < kSplitBN; c += 32) {
-                uint32_t r[32];
-                tmem_ld_32x32(t + c, r);
-                tmem_ld_wait();
+        for (int c = 0; c < kSplitBN / 2; c += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32(t + c, r);
+            tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<uint4*>(row + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-            }
+            for (int j = 0; j < 32; j += 4)
+                *reinterpret_cast<uint4*>(row + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
         }
     }
     // This CTA's share of the join: every SPLITS-th row, 16 (gated: 8) octets a row

@@ -128,11 +128,15 @@ dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
         if constexpr (GATED) {
             if (a.out1) put(a.out1, z);
             if (a.out2) put(a.out2, u);
-            put(a.out0, act_value(a.fn, z) * u);
+            float v[1] = {z};
+            act_values(a.fn, v);
+            put(a.out0, v[0] * u);
         } else {
             if (a.bias) z += a.bias[col];
             if (a.out1) put(a.out1, z);
-            z = act_value(a.fn, z);
+            float v[1] = {z};
+            act_values(a.fn, v);
+            z = v[0];
             if (a.residual) z += __uint_as_float(static_cast<uint32_t>(a.residual[at]) << 16);
             put(a.out0, z);
         }

@@ -33,14 +33,14 @@ gated_grad_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ g, con
         unpack_bf16x8(dh[i], h);
         unpack_bf16x8(g[i], a);
         unpack_bf16x8(u[i], b);
+        float slope[8];
+        act_slopes(fn, a, slope);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float value;
-            const float slope = act_slope(fn, a[j], value);
-            a[j] = h[j] * b[j] * slope;
-            b[j] = h[j] * value;
+            slope[j] *= h[j] * b[j];
+            b[j] = h[j] * a[j];
         }
-        dg[i] = pack_bf16x8(a);
+        dg[i] = pack_bf16x8(slope);
         du[i] = pack_bf16x8(b);
     }
     pdl_trigger();
@@ -67,11 +67,10 @@ linear_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__
             if (fn != FN_NONE) {
                 float v[8];
                 unpack_bf16x8(*reinterpret_cast<const uint4*>(z + at), v);
+                float slope[8];
+                act_slopes(fn, v, slope);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float value;
-                    d[j] *= act_slope(fn, v[j], value);
-                }
+                for (int j = 0; j < 8; ++j) d[j] *= slope[j];
                 *reinterpret_cast<uint4*>(dz + at) = pack_bf16x8(d);
             }
 #pragma unroll
