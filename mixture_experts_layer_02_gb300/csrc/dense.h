@@ -43,18 +43,13 @@ struct NormBwdArgs {
 int rmsnorm_bwd_parts(long long rows, int D);
 cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t st);
 
-// out[c] = sum over p (in order) of partial[p][c].
-cudaError_t launch_column_sums(const float* partial, int parts, int cols, float* out, cudaStream_t st);
-
 // ---- elementwise halves of the gradients (dense_grad.cu) ----
 // dg = dh u act'(g), du = dh act(g) over n values (n % 8 == 0).
 cudaError_t launch_gated_grad(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int fn, long long n,
                               uint16_t* dg, uint16_t* du, cudaStream_t st);
-// dz = dy act'(z) (dz NULL: not stored) and, where dbias is set, dbias = the column sums of the unrounded dz
-// through partial [linear_grad_parts(rows)][cols].
-int linear_grad_parts(long long rows);
+// dz = dy act'(z) (FN_NONE: not stored) and, where dbias is set, dbias = the column sums of the unrounded dz.
 cudaError_t launch_linear_grad(const uint16_t* dy, const uint16_t* z, int fn, long long rows, int cols, uint16_t* dz,
-                               float* dbias, float* partial, cudaStream_t st);
+                               float* dbias, cudaStream_t st);
 
 // ---- tensor-core products (dense_gemm*.cu) ----
 // out[m, n] = sum_k A[m, k] B[n, k], bf16 operands, fp32 accumulation.  Each

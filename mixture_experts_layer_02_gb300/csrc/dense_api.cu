@@ -80,16 +80,15 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // byte offsets of the backward workspaces (the header first)
 struct BackwardLayout {
-    size_t d0, d1, partial, total;
+    size_t d0, d1, total;
 };
 
-BackwardLayout backward_layout(int N, int F, int grads, int parts) {
+BackwardLayout backward_layout(int N, int F, int grads) {
     BackwardLayout l;
     const size_t one = up256(static_cast<size_t>(N) * F * 2);
     l.d0 = kWsHeaderBytes;
     l.d1 = l.d0 + one;
-    l.partial = l.d0 + one * grads;
-    l.total = l.partial + up256(static_cast<size_t>(parts) * F * sizeof(float));
+    l.total = l.d0 + one * grads;
     return l;
 }
 
@@ -225,7 +224,7 @@ size_t moe::dense_workspace_size(const char* op, int N, int D, int F) {
         return check_widths(N, D, F) == MOE_OK ? kWsHeaderBytes : 0;
     if (!gated && strcmp(op, "linear_backward")) return 0;
     if (check_widths(N, D, F) != MOE_OK) return 0;
-    return backward_layout(N, F, gated ? 2 : 1, gated ? 0 : linear_grad_parts(N)).total;
+    return backward_layout(N, F, gated ? 2 : 1).total;
 }
 
 extern "C" {
@@ -310,7 +309,7 @@ moe_status moe_gated_linear_backward(const moe_bf16* dh, const moe_bf16* x, cons
     NEED(w3);
     NEED(g);
     NEED(u);
-    const BackwardLayout l = backward_layout(N, F, 2, 0);
+    const BackwardLayout l = backward_layout(N, F, 2);
     NEED_WS(l.total);
     uint16_t* dg = reinterpret_cast<uint16_t*>(at(ws, l.d0));
     uint16_t* du = reinterpret_cast<uint16_t*>(at(ws, l.d1));
@@ -371,10 +370,10 @@ moe_status moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, const moe_
     NEED(x);
     NEED(w);
     if (fn != MOE_FN_NONE) NEED(z);
-    const BackwardLayout l = backward_layout(N, F, 1, linear_grad_parts(N));
+    const BackwardLayout l = backward_layout(N, F, 1);
     NEED_WS(l.total);
     uint16_t* dz = reinterpret_cast<uint16_t*>(at(ws, l.d0));
-    s = launched(launch_linear_grad(dy, z, fn, N, F, dz, dbias, reinterpret_cast<float*>(at(ws, l.partial)), st),
+    s = launched(launch_linear_grad(dy, z, fn, N, F, dz, dbias, st),
                  "linear gradient launch");
     const uint16_t* grad = fn == MOE_FN_NONE ? dy : dz;
     if (s == MOE_OK && dx) {

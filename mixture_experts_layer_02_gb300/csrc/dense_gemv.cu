@@ -69,10 +69,21 @@ dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    pdl_wait();
-    pdl_trigger();
-
     const int steps = (K + 63) >> 6;
+    // The first steps' weights start their way into L2 while the kernel before
+    // this one drains (L2 is coherent: if it writes them, the loads see that).
+    if (t == 0)
+#pragma unroll
+        for (int b = 0; b < kGemvBatch; ++b) {
+            const int k = (warp + b * kGemvWarps) * 64;
+            if (k < K) {
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(lo + k));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(hi + k));
+            }
+        }
+    pdl_trigger();
+    pdl_wait();
+
     const uint4 zero = make_uint4(0, 0, 0, 0);
     for (int s0 = warp; s0 < steps; s0 += kGemvWarps * kGemvBatch) {
         uint4 wl[kGemvBatch][2], wh[kGemvBatch][2], xv[kGemvBatch][NT][2];

@@ -476,10 +476,6 @@ column_sums_kernel(const float* __restrict__ partial, int parts, int cols, float
     pdl_trigger();
 }
 
-cudaError_t launch_column_sums(const float* partial, int parts, int cols, float* out, cudaStream_t st) {
-    return launch_kernel(column_sums_kernel, dim3((cols + 31) / 32), dim3(1024), 0, st, partial, parts, cols, out);
-}
-
 int rmsnorm_bwd_parts(long long rows, int D) { return norm_bwd_shape(rows, D).grid; }
 
 namespace {
@@ -512,7 +508,7 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, cudaStream_t st) {
     else if (s.v == 2) e = ring_go<2>(a, s, st);
     else e = ring_go<4>(a, s, st);
     if (e != cudaSuccess || !a.dweight) return e;
-    return launch_column_sums(a.partial, s.grid, a.D, a.dweight, st);
+    return launch_kernel(column_sums_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, st, a.partial, s.grid, a.D, a.dweight);
 }
 
 }  // namespace moe
