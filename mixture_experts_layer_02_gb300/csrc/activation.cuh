@@ -16,6 +16,26 @@ enum { FN_NONE = 0, FN_RELU = 1, FN_SILU = 2, FN_GELU = 3, FN_GELU_TANH = 4 };
 constexpr float kGeluTanh2 = 1.5957691216057308f;
 constexpr float kGeluCubic = 0.044715f;
 
+// Two fp32 operations in one instruction, each rounded as alone.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // The normal distribution function Phi(z); `e` gets exp(-z^2 / 2) (its density
 // times sqrt(2 pi)).  For x = |z| / sqrt 2, erfc(x) = exp(-x^2) erfcx(x), and
 // erfcx(x) is t P(t) with t = 1 / (1 + 0.4 x): P is the polynomial of degree 8
@@ -24,27 +44,27 @@ constexpr float kGeluCubic = 0.044715f;
 // holds far into the negative tail, where 1 + erf would cancel, and one
 // exponential serves the value and the slope.  erfcf took 2.5 times the
 // instructions, and a gelu epilogue or gradient was bound by them.
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-    const float t = __fdividef(1.0f, fmaf(0.28284271247461903f, fabsf(z), 1.0f));
-    float p = 0.0459682680666447f;
-    p = fmaf(p, t, -0.1630595624446869f);
-    p = fmaf(p, t, 0.1304987967014313f);
-    p = fmaf(p, t, 0.0354329086840153f);
-    p = fmaf(p, t, 0.1154701560735703f);
-    p = fmaf(p, t, 0.1784794181585312f);
-    p = fmaf(p, t, 0.2056105583906174f);
-    p = fmaf(p, t, 0.2259367406368256f);
-    p = fmaf(p, t, 0.2256629019975662f);
-    e = __expf(-0.5f * z * z);
-    const float tail = 0.5f * e * (p * t);
-    return z >= 0.0f ? 1.0f - tail : tail;
+// Two at a time.
+__device__ __forceinline__ float2 normal_cdf2(float2 z, float2& e) {
+    auto pair = [](float v) { return make_float2(v, v); };
+    const float2 d = fma2(pair(0.28284271247461903f), make_float2(fabsf(z.x), fabsf(z.y)), pair(1.0f));
+    const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y));
+    float2 p = pair(0.0459682680666447f);
+    p = fma2(p, t, pair(-0.1630595624446869f));
+    p = fma2(p, t, pair(0.1304987967014313f));
+    p = fma2(p, t, pair(0.0354329086840153f));
+    p = fma2(p, t, pair(0.1154701560735703f));
+    p = fma2(p, t, pair(0.1784794181585312f));
+    p = fma2(p, t, pair(0.2056105583906174f));
+    p = fma2(p, t, pair(0.2259367406368256f));
+    p = fma2(p, t, pair(0.2256629019975662f));
+    const float2 h = mul2(mul2(z, z), pair(-0.5f));
+    e = make_float2(__expf(h.x), __expf(h.y));
+    const float2 tail = mul2(mul2(e, pair(0.5f)), mul2(p, t));
+    return make_float2(z.x >= 0.0f ? 1.0f - tail.x : tail.x, z.y >= 0.0f ? 1.0f - tail.y : tail.y);
 }
 
 __device__ __forceinline__ float act_relu(float z) { return z <= 0.0f ? 0.0f : z; }  // a NaN stays one
-__device__ __forceinline__ float act_gelu(float z) {
-    float e;
-    return z * normal_cdf(z, e);
-}
 __device__ __forceinline__ float act_gelu_tanh(float z) {
     return __fdividef(z, 1.0f + __expf(-kGeluTanh2 * (z + kGeluCubic * z * z * z)));
 }
@@ -60,7 +80,13 @@ __device__ __forceinline__ void act_values(int fn, float (&z)[N]) {
         for (int j = 0; j < N; ++j) z[j] = silu_f32(z[j]);
     } else if (fn == FN_GELU) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) z[j] = act_gelu(z[j]);
+        for (int j = 0; j < N; j += 2) {
+            float2 e;
+            const float2 v = make_float2(z[j], z[(j + 1) % N]);
+            const float2 r = mul2(v, normal_cdf2(v, e));
+            z[j] = r.x;
+            if (j + 1 < N) z[(j + 1) % N] = r.y;
+        }
     } else if (fn == FN_GELU_TANH) {
 #pragma unroll
         for (int j = 0; j < N; ++j) z[j] = act_gelu_tanh(z[j]);
@@ -80,9 +106,10 @@ __device__ __forceinline__ float sigmoid_f32(float q, float& one_minus) {
     return q >= 0.0f ? r : small;
 }
 
-// slope[j] = fn'(z[j]) and z[j] = fn(z[j]).
+// slope[j] = fn'(z[j]) and z[j] = fn(z[j]), N even.
 template <int N>
 __device__ __forceinline__ void act_slopes(int fn, float (&z)[N], float (&slope)[N]) {
+    static_assert(N % 2 == 0, "pairs");
     if (fn == FN_SILU) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -93,11 +120,16 @@ __device__ __forceinline__ void act_slopes(int fn, float (&z)[N], float (&slope)
         }
     } else if (fn == FN_GELU) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            float e;
-            const float c = normal_cdf(z[j], e);
-            slope[j] = c + z[j] * 0.3989422804014327f * e;  // 1/sqrt(2 pi)
-            z[j] *= c;
+        for (int j = 0; j < N; j += 2) {
+            float2 e;
+            const float2 v = make_float2(z[j], z[j + 1]);
+            const float2 c = normal_cdf2(v, e);
+            const float2 s = fma2(mul2(v, make_float2(0.3989422804014327f, 0.3989422804014327f)), e, c);  // 1/sqrt(2 pi)
+            const float2 r = mul2(v, c);
+            slope[j] = s.x;
+            slope[j + 1] = s.y;
+            z[j] = r.x;
+            z[j + 1] = r.y;
         }
     } else if (fn == FN_GELU_TANH) {
 #pragma unroll

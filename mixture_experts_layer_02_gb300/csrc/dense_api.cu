@@ -103,7 +103,7 @@ struct TileKind {
     int bn;                        // 0: one CTA, 128 x 128; else a pair, 256 x bn
     double block, whole, joined;   // a k-block; the rest of a round with K whole or in parts
 };
-constexpr TileKind kSplitTiles[3] = {{0, 0.244, 4.2, 4.5}, {128, 0.206, 6.4, 7.2}, {256, 0.294, 8.0, 10.3}};
+constexpr TileKind kSplitTiles[3] = {{0, 0.24, 3.6, 4.5}, {128, 0.206, 5.0, 7.2}, {256, 0.30, 5.0, 10.3}};
 constexpr double kJoinRows = 2.5, kJoinEight = 1.0;  // one-CTA tiles: a join of all 128 rows, of eight parts
 constexpr double kPairBlock = 0.32, kPairRound = 1.5, kPairOnce = 4.5;  // persistent pairs
 constexpr double kMulticastRate = 0.97;              // of the block, where two pairs share an operand

@@ -53,7 +53,7 @@ gated_grad_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ g, con
 // (which took 3 us of the 10 at 777 x 4096).
 constexpr int kGradParts = 8;
 
-__global__ void __cluster_dims__(1, kGradParts, 1) __launch_bounds__(kGradThreads)
+__global__ void __cluster_dims__(1, kGradParts, 1) __launch_bounds__(kGradThreads, 4)
 linear_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int fn, long long rows, int cols,
                    uint16_t* __restrict__ dz, float* __restrict__ dbias) {
     __shared__ float s_warp[kGradThreads / 32][64];
@@ -63,19 +63,26 @@ linear_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__
     const int col = blockIdx.x * 64 + tx * 8;
     const long long r0 = rows * blockIdx.y / kGradParts, r1 = rows * (blockIdx.y + 1) / kGradParts;
     float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    // the next row's loads are issued before this row's arithmetic
+    uint4 dn = make_uint4(0, 0, 0, 0), zn = dn;
+    auto fetch = [&](long long r) {
+        if (r >= r1) return;
+        dn = *reinterpret_cast<const uint4*>(dy + r * cols + col);
+        if (fn != FN_NONE) zn = *reinterpret_cast<const uint4*>(z + r * cols + col);
+    };
     if (col < cols) {
-#pragma unroll 2
+        fetch(r0 + ty);
         for (long long r = r0 + ty; r < r1; r += 32) {
-            const long long at = r * cols + col;
-            float d[8];
-            unpack_bf16x8(*reinterpret_cast<const uint4*>(dy + at), d);
+            float d[8], v[8];
+            unpack_bf16x8(dn, d);
+            unpack_bf16x8(zn, v);
+            fetch(r + 32);
             if (fn != FN_NONE) {
-                float v[8], slope[8];
-                unpack_bf16x8(*reinterpret_cast<const uint4*>(z + at), v);
+                float slope[8];
                 act_slopes(fn, v, slope);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d[j] *= slope[j];
-                *reinterpret_cast<uint4*>(dz + at) = pack_bf16x8(d);
+                *reinterpret_cast<uint4*>(dz + r * cols + col) = pack_bf16x8(d);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[j] += d[j];
