@@ -114,7 +114,7 @@ inline cudaError_t dense_split(DenseKind kind, const CUtensorMap* m, const Dense
 }
 
 // A few rows (DENSE_GATED, DENSE_LINEAR; M <= kGemvMaxRows): one pass over the weights.
-constexpr int kGemvMaxRows = 16;
+constexpr int kGemvMaxRows = 32;
 cudaError_t launch_dense_gemv(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st);
 
 // CTA pairs on 256 x 256 tiles, persistent: clusters of one pair (cluster = 2)

@@ -107,10 +107,15 @@ constexpr TileKind kSplitTiles[3] = {{0, 0.24, 3.6, 4.5}, {128, 0.206, 5.0, 7.2}
 constexpr double kJoinRows = 2.5, kJoinEight = 1.0;  // one-CTA tiles: a join of all 128 rows, of eight parts
 constexpr double kPairBlock = 0.32, kPairRound = 1.5, kPairOnce = 4.5;  // persistent pairs
 constexpr double kMulticastRate = 0.97;              // of the block, where two pairs share an operand
+// The streamed form (M <= kGemvMaxRows) reads x once a block of 16 weight rows:
+// weights at the HBM rate, or weights and x at the L2 rate that 240 blocks and
+// more reach, whichever takes longer.  MB a microsecond is TB a second.
+constexpr double kHbmRate = 6.3, kGemvL2Rate = 10.0, kGemvBlocks = 240.0, kGemvOnce = 2.4;
 
 struct Plan {
     int bn, splits;         // split tiles
     int cluster, clusters;  // persistent pairs (cluster 0: split tiles)
+    bool stream;            // the streamed form instead
 };
 
 int env_int(const char* name, int dflt) {
@@ -124,7 +129,13 @@ int env_int(const char* name, int dflt) {
 moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p) {
     const int n2 = kind == DENSE_GATED ? 128 : 256;
     const int kernel = env_int("MOE_DENSE_KERNEL", 0), fixed = env_int("MOE_DENSE_SPLIT", -1);
-    *p = {0, 1, 0, 0};
+    *p = {0, 1, 0, 0, false};
+    const bool forward = kind == DENSE_GATED || kind == DENSE_LINEAR;
+    const double weights = 2e-6 * a.N * a.K * (kind == DENSE_GATED ? 2 : 1);  // MB
+    if (forward && a.M <= kGemvMaxRows && kernel == 3) {
+        p->stream = true;
+        return MOE_OK;
+    }
     double best = 1e30;
     for (const TileKind& t : kSplitTiles) {
         const int rows = t.bn ? 2 * kBM : kBM, width = (t.bn ? t.bn : 128) / (kind == DENSE_GATED ? 2 : 1);
@@ -137,7 +148,8 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
             if (st != MOE_OK) return st;
             double rest = s == 1 ? t.whole : t.joined;
             if (s > 1 && t.bn == 0) rest += kJoinRows * std::min(a.M, kBM) / kBM + (s == 8 ? kJoinEight : 0.0);
-            const double c = static_cast<double>((tiles + limit - 1) / limit) * (kblocks * t.block / s + rest);
+            const double rounds = static_cast<double>((tiles + limit - 1) / limit);
+            const double c = std::max(rounds * kblocks * t.block / s, forward ? weights / kHbmRate : 0.0) + rounds * rest;
             if (c < best) {
                 best = c;
                 p->bn = t.bn;
@@ -146,6 +158,15 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
         }
     }
     if (kernel == 1) return MOE_OK;
+    if (forward && a.M <= kGemvMaxRows && kernel == 0) {
+        const int blocks = (a.N + (kind == DENSE_GATED ? 7 : 15)) / (kind == DENSE_GATED ? 8 : 16);
+        const double l2 = weights + 2e-6 * blocks * a.M * a.K;
+        const double c = kGemvOnce + std::max(weights / kHbmRate, l2 / (kGemvL2Rate * std::min(1.0, blocks / kGemvBlocks)));
+        if (c < best) {
+            best = c;
+            p->stream = true;
+        }
+    }
     if (kernel == 2) best = 1e30;
     for (int cl = 2; cl <= 4; cl += 2) {
         if (env_int("MOE_DENSE_CLUSTER", cl) != cl) continue;
@@ -158,6 +179,7 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
         const double c = static_cast<double>((tiles + limit - 1) / limit) * (kblocks * block + kPairRound) + kPairOnce;
         if (c < best) {
             best = c;
+            p->stream = false;
             p->cluster = cl;
             p->clusters = static_cast<int>(std::min<long long>(tiles, limit));
         }
@@ -167,14 +189,12 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
 
 // One product: tensor maps, the choice of kernel, the launch.
 moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
-    const int kernel = env_int("MOE_DENSE_KERNEL", 0);
-    if ((kind == DENSE_GATED || kind == DENSE_LINEAR) && a.M <= kGemvMaxRows && (kernel == 0 || kernel == 3))
-        return launched(launch_dense_gemv(kind, o, a, st), "dense product launch");
     const bool a_mn = kind == DENSE_WGRAD, b_mn = kind == DENSE_DGRAD || kind == DENSE_WGRAD;
     const int kblocks = (a.K + kBK - 1) / kBK * a.segs;
     Plan p;
     const moe_status planned = plan_product(kind, a, kblocks, &p);
     if (planned != MOE_OK) return planned;
+    if (p.stream) return launched(launch_dense_gemv(kind, o, a, st), "dense product launch");
     // K-major boxes: 128 rows of A; of B what one CTA loads at a time
     const int b_rows = p.cluster ? 256 / p.cluster : (p.bn ? p.bn / 2 : (kind == DENSE_GATED ? 64 : 128));
     CUtensorMap m[4];

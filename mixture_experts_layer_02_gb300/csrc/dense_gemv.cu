@@ -31,7 +31,9 @@ namespace {
 
 constexpr int kGemvWarps = 8;
 constexpr int kGemvRows = 16;
-constexpr int kGemvBatch = 4;  // steps of 64 K loaded ahead
+// steps of 64 K loaded ahead, by groups of eight tokens: what 128 registers hold
+template <int NT>
+constexpr int kGemvBatch = NT <= 2 ? 4 : 2;
 
 __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
@@ -69,12 +71,13 @@ dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    constexpr int BATCH = kGemvBatch<NT>;
     const int steps = (K + 63) >> 6;
     // The first steps' weights start their way into L2 while the kernel before
     // this one drains (L2 is coherent: if it writes them, the loads see that).
     if (t == 0)
 #pragma unroll
-        for (int b = 0; b < kGemvBatch; ++b) {
+        for (int b = 0; b < BATCH; ++b) {
             const int k = (warp + b * kGemvWarps) * 64;
             if (k < K) {
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(lo + k));
@@ -85,10 +88,10 @@ dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
     pdl_wait();
 
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int s0 = warp; s0 < steps; s0 += kGemvWarps * kGemvBatch) {
-        uint4 wl[kGemvBatch][2], wh[kGemvBatch][2], xv[kGemvBatch][NT][2];
+    for (int s0 = warp; s0 < steps; s0 += kGemvWarps * BATCH) {
+        uint4 wl[BATCH][2], wh[BATCH][2], xv[BATCH][NT][2];
 #pragma unroll
-        for (int b = 0; b < kGemvBatch; ++b)
+        for (int b = 0; b < BATCH; ++b)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int k = (s0 + b * kGemvWarps) * 64 + j * 32 + t * 8;
@@ -97,7 +100,7 @@ dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
                 wh[b][j] = in ? ld_once(hi + k) : zero;
             }
 #pragma unroll
-        for (int b = 0; b < kGemvBatch; ++b)
+        for (int b = 0; b < BATCH; ++b)
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -108,7 +111,7 @@ dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
                                       : zero;
                 }
 #pragma unroll
-        for (int b = 0; b < kGemvBatch; ++b)
+        for (int b = 0; b < BATCH; ++b)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -164,8 +167,10 @@ cudaError_t gemv_go(const DenseOperands& o, const DenseArgs& a, cudaStream_t st)
 }  // namespace
 
 cudaError_t launch_dense_gemv(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
-    if (kind == DENSE_GATED) return a.M <= 8 ? gemv_go<true, 1>(o, a, st) : gemv_go<true, 2>(o, a, st);
-    return a.M <= 8 ? gemv_go<false, 1>(o, a, st) : gemv_go<false, 2>(o, a, st);
+    const int nt = (a.M + 7) / 8;
+    if (kind == DENSE_GATED)
+        return nt <= 1 ? gemv_go<true, 1>(o, a, st) : (nt <= 2 ? gemv_go<true, 2>(o, a, st) : gemv_go<true, 4>(o, a, st));
+    return nt <= 1 ? gemv_go<false, 1>(o, a, st) : (nt <= 2 ? gemv_go<false, 2>(o, a, st) : gemv_go<false, 4>(o, a, st));
 }
 
 }  // namespace moe

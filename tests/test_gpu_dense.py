@@ -375,6 +375,29 @@ def test_no_rows(moe):
     assert (dw == 0).all() and (db == 0).all()
 
 
+def test_more_than_two_to_the_31_elements(moe):
+    """Offsets past 32 bits: the last rows of tensors of 2.2e9 elements."""
+    n, wide, narrow = 270_001, 8192, 64
+    tail = slice(n - 3, n)
+    x, w = randn(n, narrow, seed=1), randn(wide, narrow, seed=2, scale=narrow ** -0.5)
+    y, _ = moe.moe_linear(x, w)
+    (ry, ey), _ = R.linear(x[tail], w, None, None, "none")
+    assert_within(y[tail], ry, ey, "y")
+    weight = randn(wide, seed=3) + 1
+    z, _, _, s = moe.moe_rmsnorm(y, weight, residual=y)
+    s64, z64 = R.norm(y[tail], weight, y[tail])
+    assert torch.equal(s[tail], s64.float().to(BF16))
+    assert_within(z[tail], z64, (R.H + (wide + 16) * R.U) * z64.abs(), "norm")
+    del z
+    dx, dw, db = moe.moe_linear_backward(y, x, w, z=s, fn=R.FNS["silu"], need_dbias=True)
+    (rx, ex), _, _ = R.linear_backward(y[tail], x[tail], w, s[tail], "silu")
+    assert_within(dx[tail], rx, ex, "dx")
+    assert dw.isfinite().all() and db.isfinite().all()
+    dn, _ = moe.moe_rmsnorm_backward(y, s, weight)
+    rn, _, en, _ = R.norm_backward(y[tail], s[tail], weight)
+    assert_within(dn[tail], rn, en, "norm dx")
+
+
 @pytest.mark.parametrize("fn", ["silu", "gelu"])
 def test_gradients_against_differences(moe, fn):
     """The kernels' gradients along a direction against differences of the 64-bit forward."""
