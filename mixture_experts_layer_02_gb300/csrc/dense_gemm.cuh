@@ -136,48 +136,153 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[32]) {
     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
 }
 
-// ---- fused epilogues: eight consecutive columns of one row ----
-// n % 8 == 0 for every width, so an octet is inside or outside as a whole and
-// every access is one aligned 16-byte word.
+// ---- a tile's accumulator joined over the k-parts of a cluster ----
+// Each CTA parks its accumulator (128 rows x BN fp32) in shared memory, row by
+// row, the 16-byte quads of a row permuted by its number: the parking threads
+// (one row each) and the joining warps (whole rows) both use all banks, and a
+// warp's load from another CTA is whole aligned lines (with padded rows and
+// 32-byte pieces such loads ran at 12 bytes a clock and the join took 3 us).
+template <int BN>
+__device__ __forceinline__ uint32_t park_at(int row, int quad) {
+    return static_cast<uint32_t>(row * BN * 4 + ((quad ^ (row & 7)) << 4));
+}
+
+template <int BN>
+__device__ __forceinline__ void park_rows(uint8_t* park, uint32_t tmem, int q, int half, int lane) {
+    const int row = q * 32 + lane;
+    const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * (BN / 2));
+#pragma unroll 1
+    for (int c = 0; c < BN / 2; c += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32(t + c, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(park + park_at<BN>(row, half * (BN / 8) + c / 4 + j)) =
+                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+    }
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Four consecutive columns of one row (every width is a multiple of 8, so a quad
+// is inside or outside as a whole).
+__device__ __forceinline__ uint2* quad_of(uint16_t* base, long long row, int ld, int col) {
+    return reinterpret_cast<uint2*>(base + row * ld + col);
+}
+__device__ __forceinline__ uint2 pack_quad(const float (&v)[4]) {
+    return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+
+// h = act(g) u from the fp32 accumulators (g and u are rounded only where they
+// are stored for the backward pass).
+__device__ __forceinline__ void gated_quad(const DenseArgs& a, long long row, int col, float (&g)[4], const float (&u)[4]) {
+    if (a.out1) *quad_of(a.out1, row, a.N, col) = pack_quad(g);
+    if (a.out2) *quad_of(a.out2, row, a.N, col) = pack_quad(u);
+    act_values(a.fn, g);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) g[j] *= u[j];
+    *quad_of(a.out0, row, a.N, col) = pack_quad(g);
+}
+
+// y = residual + act(acc + bias) in fp32, rounded once; `res` are the residual's four values.
+__device__ __forceinline__ void linear_quad(const DenseArgs& a, long long row, int col, float (&z)[4], const uint2& res) {
+    if (a.bias) {
+        const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + col));
+        z[0] += b.x, z[1] += b.y, z[2] += b.z, z[3] += b.w;
+    }
+    if (a.out1) *quad_of(a.out1, row, a.N, col) = pack_quad(z);
+    act_values(a.fn, z);
+    if (a.residual) {
+        z[0] += __uint_as_float(res.x << 16), z[1] += __uint_as_float(res.x & 0xffff0000u);
+        z[2] += __uint_as_float(res.y << 16), z[3] += __uint_as_float(res.y & 0xffff0000u);
+    }
+    *quad_of(a.out0, row, a.N, col) = pack_quad(z);
+}
+
+// The share of CTA `part` of `SPLITS`: every SPLITS-th row.  Thread t of 256 takes
+// quads t, t + 256, ... of those rows, in passes of up to sixteen loads, all issued
+// before the first is used; `first` + k * `step` are the ranks of the k-parts, summed
+// in order.
+template <int KIND, int BN, int SPLITS>
+__device__ __forceinline__ void join_parts(const DenseArgs& a, int mat, uint32_t park, int m0, int n0, int part,
+                                           uint32_t first, uint32_t step) {
+    constexpr bool GATED = DenseLayout<KIND>::GATED;
+    constexpr int HALVES = GATED ? 2 : 1;
+    constexpr int QN = BN / 4 / HALVES;  // output quads of a row
+    constexpr int ITEMS = kBM / SPLITS * QN;
+    constexpr int MOST = 16 / (HALVES * SPLITS), ALL = (ITEMS + 255) / 256;
+    constexpr int PER = MOST < ALL ? MOST : ALL;
+#pragma unroll 1
+    for (int base = 0; base < ITEMS; base += PER * 256) {
+        int rows[PER], cols[PER];
+        uint2 res[PER];
+        float4 parts[PER][HALVES][SPLITS];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int it = base + i * 256 + static_cast<int>(threadIdx.x);
+            const int r = it / QN * SPLITS + part, q = it % QN;
+            const bool in = it < ITEMS && m0 + r < a.M && n0 + q * 4 < a.N;
+            rows[i] = in ? r : -1;
+            cols[i] = q * 4;
+            res[i] = make_uint2(0, 0);
+            if (KIND == DENSE_LINEAR && in && a.residual)
+                res[i] = *quad_of(const_cast<uint16_t*>(a.residual), m0 + r, a.N, n0 + q * 4);
+            if (!in) continue;
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                for (int s = 0; s < SPLITS; ++s)
+                    parts[i][h][s] = ld_cluster_v4(mapa_shared(park + park_at<BN>(r, h * QN + q), first + s * step));
+        }
+        float v[PER][HALVES][4];
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+#pragma unroll
+            for (int h = 0; h < HALVES; ++h) {
+                v[i][h][0] = v[i][h][1] = v[i][h][2] = v[i][h][3] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < SPLITS; ++s) {
+                    const float4 x = parts[i][h][s];
+                    v[i][h][0] += x.x, v[i][h][1] += x.y, v[i][h][2] += x.z, v[i][h][3] += x.w;
+                }
+            }
+        // the epilogue in a rolled loop, the items moving to the front: its instructions run once a launch
+#pragma unroll 1
+        for (int n = 0; n < PER; ++n) {
+            if (rows[0] >= 0) {
+                const long long row = static_cast<long long>(m0) + rows[0];
+                const int col = n0 + cols[0];
+                if constexpr (GATED) gated_quad(a, row, col, v[0][0], v[0][HALVES - 1]);
+                else if constexpr (KIND == DENSE_LINEAR) linear_quad(a, row, col, v[0][0], res[0]);
+                else *quad_of(mat ? a.out1 : a.out0, row, a.N, col) = pack_quad(v[0][0]);
+            }
+#pragma unroll
+            for (int i = 0; i + 1 < PER; ++i) {
+                rows[i] = rows[i + 1];
+                cols[i] = cols[i + 1];
+                res[i] = res[i + 1];
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[i][h][j] = v[i + 1][h][j];
+            }
+        }
+    }
+}
+
 __device__ __forceinline__ uint4* octet(uint16_t* base, long long row, int ld, int col) {
     return reinterpret_cast<uint4*>(base + row * ld + col);
 }
 __device__ __forceinline__ const uint4* octet(const uint16_t* base, long long row, int ld, int col) {
     return reinterpret_cast<const uint4*>(base + row * ld + col);
-}
-
-// h = act(g) u from the fp32 accumulators (g and u are rounded only where they
-// are stored for the backward pass).
-__device__ __forceinline__ void gated_octet(const DenseArgs& a, long long row, int col, const float (&g)[8],
-                                            const float (&u)[8]) {
-    float h[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = g[j];
-    act_values(a.fn, h);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] *= u[j];
-    *octet(a.out0, row, a.N, col) = pack_bf16x8(h);
-    if (a.out1) *octet(a.out1, row, a.N, col) = pack_bf16x8(g);
-    if (a.out2) *octet(a.out2, row, a.N, col) = pack_bf16x8(u);
-}
-
-// y = residual + act(acc + bias) in fp32, rounded once; `res` are the residual's eight values.
-__device__ __forceinline__ void linear_octet(const DenseArgs& a, long long row, int col, float (&z)[8], const uint4& res) {
-    if (a.bias) {
-        const float4 b0 = __ldg(reinterpret_cast<const float4*>(a.bias + col));
-        const float4 b1 = __ldg(reinterpret_cast<const float4*>(a.bias + col) + 1);
-        z[0] += b0.x, z[1] += b0.y, z[2] += b0.z, z[3] += b0.w;
-        z[4] += b1.x, z[5] += b1.y, z[6] += b1.z, z[7] += b1.w;
-    }
-    if (a.out1) *octet(a.out1, row, a.N, col) = pack_bf16x8(z);
-    act_values(a.fn, z);
-    if (a.residual) {
-        float r[8];
-        unpack_bf16x8(res, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] += r[j];
-    }
-    *octet(a.out0, row, a.N, col) = pack_bf16x8(z);
 }
 
 // ---- fused epilogues: 32 rows x 32 columns of a warp ----

@@ -32,19 +32,9 @@ struct PsCfg {
     static constexpr int B_BYTES = BN / 2 * kRowBytes;  // this CTA's half of B
     static constexpr int STAGE = kPsA + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 6 : 8;
-    static constexpr int PARK_LD = BN + 4;              // floats: 16-byte rows, quarter-warps on distinct banks
     static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE + 256;
-    static_assert(kBM * PARK_LD * 4 <= STAGES * STAGE, "the parked accumulator reuses the stages");
+    static_assert(kBM * BN * 4 <= STAGES * STAGE, "the parked accumulator reuses the stages");
 };
-
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
 
 template <int KIND, int BN, int SPLITS>
 __global__ void __launch_bounds__(kPsThreads)
@@ -57,7 +47,6 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
     constexpr int N_TILE = L::GATED ? BN / 2 : BN;  // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);  // identical offsets in all CTAs
-    float* park = reinterpret_cast<float*>(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * C::STAGE);
     uint64_t* empty = full + S;
     uint64_t* done = empty + S;
@@ -201,19 +190,7 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
         }
         return;
     }
-    if (ok) {
-        float* row = park + (q * 32 + lane) * C::PARK_LD + half * (BN / 2);
-        const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * (BN / 2));
-#pragma unroll
-        for (int c = 0; c < BN / 2; c += 32) {
-            uint32_t r[32];
-            tmem_ld_32x32(t + c, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<uint4*>(row + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-        }
-    }
+    if (ok && m0 + q * 32 < a.M) park_rows<BN>(smem, tmem, q, half, lane);  // rows that exist
     __syncwarp();
     pdl_trigger();
     tc_fence_before();
@@ -224,62 +201,7 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
         tmem_dealloc_pair(tmem, BN);
     }
 
-    // This CTA's share of the join: every SPLITS-th of its rows, N_TILE / 8 octets
-    // a row, in passes of as many octets as sixteen 16-byte loads a thread allow.
-    constexpr int OCTETS = N_TILE / 8;
-    constexpr int ITEMS = kBM * OCTETS / SPLITS;
-    constexpr int HALVES = L::GATED ? 2 : 1;
-    constexpr int PER = 8 / (HALVES * SPLITS) > 0 ? 8 / (HALVES * SPLITS) : 1;
-    const uint32_t park0 = smem_u32(park);
-#pragma unroll 1
-    for (int base = 0; base < ITEMS; base += PER * kPsThreads) {
-        int rows[PER], cols[PER];
-        uint4 res[PER];
-        float4 parts[PER][HALVES][SPLITS][2];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int it = base + i * kPsThreads + static_cast<int>(threadIdx.x);
-            const int r = it / OCTETS * SPLITS + static_cast<int>(part), c = it % OCTETS * 8;
-            const bool in = it < ITEMS && m0 + r < a.M && n0 + c < a.N;
-            rows[i] = in ? r : -1;
-            cols[i] = c;
-            if constexpr (KIND == DENSE_LINEAR) {
-                res[i] = make_uint4(0, 0, 0, 0);
-                if (in && a.residual) res[i] = *octet(a.residual, m0 + r, a.N, n0 + c);
-            }
-            if (!in) continue;
-#pragma unroll
-            for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-                for (int s = 0; s < SPLITS; ++s) {
-                    const uint32_t at = park0 + static_cast<uint32_t>(r * C::PARK_LD + h * N_TILE + c) * 4u;
-                    const uint32_t p = SPLITS > 1 ? mapa_shared(at, 2 * s + rank) : at;
-                    parts[i][h][s][0] = ld_cluster_v4(p);
-                    parts[i][h][s][1] = ld_cluster_v4(p + 16);
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (rows[i] < 0) continue;
-            float v[HALVES][8];
-#pragma unroll
-            for (int h = 0; h < HALVES; ++h) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[h][j] = 0.0f;
-#pragma unroll
-                for (int s = 0; s < SPLITS; ++s) {  // in order of the k-parts
-                    const float4 x = parts[i][h][s][0], y = parts[i][h][s][1];
-                    v[h][0] += x.x, v[h][1] += x.y, v[h][2] += x.z, v[h][3] += x.w;
-                    v[h][4] += y.x, v[h][5] += y.y, v[h][6] += y.z, v[h][7] += y.w;
-                }
-            }
-            const long long row = static_cast<long long>(m0) + rows[i];
-            const int col = n0 + cols[i];
-            if constexpr (L::GATED) gated_octet(a, row, col, v[0], v[HALVES - 1]);
-            else if constexpr (KIND == DENSE_LINEAR) linear_octet(a, row, col, v[0], res[i]);
-            else *octet(mat ? a.out1 : a.out0, row, a.N, col) = pack_bf16x8(v[0]);
-        }
-    }
+    join_parts<KIND, BN, SPLITS>(a, mat, smem_u32(smem), m0, n0, static_cast<int>(part), rank, 2);
     cluster_sync_all();  // no CTA leaves while another reads its shared memory or signals it
 }
 

@@ -45,18 +45,8 @@ constexpr int kSplitStages = 6;
 constexpr int kSplitThreads = 256;
 constexpr int kOperandBytes = kBM * kRowBytes;  // 16 KB: 128 rows x 64 K, or two MN-major boxes
 constexpr int kSplitStageBytes = 2 * kOperandBytes;
-constexpr int kParkLd = kSplitBN + 4;           // floats: 16-byte rows, quarter-warps on distinct banks
 constexpr size_t kSplitSmem = 1024 + kSplitStages * kSplitStageBytes + 128;
-static_assert(kBM * kParkLd * 4 <= kSplitStages * kSplitStageBytes, "the parked accumulator reuses the stages");
-
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
+static_assert(kBM * kSplitBN * 4 <= kSplitStages * kSplitStageBytes, "the parked accumulator reuses the stages");
 
 template <int KIND, int SPLITS>
 __global__ void __launch_bounds__(kSplitThreads)
@@ -68,7 +58,6 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
     constexpr int N_TILE = L::GATED ? kSplitBN / 2 : kSplitBN;  // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    float* park = reinterpret_cast<float*>(smem);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * kSplitStageBytes);
     uint64_t* empty = full + S;
     uint64_t* done = empty + S;
@@ -206,38 +195,8 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         }
         return;
     }
-    if (ok) {
-        float* row = park + (q * 32 + lane) * kParkLd + half * (kSplitBN / 2);
-        const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * (kSplitBN / 2));
-#pragma unroll
-        for (int c = 0; c < kSplitBN / 2; c += 32) {
-            uint32_t r[32];
-            tmem_ld_32x32(t + c, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<uint4*>(row + c + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-        }
-    }
-    // This CTA's share of the join: every SPLITS-th row, 16 (gated: 8) octets a row
-    constexpr int OCTETS = N_TILE / 8;
-    constexpr int ITEMS = kBM * OCTETS / SPLITS;
-    constexpr int PER = (ITEMS + kSplitThreads - 1) / kSplitThreads;
-    int rows[PER], cols[PER];
-    uint4 res[PER];
+    if (ok && m0 + q * 32 < a.M) park_rows<kSplitBN>(smem, tmem, q, half, lane);  // rows that exist
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int it = i * kSplitThreads + static_cast<int>(threadIdx.x);
-        const int r = it / OCTETS * SPLITS + static_cast<int>(rank), c = it % OCTETS * 8;
-        const bool in = it < ITEMS && m0 + r < a.M && n0 + c < a.N;
-        rows[i] = in ? r : -1;
-        cols[i] = c;
-        if constexpr (KIND == DENSE_LINEAR) {
-            res[i] = make_uint4(0, 0, 0, 0);
-            if (in && a.residual) res[i] = *octet(a.residual, m0 + r, a.N, n0 + c);
-        }
-    }
     pdl_trigger();
     tc_fence_before();
     __syncthreads();
@@ -245,45 +204,9 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, kSplitBN);
     }
-    if constexpr (SPLITS > 1) cluster_sync_all();  // every CTA's accumulator is parked
-
-    const uint32_t park0 = smem_u32(park);
-    constexpr int HALVES = L::GATED ? 2 : 1;
-    float4 parts[PER][HALVES][SPLITS][2];
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-            for (int s = 0; s < SPLITS; ++s) {
-                if (rows[i] < 0) continue;
-                const uint32_t at = park0 + static_cast<uint32_t>(rows[i] * kParkLd + h * N_TILE + cols[i]) * 4u;
-                const uint32_t p = SPLITS > 1 ? mapa_shared(at, s) : at;
-                parts[i][h][s][0] = ld_cluster_v4(p);
-                parts[i][h][s][1] = ld_cluster_v4(p + 16);
-            }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        if (rows[i] < 0) continue;
-        float v[HALVES][8];
-#pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[h][j] = 0.0f;
-#pragma unroll
-            for (int s = 0; s < SPLITS; ++s) {  // in rank order
-                const float4 x = parts[i][h][s][0], y = parts[i][h][s][1];
-                v[h][0] += x.x, v[h][1] += x.y, v[h][2] += x.z, v[h][3] += x.w;
-                v[h][4] += y.x, v[h][5] += y.y, v[h][6] += y.z, v[h][7] += y.w;
-            }
-        }
-        const long long row = static_cast<long long>(m0) + rows[i];
-        const int col = n0 + cols[i];
-        if constexpr (L::GATED) gated_octet(a, row, col, v[0], v[HALVES - 1]);
-        else if constexpr (KIND == DENSE_LINEAR) linear_octet(a, row, col, v[0], res[i]);
-        else *octet(mat ? a.out1 : a.out0, row, a.N, col) = pack_bf16x8(v[0]);
-    }
-    if constexpr (SPLITS > 1) cluster_sync_all();  // no CTA leaves while another reads its shared memory
+    cluster_sync_all();  // every CTA's accumulator is parked
+    join_parts<KIND, kSplitBN, SPLITS>(a, mat, smem_u32(smem), m0, n0, static_cast<int>(rank), 0, 1);
+    cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
 template <int KIND, int SPLITS>
