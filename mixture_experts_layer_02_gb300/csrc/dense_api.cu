@@ -124,18 +124,21 @@ int env_int(const char* name, int dflt) {
 }
 
 // MOE_DENSE_KERNEL = 1 (split tiles), 2 (persistent pairs) or 3 (streamed weights,
-// where M allows), MOE_DENSE_SPLIT = 10 * bn + splits and MOE_DENSE_CLUSTER = 2 or
+// where M allows), and with it MOE_DENSE_SPLIT = 10 * bn + splits and MOE_DENSE_CLUSTER = 2 or
 // 4 force a choice, for tuning and test coverage.
 moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p) {
     const int n2 = kind == DENSE_GATED ? 128 : 256;
-    const int kernel = env_int("MOE_DENSE_KERNEL", 0), fixed = env_int("MOE_DENSE_SPLIT", -1);
+    const int kernel = env_int("MOE_DENSE_KERNEL", 0);
     *p = {0, 1, 0, 0, false};
     const bool forward = kind == DENSE_GATED || kind == DENSE_LINEAR;
     const double weights = 2e-6 * a.N * a.K * (kind == DENSE_GATED ? 2 : 1);  // MB
-    if (forward && a.M <= kGemvMaxRows && kernel == 3) {
+    // up to eight rows x is at most half of what the weights are: nothing came near the streamed form
+    if (forward && ((a.M <= 8 && kernel == 0) || (a.M <= kGemvMaxRows && kernel == 3))) {
         p->stream = true;
         return MOE_OK;
     }
+    const int fixed = kernel ? env_int("MOE_DENSE_SPLIT", -1) : -1;
+    const int only = kernel ? env_int("MOE_DENSE_CLUSTER", 0) : 0;
     double best = 1e30;
     for (const TileKind& t : kSplitTiles) {
         const int rows = t.bn ? 2 * kBM : kBM, width = (t.bn ? t.bn : 128) / (kind == DENSE_GATED ? 2 : 1);
@@ -169,7 +172,7 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
     }
     if (kernel == 2) best = 1e30;
     for (int cl = 2; cl <= 4; cl += 2) {
-        if (env_int("MOE_DENSE_CLUSTER", cl) != cl) continue;
+        if (only && only != cl) continue;
         int limit = 0;
         const moe_status st = launched(dense_pair_limit(kind, cl, &limit), "dense pair limit");
         if (st != MOE_OK) return st;

@@ -140,8 +140,9 @@ __device__ __forceinline__ void tmem_row(uint32_t taddr, float (&v)[32]) {
 // Each CTA parks its accumulator (128 rows x BN fp32) in shared memory, row by
 // row, the 16-byte quads of a row permuted by its number: the parking threads
 // (one row each) and the joining warps (whole rows) both use all banks, and a
-// warp's load from another CTA is whole aligned lines (with padded rows and
-// 32-byte pieces such loads ran at 12 bytes a clock and the join took 3 us).
+// warp's load from another CTA is whole aligned lines.  Loads from other CTAs run
+// at about 23 GB/s an SM whatever their shape, so a CTA's own copy is read as plain
+// shared memory.
 template <int BN>
 __device__ __forceinline__ uint32_t park_at(int row, int quad) {
     return static_cast<uint32_t>(row * BN * 4 + ((quad ^ (row & 7)) << 4));
@@ -207,74 +208,107 @@ __device__ __forceinline__ void linear_quad(const DenseArgs& a, long long row, i
     *quad_of(a.out0, row, a.N, col) = pack_quad(z);
 }
 
-// The share of CTA `part` of `SPLITS`: every SPLITS-th row.  Thread t of 256 takes
-// quads t, t + 256, ... of those rows, in passes of up to sixteen loads, all issued
-// before the first is used; `first` + k * `step` are the ranks of the k-parts, summed
-// in order.
+// ---- the residual of a split tile, fetched into shared memory under the main loop ----
+// A CTA's rows of it (every SPLITS-th of 128) x BN columns, by four warps that have
+// no other work then; read in the epilogue as it comes, it cost about 0.6 us a step.
+// 16-byte pieces, permuted by the row.  0 bytes: no room (the whole 128 x 256 tile).
 template <int KIND, int BN, int SPLITS>
-__device__ __forceinline__ void join_parts(const DenseArgs& a, int mat, uint32_t park, int m0, int n0, int part,
-                                           uint32_t first, uint32_t step) {
+constexpr int kResidualBytes = KIND == DENSE_LINEAR && kBM / SPLITS * BN * 2 <= 32768 ? kBM / SPLITS * BN * 2 : 0;
+
+template <int BN>
+__device__ __forceinline__ uint32_t residual_at(int local_row, int piece) {
+    return static_cast<uint32_t>(local_row * BN * 2 + ((piece ^ (local_row & 15)) << 4));
+}
+
+template <int BN, int SPLITS>
+__device__ __forceinline__ void fetch_residual(const DenseArgs& a, uint8_t* res, int m0, int n0, int part, int thread) {
+    constexpr int PN = BN / 8;
+#pragma unroll 4
+    for (int it = thread; it < kBM / SPLITS * PN; it += 128) {
+        const int i = it / PN, p = it % PN;
+        const long long row = static_cast<long long>(m0) + i * SPLITS + part;
+        const int col = n0 + p * 8;
+        if (row < a.M && col < a.N)
+            *reinterpret_cast<uint4*>(res + residual_at<BN>(i, p)) =
+                *reinterpret_cast<const uint4*>(a.residual + row * a.N + col);
+    }
+}
+
+// The share of CTA `part` of `SPLITS`: every SPLITS-th row, whose parked copies
+// only this CTA reads.  Thread t of 256 takes quads t, t + 256, ... of those rows;
+// `first` + k * `step` are the ranks of the k-parts, summed in order.  First the
+// sums, in passes of up to sixteen loads, all issued before the first is used,
+// each sum back into this CTA's own copy; then the epilogue over them in a rolled
+// loop: its instructions run once a launch, and unrolled eight times they were
+// fetched cold for longer than they worked.
+template <int KIND, int BN, int SPLITS>
+__device__ __forceinline__ void join_parts(const DenseArgs& a, int mat, uint8_t* park, const uint8_t* res, int m0, int n0,
+                                           int part, uint32_t first, uint32_t step) {
     constexpr bool GATED = DenseLayout<KIND>::GATED;
     constexpr int HALVES = GATED ? 2 : 1;
     constexpr int QN = BN / 4 / HALVES;  // output quads of a row
     constexpr int ITEMS = kBM / SPLITS * QN;
     constexpr int MOST = 16 / (HALVES * SPLITS), ALL = (ITEMS + 255) / 256;
     constexpr int PER = MOST < ALL ? MOST : ALL;
+    const uint32_t park0 = smem_u32(park);
+    // item -> row of the tile (-1: none) and quad
+    auto place = [&](int it, int& r, int& q) {
+        r = it / QN * SPLITS + part;
+        q = it % QN;
+        if (it >= ITEMS || m0 + r >= a.M || n0 + q * 4 >= a.N) r = -1;
+    };
 #pragma unroll 1
     for (int base = 0; base < ITEMS; base += PER * 256) {
-        int rows[PER], cols[PER];
-        uint2 res[PER];
         float4 parts[PER][HALVES][SPLITS];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int it = base + i * 256 + static_cast<int>(threadIdx.x);
-            const int r = it / QN * SPLITS + part, q = it % QN;
-            const bool in = it < ITEMS && m0 + r < a.M && n0 + q * 4 < a.N;
-            rows[i] = in ? r : -1;
-            cols[i] = q * 4;
-            res[i] = make_uint2(0, 0);
-            if (KIND == DENSE_LINEAR && in && a.residual)
-                res[i] = *quad_of(const_cast<uint16_t*>(a.residual), m0 + r, a.N, n0 + q * 4);
-            if (!in) continue;
+            int r, q;
+            place(base + i * 256 + static_cast<int>(threadIdx.x), r, q);
+            if (r < 0) continue;
 #pragma unroll
             for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-                for (int s = 0; s < SPLITS; ++s)
-                    parts[i][h][s] = ld_cluster_v4(mapa_shared(park + park_at<BN>(r, h * QN + q), first + s * step));
+                for (int s = 0; s < SPLITS; ++s) {
+                    const uint32_t at = park_at<BN>(r, h * QN + q);
+                    if (s == part) parts[i][h][s] = *reinterpret_cast<const float4*>(park + at);
+                    else parts[i][h][s] = ld_cluster_v4(mapa_shared(park0 + at, first + s * step));
+                }
         }
-        float v[PER][HALVES][4];
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
+        for (int i = 0; i < PER; ++i) {
+            int r, q;
+            place(base + i * 256 + static_cast<int>(threadIdx.x), r, q);
+            if (r < 0) continue;
 #pragma unroll
             for (int h = 0; h < HALVES; ++h) {
-                v[i][h][0] = v[i][h][1] = v[i][h][2] = v[i][h][3] = 0.0f;
+                float4 v = parts[i][h][0];
 #pragma unroll
-                for (int s = 0; s < SPLITS; ++s) {
+                for (int s = 1; s < SPLITS; ++s) {
                     const float4 x = parts[i][h][s];
-                    v[i][h][0] += x.x, v[i][h][1] += x.y, v[i][h][2] += x.z, v[i][h][3] += x.w;
+                    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
                 }
-            }
-        // the epilogue in a rolled loop, the items moving to the front: its instructions run once a launch
-#pragma unroll 1
-        for (int n = 0; n < PER; ++n) {
-            if (rows[0] >= 0) {
-                const long long row = static_cast<long long>(m0) + rows[0];
-                const int col = n0 + cols[0];
-                if constexpr (GATED) gated_quad(a, row, col, v[0][0], v[0][HALVES - 1]);
-                else if constexpr (KIND == DENSE_LINEAR) linear_quad(a, row, col, v[0][0], res[0]);
-                else *quad_of(mat ? a.out1 : a.out0, row, a.N, col) = pack_quad(v[0][0]);
-            }
-#pragma unroll
-            for (int i = 0; i + 1 < PER; ++i) {
-                rows[i] = rows[i + 1];
-                cols[i] = cols[i + 1];
-                res[i] = res[i + 1];
-#pragma unroll
-                for (int h = 0; h < HALVES; ++h)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[i][h][j] = v[i + 1][h][j];
+                *reinterpret_cast<float4*>(park + park_at<BN>(r, h * QN + q)) = v;
             }
         }
+    }
+#pragma unroll 1
+    for (int it = threadIdx.x; it < ITEMS; it += 256) {
+        int r, q;
+        place(it, r, q);
+        if (r < 0) continue;
+        float v[HALVES][4];
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) {
+            const float4 x = *reinterpret_cast<const float4*>(park + park_at<BN>(r, h * QN + q));
+            v[h][0] = x.x, v[h][1] = x.y, v[h][2] = x.z, v[h][3] = x.w;
+        }
+        const long long row = static_cast<long long>(m0) + r;
+        const int col = n0 + q * 4;
+        if constexpr (GATED) gated_quad(a, row, col, v[0], v[HALVES - 1]);
+        else if constexpr (KIND == DENSE_LINEAR) linear_quad(a, row, col, v[0],
+                                                            *reinterpret_cast<const uint2*>(
+                                                                res + residual_at<BN>(r / SPLITS, q >> 1) + (q & 1) * 8));
+        else *quad_of(mat ? a.out1 : a.out0, row, a.N, col) = pack_quad(v[0]);
     }
 }
 
@@ -312,13 +346,13 @@ struct RowChunk {
         }
     }
     // what fetch read, as this thread's row
-    __device__ __forceinline__ void to_row(const uint4 (&v)[4], uint4 (&row)[4]) const {
+    __device__ __forceinline__ void to_row(uint4 (&v)[4]) const {
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) *cell(i * 8 + (lane >> 2), lane & 3) = v[i];
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) row[i] = *cell(lane, i);
+        for (int i = 0; i < 4; ++i) v[i] = *cell(lane, i);
     }
     __device__ __forceinline__ void store(uint16_t* base, const float (&v)[32]) const {
         __syncwarp();
@@ -345,7 +379,9 @@ __device__ __forceinline__ void gated_chunk(const DenseArgs& a, const RowChunk& 
     c.store(a.out0, g);
 }
 
-__device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk& c, float (&z)[32], const uint4 (&res)[4]) {
+// `res`: the residual as RowChunk::fetch left it, or (own_row) this thread's row of it.
+__device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk& c, float (&z)[32], uint4 (&res)[4],
+                                             bool own_row) {
     if (a.bias) {
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
@@ -359,12 +395,11 @@ __device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk&
     if (a.out1) c.store(a.out1, z);
     act_values(a.fn, z);
     if (a.residual) {
-        uint4 row[4];
-        c.to_row(res, row);
+        if (!own_row) c.to_row(res);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float r[8];
-            unpack_bf16x8(row[i], r);
+            unpack_bf16x8(res[i], r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[8 * i + j] += r[j];
         }
@@ -374,9 +409,10 @@ __device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk&
 
 // The epilogue of a whole accumulator of 128 rows x BN columns by eight warps:
 // warp (q, half) takes lanes 32 q .. and half of the output columns.
+// `res`: the tile's residual in shared memory (fetch_residual), or NULL: read here.
 template <int KIND, int BN>
-__device__ __forceinline__ void whole_epilogue(const DenseArgs& a, int mat, uint32_t tmem, uint8_t* chunk_smem, int m0,
-                                               int n0, int q, int half, int lane) {
+__device__ __forceinline__ void whole_epilogue(const DenseArgs& a, int mat, uint32_t tmem, uint8_t* chunk_smem,
+                                               const uint8_t* res, int m0, int n0, int q, int half, int lane) {
     constexpr bool GATED = DenseLayout<KIND>::GATED;
     constexpr int COLS = GATED ? BN / 4 : BN / 2;  // output columns of a warp
     const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * COLS);
@@ -385,10 +421,16 @@ __device__ __forceinline__ void whole_epilogue(const DenseArgs& a, int mat, uint
         float v[32];
         const RowChunk chunk{chunk_smem, static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M, a.N, lane};
         if constexpr (KIND == DENSE_LINEAR) {
-            uint4 res[4];
-            if (a.residual) chunk.fetch(a.residual, res);
+            uint4 piece[4];
+            if (res) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    piece[i] = *reinterpret_cast<const uint4*>(res + residual_at<BN>(q * 32 + lane, (half * COLS + c) / 8 + i));
+            } else if (a.residual) {
+                chunk.fetch(a.residual, piece);
+            }
             tmem_row(t + c, v);
-            linear_chunk(a, chunk, v, res);
+            linear_chunk(a, chunk, v, piece, res != nullptr);
         } else if constexpr (GATED) {
             float u[32];
             tmem_row(t + c, v);

@@ -239,7 +239,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             __syncwarp();
             if (!named_barrier_and(1, kEpiWarps * 32, ok)) break;  // given up: by all of them
             tc_fence_after();
-            whole_epilogue<KIND, kPairTile>(a, w.mat, tmem_base + static_cast<uint32_t>(acc * kPairTile), stage_smem,
+            whole_epilogue<KIND, kPairTile>(a, w.mat, tmem_base + static_cast<uint32_t>(acc * kPairTile), stage_smem, nullptr,
                                             w.m0 + static_cast<int>(crank) * kBM, w.n0, q, half, lane);
             tc_fence_before();
             __syncwarp();

@@ -32,9 +32,12 @@ struct PsCfg {
     static constexpr int B_BYTES = BN / 2 * kRowBytes;  // this CTA's half of B
     static constexpr int STAGE = kPsA + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 6 : 8;
-    static constexpr size_t SMEM = 1024 + static_cast<size_t>(STAGES) * STAGE + 256;
     static_assert(kBM * BN * 4 <= STAGES * STAGE, "the parked accumulator reuses the stages");
 };
+
+template <int KIND, int BN, int SPLITS>
+constexpr size_t kPsSmem =
+    1024 + static_cast<size_t>(PsCfg<BN>::STAGES) * PsCfg<BN>::STAGE + kResidualBytes<KIND, BN, SPLITS> + 256;
 
 template <int KIND, int BN, int SPLITS>
 __global__ void __launch_bounds__(kPsThreads)
@@ -47,7 +50,9 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
     constexpr int N_TILE = L::GATED ? BN / 2 : BN;  // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);  // identical offsets in all CTAs
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * C::STAGE);
+    constexpr int RES = kResidualBytes<KIND, BN, SPLITS>;
+    uint8_t* res = smem + S * C::STAGE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(res + RES);
     uint64_t* empty = full + S;
     uint64_t* done = empty + S;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -171,6 +176,9 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
             idle_wait(done, 0, &never, a.err);
         }
     }
+    if constexpr (RES > 0) {
+        if (warp >= 4 && a.residual) fetch_residual<BN, SPLITS>(a, res, m0, n0, static_cast<int>(part), threadIdx.x - 128);
+    }
     __syncwarp();
     __syncthreads();  // the accumulator is complete (or the product was given up)
     const bool ok = *abort_flag == 0;
@@ -178,7 +186,8 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
     const int q = warp & 3, half = warp >> 2;  // TMEM lanes 32 q .., columns of this half
     if constexpr (SPLITS == 1) {
         // nothing to join: from TMEM through the epilogue, 32 x 32 at a time
-        if (ok) whole_epilogue<KIND, BN>(a, mat, tmem, smem + warp * kChunkBytes, m0, n0, q, half, lane);
+        if (ok) whole_epilogue<KIND, BN>(a, mat, tmem, smem + warp * kChunkBytes, RES > 0 && a.residual ? res : nullptr, m0, n0,
+                                        q, half, lane);
         __syncwarp();
         pdl_trigger();
         tc_fence_before();
@@ -201,7 +210,7 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
         tmem_dealloc_pair(tmem, BN);
     }
 
-    join_parts<KIND, BN, SPLITS>(a, mat, smem_u32(smem), m0, n0, static_cast<int>(part), rank, 2);
+    join_parts<KIND, BN, SPLITS>(a, mat, smem, res, m0, n0, static_cast<int>(part), rank, 2);
     cluster_sync_all();  // no CTA leaves while another reads its shared memory or signals it
 }
 
@@ -210,7 +219,7 @@ cudaLaunchConfig_t ps_config(cudaLaunchAttribute (&attr)[2], cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * SPLITS);
     cfg.blockDim = dim3(kPsThreads);
-    cfg.dynamicSmemBytes = PsCfg<BN>::SMEM;
+    cfg.dynamicSmemBytes = kPsSmem<KIND, BN, SPLITS>;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2 * SPLITS;
@@ -233,7 +242,7 @@ cudaError_t ps_prepare(int* clusters) {
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_acquire) & bit)) {
         e = cudaFuncSetAttribute(dense_pairsplit_kernel<KIND, BN, SPLITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(PsCfg<BN>::SMEM));
+                                 static_cast<int>(kPsSmem<KIND, BN, SPLITS>));
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute attr[2];
         const cudaLaunchConfig_t cfg = ps_config<KIND, BN, SPLITS>(attr, nullptr);

@@ -45,7 +45,8 @@ constexpr int kSplitStages = 6;
 constexpr int kSplitThreads = 256;
 constexpr int kOperandBytes = kBM * kRowBytes;  // 16 KB: 128 rows x 64 K, or two MN-major boxes
 constexpr int kSplitStageBytes = 2 * kOperandBytes;
-constexpr size_t kSplitSmem = 1024 + kSplitStages * kSplitStageBytes + 128;
+template <int KIND, int SPLITS>
+constexpr size_t kSplitSmem = 1024 + kSplitStages * kSplitStageBytes + kResidualBytes<KIND, kSplitBN, SPLITS> + 128;
 static_assert(kBM * kSplitBN * 4 <= kSplitStages * kSplitStageBytes, "the parked accumulator reuses the stages");
 
 template <int KIND, int SPLITS>
@@ -58,7 +59,9 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
     constexpr int N_TILE = L::GATED ? kSplitBN / 2 : kSplitBN;  // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * kSplitStageBytes);
+    constexpr int RES = kResidualBytes<KIND, kSplitBN, SPLITS>;
+    uint8_t* res = smem + S * kSplitStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(res + RES);
     uint64_t* empty = full + S;
     uint64_t* done = empty + S;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -177,6 +180,9 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
             idle_wait(done, 0, &never, a.err);
         }
     }
+    if constexpr (RES > 0) {
+        if (warp >= 4 && a.residual) fetch_residual<kSplitBN, SPLITS>(a, res, m0, n0, static_cast<int>(rank), threadIdx.x - 128);
+    }
     __syncwarp();
     __syncthreads();  // the accumulator is complete (or the product was given up)
     const bool ok = *abort_flag == 0;
@@ -184,7 +190,8 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
     const int q = warp & 3, half = warp >> 2;  // TMEM lanes 32 q .., columns of this half
     if constexpr (SPLITS == 1) {
         // nothing to join: from TMEM through the epilogue, 32 x 32 at a time
-        if (ok) whole_epilogue<KIND, kSplitBN>(a, mat, tmem, smem + warp * kChunkBytes, m0, n0, q, half, lane);
+        if (ok) whole_epilogue<KIND, kSplitBN>(a, mat, tmem, smem + warp * kChunkBytes, RES > 0 && a.residual ? res : nullptr, m0,
+                                              n0, q, half, lane);
         __syncwarp();
         pdl_trigger();
         tc_fence_before();
@@ -205,7 +212,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         tmem_dealloc(tmem, kSplitBN);
     }
     cluster_sync_all();  // every CTA's accumulator is parked
-    join_parts<KIND, kSplitBN, SPLITS>(a, mat, smem_u32(smem), m0, n0, static_cast<int>(rank), 0, 1);
+    join_parts<KIND, kSplitBN, SPLITS>(a, mat, smem, res, m0, n0, static_cast<int>(rank), 0, 1);
     cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
@@ -214,7 +221,7 @@ cudaLaunchConfig_t split_config(cudaLaunchAttribute (&attr)[2], cudaStream_t st)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(SPLITS);
     cfg.blockDim = dim3(kSplitThreads);
-    cfg.dynamicSmemBytes = kSplitSmem;
+    cfg.dynamicSmemBytes = kSplitSmem<KIND, SPLITS>;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = SPLITS;
@@ -237,7 +244,7 @@ cudaError_t split_prepare(int* clusters) {
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_acquire) & bit)) {
         e = cudaFuncSetAttribute(dense_split_kernel<KIND, SPLITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kSplitSmem));
+                                 static_cast<int>(kSplitSmem<KIND, SPLITS>));
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute attr[2];
         const cudaLaunchConfig_t cfg = split_config<KIND, SPLITS>(attr, nullptr);
