@@ -323,10 +323,10 @@ __device__ __forceinline__ const uint4* octet(const uint16_t* base, long long ro
 // tcgen05.ld leaves one accumulator row in each thread.  Stored as it lies, a
 // warp's 16-byte store touches 32 rows at once, half a sector each; the kernel
 // that keeps g and u was bound by that (656 us against 573 us without them at
-// 4096 x 4096 x 14336).  So a chunk goes through 2 KB of shared memory per warp
+// 4096 x 4096 x 14336).  So a chunk goes through shared memory
 // and leaves (and a residual enters) as 64-byte pieces of eight rows.  The
 // 16-byte pieces of a row are permuted so that both directions use all banks.
-constexpr int kChunkBytes = 32 * 64;
+constexpr int kChunkBytes = 32 * 128;  // 64-byte rows here, 128-byte rows in plain_chunk
 
 struct RowChunk {
     uint8_t* smem;   // this warp's kChunkBytes
@@ -407,40 +407,85 @@ __device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk&
     c.store(a.out0, z);
 }
 
-// The epilogue of a whole accumulator of 128 rows x BN columns by eight warps:
-// warp (q, half) takes lanes 32 q .. and half of the output columns.
-// `res`: the tile's residual in shared memory (fetch_residual), or NULL: read here.
-template <int KIND, int BN>
-__device__ __forceinline__ void whole_epilogue(const DenseArgs& a, int mat, uint32_t tmem, uint8_t* chunk_smem,
-                                               const uint8_t* res, int m0, int n0, int q, int half, int lane) {
-    constexpr bool GATED = DenseLayout<KIND>::GATED;
-    constexpr int COLS = GATED ? BN / 4 : BN / 2;  // output columns of a warp
-    const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * COLS);
-#pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-        float v[32];
-        const RowChunk chunk{chunk_smem, static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M, a.N, lane};
-        if constexpr (KIND == DENSE_LINEAR) {
-            uint4 piece[4];
-            if (res) {
+// A gradient's 32 rows x 64 columns: 128-byte lines of four rows a store.
+__device__ __forceinline__ void plain_chunk(uint8_t* smem, uint32_t taddr, uint16_t* base, long long row0, int col0, int M,
+                                            int N, int lane) {
+    uint32_t r[64];
+    {
+        uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[0]);
+        uint32_t(&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[32]);
+        tmem_ld_32x32(taddr, lo);
+        tmem_ld_32x32(taddr + 32, hi);
+        tmem_ld_wait();
+    }
+    auto cell = [&](int row, int p) { return reinterpret_cast<uint4*>(smem + row * 128 + ((p ^ (row & 7)) << 4)); };
+    auto two = [&](int j) { return pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])); };
+    __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    piece[i] = *reinterpret_cast<const uint4*>(res + residual_at<BN>(q * 32 + lane, (half * COLS + c) / 8 + i));
-            } else if (a.residual) {
-                chunk.fetch(a.residual, piece);
-            }
-            tmem_row(t + c, v);
-            linear_chunk(a, chunk, v, piece, res != nullptr);
-        } else if constexpr (GATED) {
-            float u[32];
-            tmem_row(t + c, v);
-            tmem_row(t + BN / 2 + c, u);
-            gated_chunk(a, chunk, v, u);
-        } else {
-            tmem_row(t + c, v);
-            chunk.store(mat ? a.out1 : a.out0, v);
-        }
+    for (int i = 0; i < 8; ++i) *cell(lane, i) = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
+    __syncwarp();
+    const int col = col0 + (lane & 7) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const long long row = row0 + i * 4 + (lane >> 3);
+        if (row < M && col < N) *octet(base, row, N, col) = *cell(i * 4 + (lane >> 3), lane & 7);
     }
 }
+
+// The epilogue of a whole accumulator of 128 rows x BN columns by eight warps:
+// warp (q, half) takes lanes 32 q .. and half of the output columns.  `res`: the
+// tile's residual in shared memory (fetch_residual), or NULL: it is read here, a
+// chunk ahead, the first one by the caller into `ahead` (fetch_ahead) before it
+// waits for the accumulator.
+template <int KIND, int BN>
+struct WholeEpilogue {
+    static constexpr bool GATED = DenseLayout<KIND>::GATED;
+    static constexpr int COLS = GATED ? BN / 4 : BN / 2;  // output columns of a warp
+    const DenseArgs& a;
+    uint8_t* smem;  // this warp's kChunkBytes
+    int m0, n0, q, half, lane;
+    uint4 ahead[4];
+
+    __device__ __forceinline__ RowChunk chunk(int c) const {
+        return RowChunk{smem, static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M, a.N, lane};
+    }
+    __device__ __forceinline__ void fetch_ahead() {
+        if (KIND == DENSE_LINEAR && a.residual) chunk(0).fetch(a.residual, ahead);
+    }
+    __device__ __forceinline__ void run(int mat, uint32_t tmem, const uint8_t* res) {
+        const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * COLS);
+        if constexpr (KIND == DENSE_DGRAD || KIND == DENSE_WGRAD) {
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += 64)
+                plain_chunk(smem, t + c, mat ? a.out1 : a.out0, static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M,
+                            a.N, lane);
+        } else {
+#pragma unroll 1
+            for (int c = 0; c < COLS; c += 32) {
+                float v[32];
+                if constexpr (KIND == DENSE_LINEAR) {
+                    uint4 piece[4];
+                    if (res) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            piece[i] = *reinterpret_cast<const uint4*>(
+                                res + residual_at<BN>(q * 32 + lane, (half * COLS + c) / 8 + i));
+                    } else if (a.residual) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) piece[i] = ahead[i];
+                        if (c + 32 < COLS) chunk(c + 32).fetch(a.residual, ahead);
+                    }
+                    tmem_row(t + c, v);
+                    linear_chunk(a, chunk(c), v, piece, res != nullptr);
+                } else {
+                    float u[32];
+                    tmem_row(t + c, v);
+                    tmem_row(t + BN / 2 + c, u);
+                    gated_chunk(a, chunk(c), v, u);
+                }
+            }
+        }
+    }
+};
 
 }  // namespace moe

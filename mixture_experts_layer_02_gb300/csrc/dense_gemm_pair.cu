@@ -235,12 +235,13 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         uint32_t acc_phase = 0;
         for (int tile = first; tile < tiles; tile += step) {
             const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
+            WholeEpilogue<KIND, kPairTile> e{a, stage_smem, w.m0 + static_cast<int>(crank) * kBM, w.n0, q, half, lane, {}};
+            e.fetch_ahead();
             const bool ok = warp != 2 || lane != 0 || idle_wait(&tfull[acc], acc_phase, abort_flag, err);
             __syncwarp();
             if (!named_barrier_and(1, kEpiWarps * 32, ok)) break;  // given up: by all of them
             tc_fence_after();
-            whole_epilogue<KIND, kPairTile>(a, w.mat, tmem_base + static_cast<uint32_t>(acc * kPairTile), stage_smem, nullptr,
-                                            w.m0 + static_cast<int>(crank) * kBM, w.n0, q, half, lane);
+            e.run(w.mat, tmem_base + static_cast<uint32_t>(acc * kPairTile), nullptr);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * acc);

@@ -186,8 +186,11 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
     const int q = warp & 3, half = warp >> 2;  // TMEM lanes 32 q .., columns of this half
     if constexpr (SPLITS == 1) {
         // nothing to join: from TMEM through the epilogue, 32 x 32 at a time
-        if (ok) whole_epilogue<KIND, BN>(a, mat, tmem, smem + warp * kChunkBytes, RES > 0 && a.residual ? res : nullptr, m0, n0,
-                                        q, half, lane);
+        if (ok) {
+            WholeEpilogue<KIND, BN> e{a, smem + warp * kChunkBytes, m0, n0, q, half, lane, {}};
+            if (RES == 0) e.fetch_ahead();
+            e.run(mat, tmem, RES > 0 && a.residual ? res : nullptr);
+        }
         __syncwarp();
         pdl_trigger();
         tc_fence_before();
