@@ -8,21 +8,39 @@
 // issues the MMAs for both.  Two 256-column accumulators fill TMEM: the
 // epilogue of a tile runs under the main loop of the next.
 //
-// Sharing an operand.  With two CTAs to a cluster each SM reads 64 bytes a
-// clock from L2 (A and B halves of 16 KB per 512-clock k-block), and that is
-// what holds the main loop back: a prefetch of later k-blocks into L2, which
-// only adds requests, made it 8 to 14 % slower.  With four (CL = 4), two pairs
-// take m-tiles one above the other and the same columns: each CTA loads half of
-// its B half and multicasts it to the CTA of the other pair that needs the same,
-// 48 bytes a clock.  A stage is then free when both pairs' MMAs have read it
-// (two commits on `empty`).  36 clusters of four hold 144 of the 152 SMs.
+// The main loop.  A k-block is 512 clocks of MMA, and the threads that feed it
+// have to be quicker than that: one thread issuing both operands' copies took
+// 570 clocks a k-block (time stamps), the MMA issuer 480, of which 200 waited for
+// the answer of a barrier that was complete.  So A and B have a copy thread each,
+// the MMA warp walks the stages as a whole with the next barrier asked ahead
+// (StageWalk), and no other warp polls during a main loop.  That took the tensor
+// pipe from 89 to 95 .. 97 % of the active cycles: 498 us alone at 4096 x 4096 x
+// 2 x 14336 keeping both projections (1.93 PFLOP/s), 575 us in a long run, where
+// the board's power limit holds the clock near 1.5 GHz (1.67 PFLOP/s; a library
+// product of 8192^3 runs at 1.71 there).
+//
+// Sharing an operand.  With four CTAs to a cluster (CL = 4), two pairs take
+// m-tiles one above the other and the same columns: each CTA loads half of its B
+// half and multicasts it to the CTA of the other pair that needs the same, so L2
+// is read 48 instead of 64 bytes a clock and SM.  A stage is then free when both
+// pairs' MMAs have read it (two commits on `empty`).  36 clusters of four hold
+// 144 of the 152 SMs.  It gains 1 to 3 % where the rounds of tiles come out alike
+// (4096 x 14336 x 4096: 303 against 310 us) and loses where they do not (weight
+// gradient 4096 x 2048 x 7168: 82 against 74), so the plan goes by the rounds.
+// Asking L2 for later k-blocks ahead made every size 8 to 14 % slower.
+//
+// A last round that leaves pairs idle was dealt out along K over all of them (with
+// fp32 fragments joined through memory): 273 instead of 297 us alone at 4096 x
+// 14336 x 4096, but no gain in a long run, where power and not pairs is short,
+// and slower at smaller sizes; it is not kept.
 //
 // Order of tiles: bands of 8 m-tiles, inside a band n by n, m innermost, so
 // that the pairs working at one time share weight tiles and token rows in L2.
 //
 // Barriers as in grouped_gemm_2sm.cuh: full (even CTA, both CTAs' bytes),
 // empty and tfull (multicast commits), tempty (even CTA, the 16 epilogue warps
-// of both CTAs).  Every wait is bounded.
+// of both CTAs).  Every wait is bounded.  Warps: 0 copies A, 1 allocates TMEM and
+// issues the MMAs, 2..9 epilogue, 10 copies B.
 #include <algorithm>
 #include <atomic>
 

@@ -10,24 +10,27 @@
 // epilogue on the sums.  No fp32 partials reach HBM, there is no second launch,
 // and the order of the additions is fixed.
 //
-// For at most 128 rows (more: dense_gemm_pairsplit.cuh), where the weights come
-// from HBM once and latency is the rest.
+// Used for up to about 128 rows, where the weights come from HBM once and latency
+// is the rest, and above that where its rounds come out better than a pair's.
 //   - Time stamps at 256 x 4096 x 4096 (S = 2, 32 k-blocks a CTA) showed a TMA
-//     round trip of 1.1 us: three 32 KB stages moved a k-block each 0.37 us,
-//     six (one CTA an SM) each 0.25 us.  That is what an SM takes in (64 bytes a
-//     clock), so sharing operand tiles over a cluster by multicast, which was
-//     built and measured, changed nothing here.
-//   - The join took 4 us with one octet of a row after another; every thread now
-//     issues all its distributed-shared-memory loads at once, of rows that exist,
-//     and rows are dealt to the CTAs in turn (a 33-row product would otherwise
-//     leave the join to one of them).
+//     round trip of 1.1 us: three 32 KB stages moved a k-block each 0.37 us, six
+//     (one CTA an SM) and separate copy threads each 0.23 us.  That is what an SM
+//     takes in (64 bytes a clock), so sharing operand tiles over a cluster by
+//     multicast, which was built and measured, changed nothing here.
+//   - With K in parts, 4 to 5 us follow the main loop: parking 0.5, barrier 0.6,
+//     sums 1.4 (one latency of loads from other CTAs), epilogue 0.2 a row of quads,
+//     barrier 0.6.  The loads are all in flight at once, rows are dealt to the CTAs
+//     in turn (33 rows would otherwise leave the join to one of them), rows that do
+//     not exist are neither parked nor read, and the residual waits in shared memory.
+//   Measured: gated 100 x 2048 x 768 7.2 us, linear 64 x 7168 x 2048 11.1 us,
+//   33 x 2048 x 2048 6.0 us.
 //
 // Warp roles: 0 copies A, 2 copies B (one thread issuing both took longer than a
 // k-block's MMAs), 1 allocates TMEM and issues the MMAs; all eight
 // park the accumulator (warp w reads TMEM lanes 32 (w % 4) .. and columns 64
 // (w / 4) ..), join and run the epilogue.
 //
-// Every wait is bounded (mbar_wait); whatever a role sees, every thread reaches
+// Every wait is bounded; whatever a role sees, every thread reaches
 // both cluster barriers, so no CTA waits for one that left.
 #pragma once
 

