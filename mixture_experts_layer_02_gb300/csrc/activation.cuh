@@ -136,7 +136,9 @@ __device__ __forceinline__ void act_slopes(int fn, float (&z)[N], float (&slope)
         for (int j = 0; j < N; ++j) {
             float m;
             const float x = z[j], p = sigmoid_f32(kGeluTanh2 * (x + kGeluCubic * x * x * x), m);
-            slope[j] = p * (1.0f + x * m * kGeluTanh2 * (1.0f + 3.0f * kGeluCubic * x * x));
+            // m is 0 long before |x| = 64; beyond 1e19 its product with x^2 = infinity would be a NaN
+            const float y = fminf(fmaxf(x, -64.0f), 64.0f);
+            slope[j] = p * (1.0f + y * m * kGeluTanh2 * (1.0f + 3.0f * kGeluCubic * y * y));
             z[j] = x * p;
         }
     } else if (fn == FN_RELU) {

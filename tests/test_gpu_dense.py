@@ -265,10 +265,12 @@ def test_extreme_pre_activations(moe):
     """Slopes far out: 0 or 1, never NaN, for every activation."""
     z = torch.tensor([[-3e38, -1e30, -200.0, -90.0, 90.0, 200.0, 1e30, 3e38]], device="cuda").to(BF16)
     x, w, dy = torch.ones(1, 8, device="cuda", dtype=BF16), torch.eye(8, device="cuda", dtype=BF16), torch.ones_like(z)
-    for fn in ("relu", "silu"):
+    for fn in sorted(R.FNS):
         dx, dw, db = moe.moe_linear_backward(dy, x, w, z=z, fn=R.FNS[fn], need_dbias=True)
         want = R.slope(z.double(), fn)  # at -90 the slope is -89 e^-90, not 0
         assert_within(dx, want, (2 * R.H + R.ACT_EPS) * want.abs(), fn)
+        want = R.act(z.double(), fn)
+        assert_within(moe.moe_linear(z, w, fn=R.FNS[fn])[0], want, (R.H + R.ACT_EPS) * want.abs(), fn)
 
 
 @pytest.mark.parametrize("n", [4, 40, 300])
@@ -439,10 +441,11 @@ def test_more_tiles_than_pairs(moe, n, d, f):
     assert moe.read_device_error(ws) == moe.MOE_OK
 
 
-@pytest.mark.parametrize("kernel", ["1", "2"])
-def test_withheld_load_times_out_and_recovers(moe, kernel, monkeypatch):
+@pytest.mark.parametrize("kernel,split", [("1", "1"), ("1", "4"), ("1", "1282"), ("1", "2561"), ("2", "0")])
+def test_withheld_load_times_out_and_recovers(moe, kernel, split, monkeypatch):
     """A load that never lands: the call ends, says so, and the next one is right."""
     monkeypatch.setenv("MOE_DENSE_KERNEL", kernel)
+    monkeypatch.setenv("MOE_DENSE_SPLIT", split)
     x, w = randn(70, 264, seed=1), randn(136, 264, seed=2, scale=0.1)
     ws = moe.workspace("linear", N=70, D=264, Dff=136)
     want = moe.moe_linear(x, w, ws=ws)[0].clone()
