@@ -45,20 +45,22 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Read once: not kept in L1.
+// Read once: not kept in L1.  A coherent load, like those of x below: weights and x
+// may be what the launch before this one writes while this grid is resident, and
+// the non-coherent path is for data that nothing writes in a grid's lifetime.
 __device__ __forceinline__ uint4 ld_once(const uint16_t* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
     return v;
 }
 
 // NT: groups of eight tokens.
 template <bool GATED, int NT>
 __global__ void __launch_bounds__(kGemvWarps * 32, 2)
-dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w, const uint16_t* __restrict__ w3,
-                  const DenseArgs a) {
+dense_gemv_kernel(const uint16_t* x, const uint16_t* w, const uint16_t* w3, const DenseArgs a) {
     __shared__ float sums[kGemvWarps][NT * 8][kGemvRows + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -86,8 +88,11 @@ dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(hi + k));
             }
         }
-    pdl_trigger();
+    // The next launch may start once every block is past its wait, never before: a
+    // chain of such launches would otherwise be resident several deep, and a grid
+    // that started before its inputs' last writer could find older copies in L1.
     pdl_wait();
+    pdl_trigger();
 
     const uint4 zero = make_uint4(0, 0, 0, 0);
     for (int s0 = warp; s0 < steps; s0 += kGemvWarps * BATCH) {
@@ -109,7 +114,7 @@ dense_gemv_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w
                 for (int j = 0; j < 2; ++j) {
                     const int k = (s0 + b * kGemvWarps) * 64 + j * 32 + t * 8, tok = i * 8 + g;
                     xv[b][i][j] = k < K && tok < a.M
-                                      ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<long long>(tok) * K + k))
+                                      ? *reinterpret_cast<const uint4*>(x + static_cast<long long>(tok) * K + k)
                                       : zero;
                 }
 #pragma unroll
