@@ -196,7 +196,7 @@ __device__ __forceinline__ void gated_quad(const DenseArgs& a, long long row, in
 // y = residual + act(acc + bias) in fp32, rounded once; `res` are the residual's four values.
 __device__ __forceinline__ void linear_quad(const DenseArgs& a, long long row, int col, float (&z)[4], const uint2& res) {
     if (a.bias) {
-        const float4 b = __ldg(reinterpret_cast<const float4*>(a.bias + col));
+        const float4 b = *reinterpret_cast<const float4*>(a.bias + col);
         z[0] += b.x, z[1] += b.y, z[2] += b.z, z[3] += b.w;
     }
     if (a.out1) *quad_of(a.out1, row, a.N, col) = pack_quad(z);
@@ -386,8 +386,8 @@ __device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk&
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
             if (c.col0 + o * 8 >= a.N) break;
-            const float4 b0 = __ldg(reinterpret_cast<const float4*>(a.bias + c.col0 + o * 8));
-            const float4 b1 = __ldg(reinterpret_cast<const float4*>(a.bias + c.col0 + o * 8) + 1);
+            const float4* b = reinterpret_cast<const float4*>(a.bias + c.col0 + o * 8);
+            const float4 b0 = b[0], b1 = b[1];
             z[8 * o] += b0.x, z[8 * o + 1] += b0.y, z[8 * o + 2] += b0.z, z[8 * o + 3] += b0.w;
             z[8 * o + 4] += b1.x, z[8 * o + 5] += b1.y, z[8 * o + 6] += b1.z, z[8 * o + 7] += b1.w;
         }

@@ -6,7 +6,8 @@
 // One pass over the inputs in 16-byte words, bound by HBM and, with GELU, by its
 // arithmetic (777 x 4096 with the bias gradient 7.0 us, 4096 x 4096 24 us).  dg, du and dz are
 // rounded to bf16 once: they are operands of tensor-core products next, which
-// take bf16.  dbias is summed from the unrounded fp32 values.
+// take bf16.  dbias is summed from the unrounded fp32 values.  Coherent loads only (no
+// const __restrict__): the launch before may still be writing them when blocks start.
 #include <algorithm>
 
 #include "activation.cuh"
@@ -25,8 +26,7 @@ int sms() {
 }
 
 __global__ void __launch_bounds__(kGradThreads)
-gated_grad_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ g, const uint4* __restrict__ u, int fn,
-                  long long chunks, uint4* __restrict__ dg, uint4* __restrict__ du) {
+gated_grad_kernel(const uint4* dh, const uint4* g, const uint4* u, int fn, long long chunks, uint4* dg, uint4* du) {
     pdl_wait();
     for (long long i = static_cast<long long>(blockIdx.x) * kGradThreads + threadIdx.x; i < chunks;
          i += static_cast<long long>(gridDim.x) * kGradThreads) {
@@ -55,8 +55,8 @@ gated_grad_kernel(const uint4* __restrict__ dh, const uint4* __restrict__ g, con
 constexpr int kGradParts = 8;
 
 __global__ void __cluster_dims__(1, kGradParts, 1) __launch_bounds__(kGradThreads, 4)
-linear_grad_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z, int fn, long long rows, int cols,
-                   uint16_t* __restrict__ dz, float* __restrict__ dbias) {
+linear_grad_kernel(const uint16_t* dy, const uint16_t* z, int fn, long long rows, int cols, uint16_t* dz,
+                   float* dbias) {
     __shared__ float s_warp[kGradThreads / 32][64];
     __shared__ float s_part[64];
     pdl_wait();

@@ -13,6 +13,9 @@
 // (to 8192) or 1024 threads.  The sum of squares and the row's maximum come out of ONE reduction:
 // y_j is formed as fl(fl(s_j w_j) r) with r > 0 and rounding is monotone, so
 // max|y| = fl(max|fl(s_j w_j)| r) exactly.
+//
+// Every global load here is a coherent one (no __ldg, no const __restrict__): the
+// launch before may still be writing what this one reads when its blocks start.
 #include <algorithm>
 #include <atomic>
 
@@ -56,6 +59,17 @@ __device__ __forceinline__ void row_reduce(float& a, uint32_t& m, float* s_a, ui
     }
 }
 
+// The weight, which every row reads again, among rows that are read once: kept in
+// L1 first.  Without the hint 42.5 instead of 41.2 us at 4096 x 7168.
+__device__ __forceinline__ uint4 ld_kept(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::evict_last.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // T threads a row (32: eight rows in a block of 256), V 16-byte chunks a thread.
 template <int T, int V>
 __global__ void __launch_bounds__(T < 256 ? 256 : T)
@@ -80,7 +94,7 @@ rmsnorm_kernel(const NormArgs a) {
             const bool in = c < chunks;
             xv[i] = in ? xr[c] : make_uint4(0, 0, 0, 0);
             rv[i] = in && a.residual ? rr[c] : make_uint4(0, 0, 0, 0);
-            wv[i] = in ? __ldg(wrow + c) : make_uint4(0, 0, 0, 0);
+            wv[i] = in ? ld_kept(wrow + c) : make_uint4(0, 0, 0, 0);
         }
         float sw[V][8];
         float sum = 0.0f;
@@ -384,7 +398,7 @@ rmsnorm_bwd_wide_kernel(const NormBwdArgs a) {
             float s[8], d[8], w[8];
             unpack_bf16x8(sv[i], s);
             unpack_bf16x8(dv[i], d);
-            unpack_bf16x8(c < chunks ? __ldg(wrow + c) : make_uint4(0, 0, 0, 0), w);
+            unpack_bf16x8(c < chunks ? wrow[c] : make_uint4(0, 0, 0, 0), w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 s2 += s[j] * s[j];
@@ -417,7 +431,7 @@ rmsnorm_bwd_wide_kernel(const NormBwdArgs a) {
             float s[8], d[8], w[8], e[8], dx[8];
             unpack_bf16x8(sv[i], s);
             unpack_bf16x8(dv[i], d);
-            unpack_bf16x8(__ldg(wrow + c), w);
+            unpack_bf16x8(wrow[c], w);
             unpack_bf16x8(a.dresidual ? reinterpret_cast<const uint4*>(a.dresidual)[r * chunks + c] : make_uint4(0, 0, 0, 0), e);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -443,7 +457,7 @@ rmsnorm_bwd_wide_kernel(const NormBwdArgs a) {
 // 32 columns a block, 32 threads a column: thread y sums parts y, y + 32, ... in
 // order, then the 32 sums are added in order.
 __global__ void __launch_bounds__(1024)
-column_sums_kernel(const float* __restrict__ partial, int parts, int cols, float* __restrict__ out) {
+column_sums_kernel(const float* partial, int parts, int cols, float* out) {
     __shared__ float s[32][33];
     pdl_wait();
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), y = threadIdx.x >> 5;
