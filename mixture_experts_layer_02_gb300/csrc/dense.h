@@ -117,12 +117,11 @@ inline cudaError_t dense_split(DenseKind kind, const CUtensorMap* m, const Dense
 constexpr int kGemvMaxRows = 32;
 cudaError_t launch_dense_gemv(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st);
 
-// CTA pairs on 256 x 256 tiles, persistent: clusters of one pair (cluster = 2)
-// or of two pairs one above the other (4).
+// CTA pairs on 256 x 256 tiles, persistent: one pair a cluster.
 constexpr int kPairTile = 256;
 // clusters the device holds at once
-cudaError_t dense_pair_limit(DenseKind kind, int cluster, int* clusters);
-cudaError_t launch_dense_pair(DenseKind kind, const CUtensorMap* maps, const DenseArgs& a, int cluster, int clusters,
+cudaError_t dense_pair_limit(DenseKind kind, int* clusters);
+cudaError_t launch_dense_pair(DenseKind kind, const CUtensorMap* maps, const DenseArgs& a, int clusters,
                               cudaStream_t st);
 
 }  // namespace moe

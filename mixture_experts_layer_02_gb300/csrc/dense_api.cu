@@ -95,27 +95,35 @@ BackwardLayout backward_layout(int N, int F, int grads) {
 uint8_t* at(void* ws, size_t off) { return static_cast<uint8_t*>(ws) + off; }
 
 // ---- the choice of kernel ----
-// Estimated microseconds, fitted to times measured on GB300 over 33 to 4096 rows
-// and K of 768 to 16384 (within about 10 % of each): rounds over the clusters
-// that fit the device, each k-blocks (64 of K) times the time of one, plus first
-// load, join and epilogue.
+// Estimated microseconds of the product alone: rounds over the clusters that fit
+// the device, each k-blocks (64 of K) times the time of one, plus first load, join
+// and epilogue.  Fitted to times measured on GB300 over 33 to 4096 rows and K of 768
+// to 16384; whole tiles and pairs again over 24 products of 64 to 1792 tiles and K of
+// 2 to 14336, most within 10 %, the worst 21 % off (4096 x 2048 x 768 gated: 29.3 for
+// 24.2).  What the estimates leave out is the same for every form: the activation,
+// a kept pre-activation (1001 x 4096 x 2056 takes 18 us, with bias, GELU and z 22.7),
+// and the clock under the power limit.
 struct TileKind {
-    int bn;                        // 0: one CTA, 128 x 128; else a pair, 256 x bn
-    double block, whole, joined;   // a k-block; the rest of a round with K whole or in parts
+    int bn;                                // 0: one CTA, 128 x 128; else a pair, 256 x bn
+    double whole_block, whole;             // K whole: a k-block, the rest of a round
+    double block, joined;                  // K in parts
 };
-constexpr TileKind kSplitTiles[3] = {{0, 0.24, 3.6, 4.5}, {128, 0.206, 5.0, 7.2}, {256, 0.30, 5.0, 10.3}};
+constexpr TileKind kSplitTiles[3] = {{0, 0.24, 3.6, 0.24, 4.5}, {128, 0.206, 5.0, 0.206, 7.2}, {256, 0.325, 5.1, 0.30, 10.3}};
 constexpr double kJoinRows = 2.5, kJoinEight = 1.0;  // one-CTA tiles: a join of all 128 rows, of eight parts
-constexpr double kPairBlock = 0.32, kPairRound = 1.5, kPairOnce = 4.5;  // persistent pairs
-constexpr double kMulticastRate = 0.97;              // of the block, where two pairs share an operand
+// Persistent pairs.  Over several rounds they beat whole 256 x 256 tiles, whose
+// epilogue no main loop hides (4096^3 92 against 105 us, 4096 x 14336 x 4096 304
+// against 314); in one round the whole tile ends earlier where K is short (weight
+// gradient 777 x 1024 x 4096: 8.6 against 9.2).
+constexpr double kPairBlock = 0.308, kPairRound = 2.0, kPairOnce = 5.7;
 // The streamed form (M <= kGemvMaxRows) reads x once a block of 16 weight rows:
 // weights at the HBM rate, or weights and x at the L2 rate that 240 blocks and
 // more reach, whichever takes longer.  MB a microsecond is TB a second.
 constexpr double kHbmRate = 6.3, kGemvL2Rate = 10.0, kGemvBlocks = 240.0, kGemvOnce = 2.4;
 
 struct Plan {
-    int bn, splits;         // split tiles
-    int cluster, clusters;  // persistent pairs (cluster 0: split tiles)
-    bool stream;            // the streamed form instead
+    int bn, splits;  // split tiles
+    int pairs;       // persistent pairs instead, where not 0
+    bool stream;     // the streamed form instead
 };
 
 int env_int(const char* name, int dflt) {
@@ -124,12 +132,12 @@ int env_int(const char* name, int dflt) {
 }
 
 // MOE_DENSE_KERNEL = 1 (split tiles), 2 (persistent pairs) or 3 (streamed weights,
-// where M allows), and with it MOE_DENSE_SPLIT = 10 * bn + splits and MOE_DENSE_CLUSTER = 2 or
-// 4 force a choice, for tuning and test coverage.
+// where M allows), and with it MOE_DENSE_SPLIT = 10 * bn + splits force a choice, for
+// tuning and test coverage.
 moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p) {
     const int n2 = kind == DENSE_GATED ? 128 : 256;
     const int kernel = env_int("MOE_DENSE_KERNEL", 0);
-    *p = {0, 1, 0, 0, false};
+    *p = {0, 1, 0, false};
     const bool forward = kind == DENSE_GATED || kind == DENSE_LINEAR;
     const double weights = 2e-6 * a.N * a.K * (kind == DENSE_GATED ? 2 : 1);  // MB
     // up to eight rows x is at most half of what the weights are: nothing came near the streamed form
@@ -138,7 +146,6 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
         return MOE_OK;
     }
     const int fixed = kernel ? env_int("MOE_DENSE_SPLIT", -1) : -1;
-    const int only = kernel ? env_int("MOE_DENSE_CLUSTER", 0) : 0;
     double best = 1e30;
     for (const TileKind& t : kSplitTiles) {
         const int rows = t.bn ? 2 * kBM : kBM, width = (t.bn ? t.bn : 128) / (kind == DENSE_GATED ? 2 : 1);
@@ -149,10 +156,11 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
             int limit = 0;
             const moe_status st = launched(dense_split(kind, nullptr, a, t.bn, s, nullptr, &limit), "dense split limit");
             if (st != MOE_OK) return st;
+            const double block = s == 1 ? t.whole_block : t.block;
             double rest = s == 1 ? t.whole : t.joined;
             if (s > 1 && t.bn == 0) rest += kJoinRows * std::min(a.M, kBM) / kBM + (s == 8 ? kJoinEight : 0.0);
             const double rounds = static_cast<double>((tiles + limit - 1) / limit);
-            const double c = std::max(rounds * kblocks * t.block / s, forward ? weights / kHbmRate : 0.0) + rounds * rest;
+            const double c = std::max(rounds * kblocks * block / s, forward ? weights / kHbmRate : 0.0) + rounds * rest;
             if (c < best) {
                 best = c;
                 p->bn = t.bn;
@@ -170,22 +178,15 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
             p->stream = true;
         }
     }
-    if (kernel == 2) best = 1e30;
-    for (int cl = 2; cl <= 4; cl += 2) {
-        if (only && only != cl) continue;
-        int limit = 0;
-        const moe_status st = launched(dense_pair_limit(kind, cl, &limit), "dense pair limit");
-        if (st != MOE_OK) return st;
-        const int rows = kPairTile * cl / 2;
-        const long long tiles = static_cast<long long>((a.M + rows - 1) / rows) * ((a.N + n2 - 1) / n2) * a.mats;
-        const double block = kPairBlock * (cl == 2 ? 1.0 : kMulticastRate);
-        const double c = static_cast<double>((tiles + limit - 1) / limit) * (kblocks * block + kPairRound) + kPairOnce;
-        if (c < best) {
-            best = c;
-            p->stream = false;
-            p->cluster = cl;
-            p->clusters = static_cast<int>(std::min<long long>(tiles, limit));
-        }
+    int limit = 0;
+    const moe_status st = launched(dense_pair_limit(kind, &limit), "dense pair limit");
+    if (st != MOE_OK) return st;
+    const long long tiles =
+        static_cast<long long>((a.M + kPairTile - 1) / kPairTile) * ((a.N + n2 - 1) / n2) * a.mats;
+    const double c = static_cast<double>((tiles + limit - 1) / limit) * (kblocks * kPairBlock + kPairRound) + kPairOnce;
+    if (c < best || kernel == 2) {
+        p->stream = false;
+        p->pairs = static_cast<int>(std::min<long long>(tiles, limit));
     }
     return MOE_OK;
 }
@@ -199,7 +200,7 @@ moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, c
     if (planned != MOE_OK) return planned;
     if (p.stream) return launched(launch_dense_gemv(kind, o, a, st), "dense product launch");
     // K-major boxes: 128 rows of A; of B what one CTA loads at a time
-    const int b_rows = p.cluster ? 256 / p.cluster : (p.bn ? p.bn / 2 : (kind == DENSE_GATED ? 64 : 128));
+    const int b_rows = p.pairs ? 128 : (p.bn ? p.bn / 2 : (kind == DENSE_GATED ? 64 : 128));
     CUtensorMap m[4];
     auto map_a = [&](CUtensorMap* t, const uint16_t* q) {
         return a_mn ? make_bf16_map(t, q, a.K, a.M, 64) : make_bf16_map(t, q, a.M, a.K, kBM);
@@ -214,8 +215,8 @@ moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, c
     if (s != 0) return static_cast<moe_status>(s);
     if (!o.a1) m[1] = m[0];
     if (!o.b1) m[3] = m[2];
-    if (!p.cluster) return launched(dense_split(kind, m, a, p.bn, p.splits, st), "dense product launch");
-    return launched(launch_dense_pair(kind, m, a, p.cluster, p.clusters, st), "dense pair product launch");
+    if (!p.pairs) return launched(dense_split(kind, m, a, p.bn, p.splits, st), "dense product launch");
+    return launched(launch_dense_pair(kind, m, a, p.pairs, st), "dense pair product launch");
 }
 
 DenseArgs args_of(int M, int N, int K, void* ws) {

@@ -49,17 +49,6 @@ __host__ __device__ constexpr uint32_t dense_idesc(int M, int N) {
     return idesc_bf16_f32(M, N) | (DenseLayout<KIND>::A_MN ? 1u << 15 : 0u) | (DenseLayout<KIND>::B_MN ? 1u << 16 : 0u);
 }
 
-// tma_load_2d_pair into the CTAs of `mask` at the same offset; each copy's bytes
-// are counted in the destination's pair, on the CTA of bar_cluster's parity.
-__device__ __forceinline__ void tma_load_2d_pair_multicast(const CUtensorMap* map, uint32_t bar_cluster, void* dst, int x,
-                                                           int y, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
-        " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "h"(mask)
-        : "memory");
-}
-
 // ---- waiting ----
 // Waits on an mbarrier are polls, and polls of one SM queue up behind one
 // another: with six to eight warps polling for the end of a main loop, each wait

@@ -17,17 +17,8 @@
 // pipe from 89 to 95 .. 97 % of the active cycles: 498 us alone at 4096 x 4096 x
 // 2 x 14336 keeping both projections (1.93 PFLOP/s), 575 us in a long run, where
 // the board's power limit holds the clock near 1.5 GHz (1.67 PFLOP/s; a library
-// product of 8192^3 runs at 1.71 there).
-//
-// Sharing an operand.  With four CTAs to a cluster (CL = 4), two pairs take
-// m-tiles one above the other and the same columns: each CTA loads half of its B
-// half and multicasts it to the CTA of the other pair that needs the same, so L2
-// is read 48 instead of 64 bytes a clock and SM.  A stage is then free when both
-// pairs' MMAs have read it (two commits on `empty`).  36 clusters of four hold
-// 144 of the 152 SMs.  It gains 1 to 3 % where the rounds of tiles come out alike
-// (4096 x 14336 x 4096: 303 against 310 us) and loses where they do not (weight
-// gradient 4096 x 2048 x 7168: 82 against 74), so the plan goes by the rounds.
-// Asking L2 for later k-blocks ahead made every size 8 to 14 % slower.
+// product of 8192^3 runs at 1.71 there).  Asking L2 for later k-blocks ahead made
+// every size 8 to 14 % slower.
 //
 // A last round that leaves pairs idle was dealt out along K over all of them (with
 // fp32 fragments joined through memory): 273 instead of 297 us alone at 4096 x
@@ -56,34 +47,27 @@ constexpr int kStageBytes = 2 * kOperand;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (3 + kEpiWarps) * 32;  // A copies, MMA issuer, epilogue, B copies
 constexpr int kBand = 8;
-constexpr int kQuarter = kOperand / 2;           // what a CTA of a cluster of four loads of its B half
 constexpr size_t kPairSmem = 1024 + static_cast<size_t>(kStages) * kStageBytes + kEpiWarps * kChunkBytes + (2 * kStages + 5) * 8 + 16;
-
-// Row tiles of a cluster's tile: one pair's 256 rows, or two pairs' 512.
-template <int CL>
-constexpr int kTileRows = kPairTile * CL / 2;
 
 // Tile t of the list, as its first row and column; mats products follow one another.
 struct TilePlace {
     int mat, m0, n0;
 };
 
-template <int CL>
 __device__ __forceinline__ TilePlace place_tile(int t, int mt, int nt, int n_tile) {
-    constexpr int B = kBand * kPairTile / kTileRows<CL>;
     TilePlace w;
     w.mat = t / (mt * nt);
     t -= w.mat * mt * nt;
-    const int band = t / (B * nt), in = t - band * B * nt;
-    const int rows = min(B, mt - band * B);
+    const int band = t / (kBand * nt), in = t - band * kBand * nt;
+    const int rows = min(kBand, mt - band * kBand);
     const int n = in / rows;
-    w.m0 = (band * B + in - n * rows) * kTileRows<CL>;
+    w.m0 = (band * kBand + in - n * rows) * kPairTile;
     w.n0 = n * n_tile;
     return w;
 }
 
-template <int KIND, int CL>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kThreads, 1)
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                   const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                   const DenseArgs a) {
@@ -103,16 +87,15 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t crank = cluster_ctarank();  // in the cluster
-    const uint32_t rank = crank & 1u, lead = crank & ~1u;  // in the pair; the pair's even CTA issues its MMAs
+    const uint32_t rank = cluster_ctarank();  // in the pair; its even CTA issues the MMAs
     const bool leader = rank == 0;
-    const uint16_t both = static_cast<uint16_t>(0x3u << lead), all = static_cast<uint16_t>((1u << CL) - 1u);
+    constexpr uint16_t both = 0x3;
     uint32_t* err = a.err;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], CL / 2);
+            mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
@@ -133,10 +116,10 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     const uint32_t tmem_base = *tmem_slot;
     const int kbs = (a.K + kBK - 1) / kBK;
     const int total_kb = kbs * a.segs;
-    const int mt = (a.M + kTileRows<CL> - 1) / kTileRows<CL>, nt = (a.N + N_TILE - 1) / N_TILE;
-    const int tiles = mt * nt * a.mats, first = blockIdx.x / CL, step = gridDim.x / CL;
-    const uint32_t full_lead = mapa_shared(smem_u32(full), lead);
-    const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), lead);
+    const int mt = (a.M + kPairTile - 1) / kPairTile, nt = (a.N + N_TILE - 1) / N_TILE;
+    const int tiles = mt * nt * a.mats, first = blockIdx.x / 2, step = gridDim.x / 2;
+    const uint32_t full_lead = mapa_shared(smem_u32(full), 0);
+    const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), 0);
     pdl_wait();
 
     if (warp == 0) {  // copies of A; the even CTA's also announces the stage's bytes
@@ -147,8 +130,8 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             uint32_t phase = 0;
             bool ok = true;
             for (int tile = first; ok && tile < tiles; tile += step) {
-                const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
-                const int arow = w.m0 + static_cast<int>(crank) * kBM;
+                const TilePlace w = place_tile(tile, mt, nt, N_TILE);
+                const int arow = w.m0 + static_cast<int>(rank) * kBM;
                 for (int kb = 0; kb < total_kb; ++kb) {
                     if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
                     if (withhold) {
@@ -182,7 +165,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             uint32_t phase = 0;
             bool ok = true;
             for (int tile = first; ok && tile < tiles; tile += step) {
-                const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
+                const TilePlace w = place_tile(tile, mt, nt, N_TILE);
                 const int bcol = w.n0 + (L::GATED ? 0 : static_cast<int>(rank) * (kPairTile / 2));
                 for (int kb = 0; kb < total_kb; ++kb) {
                     if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
@@ -190,13 +173,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     const uint32_t bar = full_lead + 8u * stage;
                     uint8_t* dB = sB + stage * kOperand;
                     const CUtensorMap* mB = L::GATED ? (rank ? &tmB1 : &tmB0) : (L::B_MN && seg ? &tmB1 : &tmB0);
-                    if constexpr (CL == 4) {  // half of the B half, to both CTAs of this parity
-                        const int part = static_cast<int>(crank >> 1);
-                        const uint16_t mask = static_cast<uint16_t>(0x5u << rank);
-                        const int b64 = bcol + part * 64;
-                        tma_load_2d_pair_multicast(mB, bar, dB + part * kQuarter, L::B_MN ? b64 : k0, L::B_MN ? k0 : b64,
-                                                   mask);
-                    } else if constexpr (L::B_MN) {
+                    if constexpr (L::B_MN) {
                         tma_load_2d_pair(mB, bar, dB, bcol, k0);
                         tma_load_2d_pair(mB, bar, dB + kMnBlockBytes, bcol + 64, k0);
                     } else {
@@ -229,7 +206,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                         for (int k = 0; k < kBK / 16; ++k)
                             umma_bf16_pair(d, ad + k * kDescStep<L::A_MN>, bd + k * kDescStep<L::B_MN>, idesc,
                                            (kb | k) != 0 ? 1u : 0u);
-                        umma_commit_pair_multicast(&empty[w.stage], all);
+                        umma_commit_pair_multicast(&empty[w.stage], both);
                     }
                     __syncwarp();
                     w.advance();
@@ -252,8 +229,8 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = first; tile < tiles; tile += step) {
-            const TilePlace w = place_tile<CL>(tile, mt, nt, N_TILE);
-            WholeEpilogue<KIND, kPairTile> e{a, stage_smem, w.m0 + static_cast<int>(crank) * kBM, w.n0, q, half, lane, {}};
+            const TilePlace w = place_tile(tile, mt, nt, N_TILE);
+            WholeEpilogue<KIND, kPairTile> e{a, stage_smem, w.m0 + static_cast<int>(rank) * kBM, w.n0, q, half, lane, {}};
             e.fetch_ahead();
             const bool ok = warp != 2 || lane != 0 || idle_wait(&tfull[acc], acc_phase, abort_flag, err);
             __syncwarp();
@@ -280,7 +257,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     }
 }
 
-template <int KIND, int CL>
+template <int KIND>
 cudaError_t pair_prepare(int* clusters) {
     static std::atomic<unsigned long long> done{0};
     static int limit[64];
@@ -289,15 +266,15 @@ cudaError_t pair_prepare(int* clusters) {
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(dense_pair_kernel<KIND, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(dense_pair_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kPairSmem));
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(CL);
+        cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = kPairSmem;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<KIND, CL>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, dense_pair_kernel<KIND>, &cfg);
         if (e != cudaSuccess) return e;
         limit[dev & 63] = n;
         done.fetch_or(bit, std::memory_order_acq_rel);
@@ -306,36 +283,33 @@ cudaError_t pair_prepare(int* clusters) {
     return *clusters > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
-template <int KIND, int CL>
+template <int KIND>
 cudaError_t pair_go(const CUtensorMap* m, const DenseArgs& a, int clusters, cudaStream_t st) {
     int limit = 0;
-    cudaError_t e = pair_prepare<KIND, CL>(&limit);
+    cudaError_t e = pair_prepare<KIND>(&limit);
     if (e != cudaSuccess) return e;
     if (clusters > limit) return cudaErrorInvalidConfiguration;
-    return launch_kernel(dense_pair_kernel<KIND, CL>, dim3(CL * clusters), dim3(kThreads), kPairSmem, st, m[0], m[1], m[2],
+    return launch_kernel(dense_pair_kernel<KIND>, dim3(2 * clusters), dim3(kThreads), kPairSmem, st, m[0], m[1], m[2],
                          m[3], a);
 }
 
 }  // namespace
 
-cudaError_t dense_pair_limit(DenseKind kind, int cluster, int* clusters) {
-    const bool two = cluster == 2;
+cudaError_t dense_pair_limit(DenseKind kind, int* clusters) {
     switch (kind) {
-        case DENSE_GATED: return two ? pair_prepare<DENSE_GATED, 2>(clusters) : pair_prepare<DENSE_GATED, 4>(clusters);
-        case DENSE_LINEAR: return two ? pair_prepare<DENSE_LINEAR, 2>(clusters) : pair_prepare<DENSE_LINEAR, 4>(clusters);
-        case DENSE_DGRAD: return two ? pair_prepare<DENSE_DGRAD, 2>(clusters) : pair_prepare<DENSE_DGRAD, 4>(clusters);
-        default: return two ? pair_prepare<DENSE_WGRAD, 2>(clusters) : pair_prepare<DENSE_WGRAD, 4>(clusters);
+        case DENSE_GATED: return pair_prepare<DENSE_GATED>(clusters);
+        case DENSE_LINEAR: return pair_prepare<DENSE_LINEAR>(clusters);
+        case DENSE_DGRAD: return pair_prepare<DENSE_DGRAD>(clusters);
+        default: return pair_prepare<DENSE_WGRAD>(clusters);
     }
 }
 
-cudaError_t launch_dense_pair(DenseKind kind, const CUtensorMap* m, const DenseArgs& a, int cluster, int clusters,
-                              cudaStream_t st) {
-    const bool two = cluster == 2;
+cudaError_t launch_dense_pair(DenseKind kind, const CUtensorMap* m, const DenseArgs& a, int clusters, cudaStream_t st) {
     switch (kind) {
-        case DENSE_GATED: return two ? pair_go<DENSE_GATED, 2>(m, a, clusters, st) : pair_go<DENSE_GATED, 4>(m, a, clusters, st);
-        case DENSE_LINEAR: return two ? pair_go<DENSE_LINEAR, 2>(m, a, clusters, st) : pair_go<DENSE_LINEAR, 4>(m, a, clusters, st);
-        case DENSE_DGRAD: return two ? pair_go<DENSE_DGRAD, 2>(m, a, clusters, st) : pair_go<DENSE_DGRAD, 4>(m, a, clusters, st);
-        default: return two ? pair_go<DENSE_WGRAD, 2>(m, a, clusters, st) : pair_go<DENSE_WGRAD, 4>(m, a, clusters, st);
+        case DENSE_GATED: return pair_go<DENSE_GATED>(m, a, clusters, st);
+        case DENSE_LINEAR: return pair_go<DENSE_LINEAR>(m, a, clusters, st);
+        case DENSE_DGRAD: return pair_go<DENSE_DGRAD>(m, a, clusters, st);
+        default: return pair_go<DENSE_WGRAD>(m, a, clusters, st);
     }
 }
 

@@ -15,8 +15,7 @@
 //   - Time stamps at 256 x 4096 x 4096 (S = 2, 32 k-blocks a CTA) showed a TMA
 //     round trip of 1.1 us: three 32 KB stages moved a k-block each 0.37 us, six
 //     (one CTA an SM) and separate copy threads each 0.23 us.  That is what an SM
-//     takes in (64 bytes a clock), so sharing operand tiles over a cluster by
-//     multicast, which was built and measured, changed nothing here.
+//     takes in (64 bytes a clock), whichever SM or L2 it comes from.
 //   - With K in parts, 4 to 5 us follow the main loop: parking 0.5, barrier 0.6,
 //     sums 1.4 (one latency of loads from other CTAs), epilogue 0.2 a row of quads,
 //     barrier 0.6.  The loads are all in flight at once, rows are dealt to the CTAs

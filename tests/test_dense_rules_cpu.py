@@ -48,3 +48,12 @@ def test_no_loads_through_the_non_coherent_path(name):
     text = source(name)
     for word in (".nc.", ".nc ", "__ldg", "__restrict__"):
         assert word not in text, word
+
+
+@pytest.mark.parametrize("name", sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))))
+def test_no_load_into_several_ctas(name):
+    """Every bulk copy lands in one CTA: the library is also loaded by replica processes on several GPUs, where a copy
+    with cluster multicast has no place.  (Barrier signals to both CTAs of a pair are no copies.)"""
+    for m in re.finditer(r"\basm\b.*?;\s*\n", source(name), flags=re.S):
+        if "cp.async.bulk" in m.group(0):
+            assert "multicast" not in m.group(0)
