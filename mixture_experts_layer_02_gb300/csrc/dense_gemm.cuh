@@ -56,15 +56,24 @@ __host__ __device__ constexpr uint32_t dense_idesc(int M, int N) {
 // k-block of 256 to 512 clocks of MMA.  So during a main loop only its producer
 // and its MMA issuer poll (pipe_wait); one thread waits for the accumulator,
 // asleep between polls (idle_wait), and everybody else stands at a hardware
-// barrier.  Both end after kWaitLimitNs.
+// barrier.  pipe_wait ends after kWaitLimitNs.  idle_wait spans a whole main loop,
+// which a long K takes past any fixed limit: it ends kWaitLimitNs after the last
+// change of `progress`, which follows this CTA's copies of A (each behind a bounded
+// wait, so the changes end too).
 __device__ __forceinline__ bool pipe_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
     return mbar_wait(bar, parity, abort, err);
 }
 
-__device__ __forceinline__ bool idle_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-    const uint64_t t0 = globaltimer_ns();
+__device__ __forceinline__ bool idle_wait(uint64_t* bar, uint32_t parity, volatile int* abort, const volatile int* progress,
+                                          uint32_t* err) {
+    uint64_t t0 = globaltimer_ns();
+    int seen = *progress;
     while (!mbar_test_wait(bar, parity)) {
         if (*abort) return false;
+        if (*progress != seen) {
+            seen = *progress;
+            t0 = globaltimer_ns();
+        }
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
             *abort = 1;
             record_error(err, MOE_DEVERR_TIMEOUT);

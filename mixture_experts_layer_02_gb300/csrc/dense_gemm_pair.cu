@@ -85,6 +85,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* progress = abort_flag + 1;  // changes with every 256th k-block whose copy of A was issued
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();  // in the pair; its even CTA issues the MMAs
@@ -103,6 +104,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
+        *progress = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -153,6 +155,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                             tma_load_2d_pair(mA, bar, dA, k0, arow);
                         }
                     }
+                    if ((kb & 255) == 255) *progress = kb;
                     if (++stage == S) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -220,7 +223,6 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             if (elect_one()) umma_commit_pair_multicast(drain, both);
             __syncwarp();
         }
-        if (lane == 0) drain_wait(drain, 0, err);  // the pair MMAs wrote this CTA's TMEM too
     } else {
         // epilogue warp (q, half): TMEM lanes 32 q .., accumulator columns [0, 128) or [128, 256);
         // gated: 64 gate columns and the 64 up columns that belong to them
@@ -232,7 +234,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             const TilePlace w = place_tile(tile, mt, nt, N_TILE);
             WholeEpilogue<KIND, kPairTile> e{a, stage_smem, w.m0 + static_cast<int>(rank) * kBM, w.n0, q, half, lane, {}};
             e.fetch_ahead();
-            const bool ok = warp != 2 || lane != 0 || idle_wait(&tfull[acc], acc_phase, abort_flag, err);
+            const bool ok = warp != 2 || lane != 0 || idle_wait(&tfull[acc], acc_phase, abort_flag, progress, err);
             __syncwarp();
             if (!named_barrier_and(1, kEpiWarps * 32, ok)) break;  // given up: by all of them
             tc_fence_after();
@@ -249,6 +251,11 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
     pdl_trigger();
     tc_fence_before();
     __syncthreads();
+    // The pair's MMAs wrote this CTA's TMEM: they have ended.  Asked for here, when
+    // every role of the CTA is through: from the start of a launch the odd CTA would
+    // poll under every main loop and give a product of more than kWaitLimitNs up.
+    if (threadIdx.x == 32) drain_wait(drain, 0, err);
+    __syncwarp();
     cluster_sync_all();  // no CTA leaves while another of the cluster may still signal it
     if (warp == 1) {
         __syncwarp();

@@ -60,6 +60,7 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
     uint64_t* done = empty + S;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* progress = abort_flag + 1;  // changes with every 256th k-block whose copy of A was issued
     volatile int never = 0;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -75,6 +76,7 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
         }
         mbar_init(done, 1);
         *abort_flag = 0;
+        *progress = 0;
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -126,6 +128,7 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
                         tma_load_2d_pair(mA, bar, sA, kb * kBK, m0);
                     }
                 }
+                if ((n & 255) == 0) *progress = n;
                 if (++kb == kbs) { kb = 0; ++seg; }
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
@@ -176,7 +179,7 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
         }
         if (lane == 0) {
             // to the end whatever happened: TMEM is released below, nothing may be in flight
-            idle_wait(done, 0, &never, a.err);
+            idle_wait(done, 0, &never, progress, a.err);
         }
     }
     if constexpr (RES > 0) {

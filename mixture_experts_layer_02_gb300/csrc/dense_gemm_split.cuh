@@ -179,7 +179,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         __syncwarp();
         if (lane == 0) {
             // to the end whatever happened: TMEM is released below, nothing may be in flight
-            idle_wait(done, 0, &never, a.err);
+            idle_wait(done, 0, &never, &never, a.err);
         }
     }
     if constexpr (RES > 0) {
