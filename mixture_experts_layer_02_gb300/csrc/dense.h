@@ -38,6 +38,7 @@ struct NormBwdArgs {
     int D;
     float eps;
     uint32_t* err;              // workspace error word
+    const uint32_t* dbg;        // test flags
 };
 // Row groups whose dweight sums are kept apart (the workspace's size; the same on every device).
 int rmsnorm_bwd_parts(long long rows, int D);

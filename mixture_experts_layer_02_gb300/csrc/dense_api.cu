@@ -286,7 +286,7 @@ moe_status moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* s_in, const 
     NEED(dx);
     NEED_WS(dense_workspace_size("rmsnorm_backward", N, D, 0));
     const NormBwdArgs a = {dy, s_in, weight, dresidual, dx, dweight, reinterpret_cast<float*>(at(ws, kWsHeaderBytes)),
-                           N, D, eps, static_cast<uint32_t*>(ws)};
+                           N, D, eps, static_cast<uint32_t*>(ws), static_cast<const uint32_t*>(ws) + 1};
     return launched(launch_rmsnorm_bwd(a, st), "rmsnorm backward launch");
 }
 

@@ -192,8 +192,8 @@ cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t st) {
 // with four (rows above 8192; registers would spill: 46 us instead of 28 at
 // 4093 x 4096) it is read from the stage again and the next row's barrier frees it.
 // The arithmetic is done on pairs (fma.rn.f32x2), which halves it.  Measured: 4093
-// x 4096 26.1 us (5.1 TB/s; the second kernel is 3 us of it), 16384 x 7168 142 us
-// (6.6 TB/s).
+// x 4096 26.5 us (5.1 TB/s; the second kernel is 3 us of it), 16384 x 7168 140 us
+// (6.7 TB/s).
 struct NormBwdShape {
     int v;         // 16-byte chunks a thread: 1, 2 or 4
     int threads;   // T: threads of a group (a multiple of 32)
@@ -227,6 +227,14 @@ __device__ __forceinline__ float2 bf16_pair(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
 
+// After a wait that ran out (a second): copies whose barrier nobody waits for any
+// more land long before this ends, or never.  Nothing of the block's shared memory is
+// used again or given back before.
+__device__ __forceinline__ void settle_copies() {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kWaitLimitNs / 100) __nanosleep(1000);
+}
+
 template <int V>
 __global__ void __launch_bounds__(kNormBwdThreads, 1)
 rmsnorm_bwd_ring_kernel(const NormBwdArgs a, const NormBwdShape sh) {
@@ -259,8 +267,11 @@ rmsnorm_bwd_ring_kernel(const NormBwdArgs a, const NormBwdShape sh) {
         bulk_load_1d(at + row_bytes, a.dy + r * a.D, row_bytes, &full[st]);
         if (a.dresidual) bulk_load_1d(at + 2 * row_bytes, a.dresidual + r * a.D, row_bytes, &full[st]);
     };
-    if (lane == 0)
-        for (int i = 0; i < sh.stages; ++i) fill(i);
+    if (lane == 0) {
+        const bool first = row0 == 0;  // only this group reads the test hook: it is a load ahead of a copy
+        for (int i = first ? 1 : 0; i < sh.stages; ++i) fill(i);
+        if (first && !(*a.dbg & MOE_DBG_WITHHOLD_FIRST_LOAD)) fill(0);
+    }
     uint4 wv[V];
     float2 dw[V][4];
 #pragma unroll
@@ -273,9 +284,13 @@ rmsnorm_bwd_ring_kernel(const NormBwdArgs a, const NormBwdShape sh) {
     const float inv_d = 1.0f / static_cast<float>(a.D);
     int stage = 0;
     uint32_t phase = 0;
+    // A wait that ran out is recorded and ends its group's copies: a stage is filled
+    // again only after it was seen full.  The rows left are walked through all the same
+    // (no wait takes time any more).
     long long i = 0;
+    bool live = true;
     for (long long r = row0; r < a.rows; r += step, ++i) {
-        mbar_wait(&full[stage], phase, &s_abort, a.err);  // a wait that ran out is recorded; the loop goes on
+        live = mbar_wait(&full[stage], phase, &s_abort, a.err) && live;
         const uint4* ps = reinterpret_cast<const uint4*>(mine + static_cast<size_t>(stage) * 3 * row_bytes);
         const uint4* pd = ps + chunks;
         const uint4* pe = pd + chunks;
@@ -315,7 +330,7 @@ rmsnorm_bwd_ring_kernel(const NormBwdArgs a, const NormBwdShape sh) {
         } else {
             __syncwarp();
         }
-        if (lane == 0) {
+        if (lane == 0 && live) {
             if (KEEP) fill(i + sh.stages);  // every thread holds its part of this stage
             else if (i > 0) fill(i - 1 + sh.stages);  // every thread has left the previous row's stage
         }
@@ -343,6 +358,7 @@ rmsnorm_bwd_ring_kernel(const NormBwdArgs a, const NormBwdShape sh) {
         }
         if (++stage == sh.stages) { stage = 0; phase ^= 1u; }
     }
+    if (s_abort) settle_copies();
     pdl_trigger();
     if (a.dweight) {  // the groups' sums, added in group order
         __syncthreads();  // no copy is in flight: every filled stage has been waited for

@@ -40,3 +40,29 @@ def test_a_tile_of_more_than_a_second(moe, kernel, split, monkeypatch):
     assert moe.read_device_error(ws) == moe.MOE_OK
     assert torch.equal(dw, want.to(BF16))
     assert start.elapsed_time(end) > 1000.0, "the product has to outlast the limit"
+
+
+def randn(*shape, seed=0, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed * 7919 + sum((i + 1) * n for i, n in enumerate(shape)))
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(BF16)
+
+
+@pytest.mark.parametrize("n,d", [(5000, 256), (3000, 520), (1500, 4096), (700, 16384)])
+@pytest.mark.parametrize("down", [False, True])
+def test_norm_gradient_gives_up_and_recovers(moe, n, d, down):
+    """A row whose copies never start: the call ends, says so, and the next one is right.  One, two and four chunks a
+    thread, one and several groups a block."""
+    dy, s, w = randn(n, d, seed=1, scale=0.1), randn(n, d, seed=2), randn(d, seed=3) + 1
+    dres = randn(n, d, seed=4) if down else None
+    ws = moe.workspace("rmsnorm_backward", N=n, D=d)
+    want = [t.clone() for t in moe.moe_rmsnorm_backward(dy, s, w, dresidual=dres, ws=ws)]
+    assert moe.read_device_error(ws) == moe.MOE_OK
+    moe.set_debug_flags(ws, 1)
+    moe.moe_rmsnorm_backward(dy, s, w, dresidual=dres, ws=ws)
+    assert moe.read_device_error(ws) == moe.MOE_ERR_DEVICE_TIMEOUT
+    moe.set_debug_flags(ws, 0)
+    moe.clear_device_error(ws)
+    for a, b in zip(moe.moe_rmsnorm_backward(dy, s, w, dresidual=dres, ws=ws), want):
+        assert torch.equal(a, b)
+    assert moe.read_device_error(ws) == moe.MOE_OK
