@@ -5,6 +5,7 @@
 #include "activation.cuh"
 #include "dense.h"
 #include "gemm_common.cuh"
+#include "settle.cuh"
 
 namespace moe {
 

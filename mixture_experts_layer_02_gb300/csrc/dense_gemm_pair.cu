@@ -161,6 +161,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
             }
             for (int s = 0; s < S; ++s)
                 if (pending & (1u << s)) drain_wait(&full[s], (pend_parity >> s) & 1u, err);
+            if (!ok) settle_copies();
         }
     } else if (warp == 2 + kEpiWarps) {  // copies of B
         if (lane == 0) {
@@ -185,6 +186,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constan
                     if (++stage == S) { stage = 0; phase ^= 1u; }
                 }
             }
+            if (!ok) settle_copies();  // some may be of stages that were never announced
         }
     } else if (warp == 1) {
         if (leader) {

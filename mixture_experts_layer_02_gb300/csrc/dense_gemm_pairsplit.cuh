@@ -108,8 +108,9 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
             uint32_t pending = 0, pend_parity = 0;
             int stage = 0, seg = k_lo / kbs, kb = k_lo - seg * kbs;
             uint32_t phase = 0;
+            bool ok = true;
             for (int n = k_hi - k_lo; n > 0; --n) {
-                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) break;
+                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) { ok = false; break; }
                 if (withhold) {
                     withhold = false;  // test hook: this stage never fills
                 } else {
@@ -134,14 +135,16 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
             }
             for (int s = 0; s < S; ++s)
                 if (pending & (1u << s)) drain_wait(&full[s], (pend_parity >> s) & 1u, a.err);
+            if (!ok) settle_copies();
         }
     } else if (warp == 2) {  // copies of B
         if (lane == 0) {
             const int bcol = n0 + (L::GATED ? 0 : static_cast<int>(rank) * (BN / 2));
             int stage = 0, seg = k_lo / kbs, kb = k_lo - seg * kbs;
             uint32_t phase = 0;
+            bool ok = true;
             for (int n = k_hi - k_lo; n > 0; --n) {
-                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) break;
+                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) { ok = false; break; }
                 const uint32_t bar = full_lead + 8u * stage;
                 uint8_t* sB = smem + stage * C::STAGE + kPsA;
                 const CUtensorMap* mB = L::GATED ? (rank ? &tmB1 : &tmB0) : (L::B_MN && seg ? &tmB1 : &tmB0);
@@ -154,6 +157,7 @@ dense_pairsplit_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_co
                 if (++kb == kbs) { kb = 0; ++seg; }
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
+            if (!ok) settle_copies();  // some may be of stages that were never announced
         }
     } else if (warp == 1) {
         if (leader) {

@@ -114,8 +114,9 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
             uint32_t pending = 0, pend_parity = 0;
             int stage = 0, seg = k_lo / kbs, kb = k_lo - seg * kbs;
             uint32_t phase = 0;
+            bool ok = true;
             for (int n = k_hi - k_lo; n > 0; --n) {
-                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) break;
+                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) { ok = false; break; }
                 if (withhold) {
                     withhold = false;  // test hook: this stage never fills
                 } else {
@@ -136,13 +137,15 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
             }
             for (int s = 0; s < S; ++s)
                 if (pending & (1u << s)) drain_wait(&full[s], (pend_parity >> s) & 1u, a.err);
+            if (!ok) settle_copies();
         }
     } else if (warp == 2) {  // copies of B
         if (lane == 0) {
             int stage = 0, seg = k_lo / kbs, kb = k_lo - seg * kbs;
             uint32_t phase = 0;
+            bool ok = true;
             for (int n = k_hi - k_lo; n > 0; --n) {
-                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) break;
+                if (!pipe_wait(&empty[stage], phase ^ 1u, abort_flag, a.err)) { ok = false; break; }
                 uint8_t* sB = smem + stage * kSplitStageBytes + kOperandBytes;
                 if constexpr (L::GATED) {
                     tma_load_2d(&tmB0, &full[stage], sB, kb * kBK, n0);
@@ -157,6 +160,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
                 if (++kb == kbs) { kb = 0; ++seg; }
                 if (++stage == S) { stage = 0; phase ^= 1u; }
             }
+            if (!ok) settle_copies();  // some may be of stages that were never announced
         }
     } else if (warp == 1) {
         constexpr uint32_t idesc = dense_idesc<KIND>(kBM, kSplitBN);

@@ -22,6 +22,7 @@
 #include "activation.cuh"
 #include "dense.h"
 #include "quant.cuh"
+#include "settle.cuh"
 
 namespace moe {
 
@@ -226,14 +227,6 @@ __device__ __forceinline__ float2 bf16_pair(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
-
-// After a wait that ran out (a second): copies whose barrier nobody waits for any
-// more land long before this ends, or never.  Nothing of the block's shared memory is
-// used again or given back before.
-__device__ __forceinline__ void settle_copies() {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < kWaitLimitNs / 100) __nanosleep(1000);
-}
 
 template <int V>
 __global__ void __launch_bounds__(kNormBwdThreads, 1)

@@ -66,3 +66,56 @@ def test_norm_gradient_gives_up_and_recovers(moe, n, d, down):
     for a, b in zip(moe.moe_rmsnorm_backward(dy, s, w, dresidual=dres, ws=ws), want):
         assert torch.equal(a, b)
     assert moe.read_device_error(ws) == moe.MOE_OK
+
+
+#: one-CTA tiles and pair tiles with K whole and in parts, persistent pairs
+TILES = [("1", "1"), ("1", "4"), ("1", "1281"), ("1", "2562"), ("2", "0")]
+
+
+@pytest.mark.parametrize("kernel,split", TILES)
+@pytest.mark.parametrize("kind", ["gated", "linear", "dgrad", "dgrad2", "wgrad", "wgrad2"])
+def test_withheld_load_of_every_kind(moe, kind, kernel, split, monkeypatch):
+    """A load that never lands in each kind of product on each kind of tile: the call ends, says so, and the next one
+    is right.  dgrad2 sums two products, wgrad2 has two outputs.  K is 9 to 18 k-blocks: more than the
+    stages of the whole tiles."""
+    monkeypatch.setenv("MOE_DENSE_KERNEL", kernel)
+    monkeypatch.setenv("MOE_DENSE_SPLIT", split)
+    m, wide, k = 300, 264, 568
+    n, d, f = {"gated": (m, k, wide), "linear": (m, k, wide), "dgrad": (m, wide, k), "dgrad2": (m, wide, k),
+               "wgrad": (k, wide, m - 4), "wgrad2": (k, wide, m - 4)}[kind]
+    x, w1, w3 = randn(n, d, seed=1), randn(f, d, seed=2, scale=d ** -0.5), randn(f, d, seed=3, scale=d ** -0.5)
+    g, u, dy = randn(n, f, seed=4), randn(n, f, seed=5), randn(n, f, seed=6, scale=0.1)
+    op = {"gated": "gated_linear", "linear": "linear", "dgrad": "linear_backward", "wgrad": "linear_backward"}.get(
+        kind, "gated_linear_backward")
+    ws = moe.workspace(op, N=n, D=d, Dff=f)
+    L, size, st = moe.load(), ws.numel(), torch.cuda.current_stream().cuda_stream
+    outs = [torch.zeros(n, f, device="cuda", dtype=BF16)] if kind in ("gated", "linear") else \
+        [torch.zeros(n, d, device="cuda", dtype=BF16)] if kind.startswith("dgrad") else \
+        [torch.zeros(f, d, device="cuda", dtype=BF16) for _ in range(2 if kind == "wgrad2" else 1)]
+    a = [t.data_ptr() for t in (x, w1, w3, g, u, dy, ws)]
+    o = [t.data_ptr() for t in outs]
+
+    def call():
+        xp, p1, p3, gp, up, dp, wp = a
+        status = {
+            "gated": lambda: L.moe_gated_linear(xp, p1, p3, n, d, f, moe.FN_SILU, o[0], None, None, wp, size, st),
+            "linear": lambda: L.moe_linear(xp, p1, None, None, n, d, f, moe.FN_NONE, o[0], None, wp, size, st),
+            "dgrad": lambda: L.moe_linear_backward(dp, xp, p1, None, n, d, f, moe.FN_NONE, o[0], None, None, wp, size, st),
+            "wgrad": lambda: L.moe_linear_backward(dp, xp, p1, None, n, d, f, moe.FN_NONE, None, o[0], None, wp, size, st),
+            "dgrad2": lambda: L.moe_gated_linear_backward(dp, xp, p1, p3, gp, up, n, d, f, moe.FN_SILU, o[0], None, None, wp,
+                                                          size, st),
+            "wgrad2": lambda: L.moe_gated_linear_backward(dp, xp, p1, p3, gp, up, n, d, f, moe.FN_SILU, None, o[0], o[1], wp,
+                                                          size, st)}[kind]()
+        assert status == moe.MOE_OK
+
+    call()
+    assert moe.read_device_error(ws) == moe.MOE_OK
+    want = [t.clone() for t in outs]
+    moe.set_debug_flags(ws, 1)
+    call()
+    assert moe.read_device_error(ws) == moe.MOE_ERR_DEVICE_TIMEOUT
+    moe.clear_device_error(ws)
+    call()
+    assert moe.read_device_error(ws) == moe.MOE_OK
+    for t, ref in zip(outs, want):
+        assert torch.equal(t, ref) and t.isfinite().all() and (t != 0).any()
