@@ -406,7 +406,8 @@ moe_status moe_routing_stats(const int32_t* expert_offsets, int E, float decay, 
  * the norm in front of it, a dense gated expert beside the routed ones (a
  * shared expert) and the projection onto the residual stream, each with its
  * gradient.  bf16 tensors, fp32 sums; widths are positive multiples of 8 (rows
- * start on 16-byte boundaries), any number of rows.  The pages describe the
+ * start on 16-byte boundaries), any number of rows (the products: up to 2^31 -
+ * 4096 in each dimension and below 2^40 elements a tensor).  The pages describe the
  * layer's inside only, so there is no passage to cite: the formulas below are
  * the definitions.  The gradient entry points compute each output whose pointer
  * is not NULL; with N = 0 the weight gradients are set to zero.

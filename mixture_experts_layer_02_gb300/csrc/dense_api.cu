@@ -54,9 +54,15 @@ bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) !
             return refuse(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need_); \
     } while (0)
 
+// Largest size of a dimension: rounded up to whole tiles, or walked past its end by a
+// batch of steps (up to 1600 columns, dense_gemv.cu), it stays below 2^31.
+constexpr int kDimLimit = 0x7fffffff - 4095;
+
 // rows * width stays below 2^40, tile counts below 2^31
 moe_status check_widths(int N, int D, int F) {
     if (N < 0) return refuse(MOE_ERR_INVALID_ARG, "N=%d < 0", N);
+    if (std::max({N, D, F}) > kDimLimit)
+        return refuse(MOE_ERR_INVALID_ARG, "N=%d, D=%d, F=%d: above %d", N, D, F, kDimLimit);
     if (D < 8 || D % 8) return refuse(MOE_ERR_INVALID_ARG, "D=%d not a positive multiple of 8", D);
     if (F < 8 || F % 8) return refuse(MOE_ERR_INVALID_ARG, "F=%d not a positive multiple of 8", F);
     if (static_cast<long long>(N) * std::max(D, F) >= (1LL << 40) || static_cast<long long>(D) * F >= (1LL << 40))

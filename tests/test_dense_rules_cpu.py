@@ -57,3 +57,36 @@ def test_no_load_into_several_ctas(name):
     for m in re.finditer(r"\basm\b.*?;\s*\n", source(name), flags=re.S):
         if "cp.async.bulk" in m.group(0):
             assert "multicast" not in m.group(0)
+
+
+# ------------------------------------------------------------------ sizes whose tile arithmetic would leave 32 bits
+@pytest.fixture(scope="module")
+def lib():
+    from mixture_experts_layer_02_gb300 import build, moe
+    build.build()
+    return moe.load()
+
+
+LAST = 2 ** 31 - 8  # the largest multiple of 8 that an int holds
+
+
+@pytest.mark.parametrize("N,D,F", [(LAST, 8, 8), (2 ** 31 - 1, 8, 8), (2 ** 31 - 4095, 8, 8), (4, LAST, 8), (4, 8, LAST),
+                                   (40, LAST, 8), (40, 8, LAST)])
+def test_products_refuse_sizes_past_their_tile_arithmetic(lib, N, D, F):
+    """Sizes rounded up to whole tiles or batches of steps have to stay below 2^31.  Placeholders for pointers: no call may reach a launch."""
+    X, WS, big = 4096, 8192, 1 << 62
+    assert lib.moe_gated_linear(X, X, X, N, D, F, 2, X, None, None, WS, big, None) == 1
+    assert lib.moe_linear(X, X, None, None, N, D, F, 0, X, None, WS, big, None) == 1
+    assert lib.moe_gated_linear_backward(X, X, X, X, X, X, N, D, F, 2, X, X, X, WS, big, None) == 1
+    assert lib.moe_linear_backward(X, X, X, None, N, D, F, 0, X, X, None, WS, big, None) == 1
+    from mixture_experts_layer_02_gb300 import moe
+    for op in ("gated_linear", "linear", "gated_linear_backward", "linear_backward"):
+        assert moe.workspace_size(op, N=N, D=D, Dff=F) == 0
+    assert b"above 2147479552" in lib.moe_last_error_detail()
+
+
+def test_products_take_sizes_up_to_there(lib):
+    from mixture_experts_layer_02_gb300 import moe
+    assert moe.workspace_size("linear", N=2 ** 31 - 4096, D=8, Dff=8) == 256
+    assert moe.workspace_size("linear_backward", N=2 ** 31 - 4096, D=8, Dff=8) == 256 + (2 ** 31 - 4096) * 16
+    assert moe.workspace_size("linear", N=4, D=2 ** 31 - 4096, Dff=8) == 256
