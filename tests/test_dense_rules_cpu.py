@@ -73,7 +73,8 @@ LAST = 2 ** 31 - 8  # the largest multiple of 8 that an int holds
 @pytest.mark.parametrize("N,D,F", [(LAST, 8, 8), (2 ** 31 - 1, 8, 8), (2 ** 31 - 4095, 8, 8), (4, LAST, 8), (4, 8, LAST),
                                    (40, LAST, 8), (40, 8, LAST)])
 def test_products_refuse_sizes_past_their_tile_arithmetic(lib, N, D, F):
-    """Sizes rounded up to whole tiles or batches of steps have to stay below 2^31.  Placeholders for pointers: no call may reach a launch."""
+    """Sizes rounded up to whole tiles or batches of steps have to stay below 2^31.  Placeholders for pointers: no call
+    may reach a launch."""
     X, WS, big = 4096, 8192, 1 << 62
     assert lib.moe_gated_linear(X, X, X, N, D, F, 2, X, None, None, WS, big, None) == 1
     assert lib.moe_linear(X, X, None, None, N, D, F, 0, X, None, WS, big, None) == 1
