@@ -8,7 +8,9 @@
 
 ``out`` and ``s`` are the next block's x and residual.  ``Block.train_step``
 runs the norm and the shared expert forward and backward and applies plain
-gradient descent (the routed experts are inference only).
+gradient descent (the routed experts are inference only).  The block keeps its
+workspaces, so that ``Block.check`` can say whether a kernel gave up: a call
+without one drops the error word with it.
 
     python examples/ffn_block.py [--tokens N]
 """
@@ -35,6 +37,7 @@ class Block:
     w1: torch.Tensor           # [shared, D]
     w3: torch.Tensor
     w2: torch.Tensor           # [D, shared]
+    kept: dict = dataclasses.field(default_factory=dict)  # workspaces of each operation, the largest last
 
     @classmethod
     def make(cls, wl: synth.Workload, shared: int, seed: int = 0, device="cuda") -> "Block":
@@ -49,35 +52,58 @@ class Block:
                    moe.quantize_experts_e4m3(inp["w1"], inp["w3"], inp["w2"]), normal(shared, wl.D), normal(shared, wl.D),
                    normal(wl.D, shared))
 
+    def ws(self, op: str, N: int, **sizes) -> torch.Tensor:
+        """A workspace for ``op``, made anew only where the last one is too small."""
+        have = self.kept.setdefault(op, [])
+        if not have or have[-1].numel() < moe.workspace_size(op, N=N, **sizes):
+            have.append(moe.workspace(op, N=N, **sizes))
+        return have[-1]
+
+    def check(self):
+        """Wait for the GPU; raise if a kernel of this block recorded an error since the last check."""
+        for op, have in self.kept.items():
+            for w in have:
+                status = moe.read_device_error(w)
+                if status != moe.MOE_OK:
+                    moe.clear_device_error(w)
+                    raise moe.MoEError(op, status, "recorded by a kernel of this block")
+
     def routed(self, y, yq, scale):
         """The MoE layer on the norm's bf16 rows (router) and codes (experts)."""
-        wl, e = self.wl, self.experts
-        ids, w = moe.moe_route(y, self.w_gate, None, wl.K, wl.mode)
-        offsets, src, inv, rows = moe.moe_permute_e4m3(yq, ids, wl.E)
+        wl, e, N = self.wl, self.experts, y.shape[0]
+        ids, w = moe.moe_route(y, self.w_gate, None, wl.K, wl.mode, ws=self.ws("route", N, D=wl.D, E=wl.E, K=wl.K))
+        offsets, src, inv, rows = moe.moe_permute_e4m3(yq, ids, wl.E, ws=self.ws("permute", N, E=wl.E))
         y_perm = moe.moe_grouped_ffn_e4m3(rows, scale, src, offsets, e["w1q"], e["s1"], e["w3q"], e["s3"], e["w2q"], e["s2"],
-                                          wl.act)[3]
-        return moe.moe_combine(y_perm, inv, w)
+                                          wl.act, ws=self.ws("ffn", N * wl.K, D=wl.D, E=wl.E, K=1, Dff=wl.Dff))[3]
+        return moe.moe_combine(y_perm, inv, w, ws=self.ws("combine", 0))
+
+    def dense_ws(self, op: str, y) -> torch.Tensor:
+        up = op.startswith("gated")
+        D, F = (self.wl.D, self.shared) if up else (self.shared, self.wl.D)
+        return self.ws(op, y.shape[0], D=D, Dff=F)
 
     def forward(self, x, residual):
         """(out, s) of N tokens, one or many."""
         y, yq, scale, s = moe.moe_rmsnorm(x, self.norm, residual=residual, quantize=True)
-        h, _, _ = moe.moe_gated_linear(y, self.w1, self.w3)
-        out, _ = moe.moe_linear(h, self.w2, residual=self.routed(y, yq, scale))
+        h, _, _ = moe.moe_gated_linear(y, self.w1, self.w3, ws=self.dense_ws("gated_linear", y))
+        out, _ = moe.moe_linear(h, self.w2, residual=self.routed(y, yq, scale), ws=self.dense_ws("linear", y))
         return out, s
 
     def dense(self, x, residual):
         """The block without its routed experts, and what its backward pass keeps."""
         y, _, _, s = moe.moe_rmsnorm(x, self.norm, residual=residual)
-        h, g, u = moe.moe_gated_linear(y, self.w1, self.w3, save=True)
-        out, _ = moe.moe_linear(h, self.w2, residual=s)
+        h, g, u = moe.moe_gated_linear(y, self.w1, self.w3, save=True, ws=self.dense_ws("gated_linear", y))
+        out, _ = moe.moe_linear(h, self.w2, residual=s, ws=self.dense_ws("linear", y))
         return out, (y, s, h, g, u)
 
     def dense_backward(self, dout, kept):
         """Gradients (dx, dnorm, dw1, dw3, dw2) of the dense block; dx is x's and the residual's."""
         y, s, h, g, u = kept
-        dh, dw2, _ = moe.moe_linear_backward(dout, h, self.w2)
-        dy, dw1, dw3 = moe.moe_gated_linear_backward(dh, y, self.w1, self.w3, g, u)
-        dx, dnorm = moe.moe_rmsnorm_backward(dy, s, self.norm, dresidual=dout)
+        dh, dw2, _ = moe.moe_linear_backward(dout, h, self.w2, ws=self.dense_ws("linear_backward", y))
+        dy, dw1, dw3 = moe.moe_gated_linear_backward(dh, y, self.w1, self.w3, g, u,
+                                                     ws=self.dense_ws("gated_linear_backward", y))
+        dx, dnorm = moe.moe_rmsnorm_backward(dy, s, self.norm, dresidual=dout,
+                                             ws=self.ws("rmsnorm_backward", y.shape[0], D=self.wl.D))
         return dx, dnorm, dw1, dw3, dw2
 
     def train_step(self, x, residual, target, lr: float) -> torch.Tensor:
@@ -106,6 +132,7 @@ def main():
         loss = block.train_step(x, residual, target, lr=5.0)
         if step % 5 == 0 or step == 19:
             print(f"step {step:2d}  loss {loss.item():.4f}")
+    block.check()
 
 
 if __name__ == "__main__":

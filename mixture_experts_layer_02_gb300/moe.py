@@ -8,7 +8,9 @@ Functions carry the C names (``moe_route``, ``moe_permute``,
 ``moe_grouped_ffn``, ``moe_combine``, ``moe_layer_forward``) and take torch
 tensors that already live on the current CUDA device.  Outputs not passed in
 are allocated here with torch.  ``ws`` is a workspace tensor from
-:func:`workspace`; pass the same one again to avoid re-allocating.
+:func:`workspace`; pass the same one again to avoid re-allocating, and to be
+able to ask :func:`read_device_error` whether a kernel gave up: a call without
+one makes its own and drops it, the device's error word included.
 """
 from __future__ import annotations
 
