@@ -447,6 +447,8 @@ moe_status moe_rmsnorm(const moe_bf16* x, const moe_bf16* residual, const moe_bf
  *                                              residual alike)
  *   dweight = sum over rows of dy s r
  *   dy [N,D] bf16; s [N,D] bf16: what moe_rmsnorm wrote to residual_out (or x);
+ *   r is taken from this bf16 s, while moe_rmsnorm normalised the unrounded sum:
+ *   with a residual the two differ by that one rounding;
  *   dresidual [N,D] bf16 or NULL: the gradient that reached residual_out;
  *   dx [N,D] bf16 out; dweight [D] fp32 out or NULL (summed in a fixed order). */
 moe_status moe_rmsnorm_backward(const moe_bf16* dy, const moe_bf16* s, const moe_bf16* weight,

@@ -139,7 +139,8 @@ int env_int(const char* name, int dflt) {
 
 // MOE_DENSE_KERNEL = 1 (split tiles), 2 (persistent pairs) or 3 (streamed weights,
 // where M allows), and with it MOE_DENSE_SPLIT = 10 * bn + splits force a choice, for
-// tuning and test coverage.
+// tuning and test coverage.  Parts that K does not allow fall back to one-CTA tiles
+// with K whole.
 moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p) {
     const int n2 = kind == DENSE_GATED ? 128 : 256;
     const int kernel = env_int("MOE_DENSE_KERNEL", 0);

@@ -322,7 +322,7 @@ __device__ __forceinline__ const uint4* octet(const uint16_t* base, long long ro
 // tcgen05.ld leaves one accumulator row in each thread.  Stored as it lies, a
 // warp's 16-byte store touches 32 rows at once, half a sector each; the kernel
 // that keeps g and u was bound by that (83 us of 656 at 4096 x 4096 x 14336; they
-// cost 18 of 574 now).  So a chunk goes through shared memory and leaves (and a
+// cost 25 to 37 of 580 now).  So a chunk goes through shared memory and leaves (and a
 // residual enters) as 64-byte pieces of eight rows.  The 16-byte pieces of a row
 // are permuted so that both directions use all banks.
 constexpr int kChunkBytes = 32 * 128;  // 64-byte rows here, 128-byte rows in plain_chunk

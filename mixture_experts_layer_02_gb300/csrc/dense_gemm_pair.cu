@@ -14,9 +14,9 @@
 // the answer of a barrier that was complete.  So A and B have a copy thread each,
 // the MMA warp walks the stages as a whole with the next barrier asked ahead
 // (StageWalk), and no other warp polls during a main loop.  That took the tensor
-// pipe from 89 to 95 .. 97 % of the active cycles: 498 us alone at 4096 x 4096 x
-// 2 x 14336 keeping both projections (1.93 PFLOP/s), 575 us in a long run, where
-// the board's power limit holds the clock near 1.5 GHz (1.67 PFLOP/s; a library
+// pipe from 89 to 95 .. 96 % of the active cycles: 505 us alone at 4096 x 4096 x
+// 2 x 14336 keeping both projections (1.90 PFLOP/s), 576 to 587 us in a long run,
+// where the board's power limit holds the clock near 1.5 GHz (1.65 PFLOP/s; a library
 // product of 8192^3 runs at 1.71 there).  Asking L2 for later k-blocks ahead made
 // every size 8 to 14 % slower.
 //
