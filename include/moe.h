@@ -88,6 +88,9 @@ typedef enum { MOE_ACT_SILU = 0, MOE_ACT_SWIGLU = 1 } moe_act;
  *           multiples of 128)
  *   rmsnorm_backward N, D; gated_linear, linear, gated_linear_backward,
  *           linear_backward N, D, Dff (the dense operators below)
+ *   route_backward N, D, E; grouped_linear_e4m3_block and
+ *           grouped_linear_e4m3_block_backward N = total_rows, D, E, Dff = F
+ *           (header only); the other training operators take that of combine
  * The sizes do not depend on the device. */
 size_t moe_workspace_size(const char* op, int N, int D, int E, int K, int Dff);
 
@@ -486,6 +489,118 @@ moe_status moe_linear(const moe_bf16* x, const moe_bf16* w, const float* bias, c
 moe_status moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, const moe_bf16* w, const moe_bf16* z, int N,
                                int D, int F, int fn, moe_bf16* dx, moe_bf16* dw, float* dbias, void* ws,
                                size_t ws_bytes, void* stream);
+
+/* ---- Training the routed layer.  The gradients of moe_combine, moe_permute and
+ * moe_route, and the experts' products in e4m3 with a scale for each block of
+ * 128, with their gradients.  The pages describe inference only, so there is no
+ * passage to cite: the formulas below are the definitions.  Sums are fp32 and in
+ * a fixed order (the same call gives the same bits); outputs overlap no input
+ * except where said.  Gradient entry points compute each output whose pointer is
+ * not NULL; of no rows, weight gradients are zero. */
+
+/* Gradient of moe_combine (and of moe_combine_padded, inv_perm being its slot):
+ *   dy_perm[inv_perm[t,k], :] = topk_w[t,k] * dout[t, :]
+ *   dtopk_w[t,k] = sum over d of dout[t,d] * y_perm[inv_perm[t,k], d]
+ *   dout [N,D] bf16; y_perm [rows,D] bf16 (NULL allowed without dtopk_w);
+ *   inv_perm [N,K] int32: -1 is an assignment without a row (dtopk_w 0), other
+ *   entries outside 0..rows-1 are skipped and flagged MOE_ERR_DEVICE_BOUNDS; no
+ *   row is named twice; topk_w [N,K] fp32
+ *   dy_perm [rows,D] bf16 out or NULL, may be y_perm itself; rows that no entry
+ *   names are left as they were; dtopk_w [N,K] fp32 out or NULL
+ *   D a positive multiple of 8, K <= 32; ws as for "combine". */
+moe_status moe_combine_backward(const moe_bf16* dout, const moe_bf16* y_perm, const int32_t* inv_perm,
+                                const float* topk_w, int N, int D, int K, int rows, moe_bf16* dy_perm,
+                                float* dtopk_w, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_permute (and of moe_permute_padded) for the tokens:
+ *   dx[t, :] = dresidual[t, :] + sum over k of dx_perm[inv_perm[t,k], :]
+ *   dx_perm [rows,D] bf16; inv_perm, D, K and ws as for moe_combine_backward;
+ *   dresidual [N,D] bf16 or NULL: the gradient that reached x otherwise
+ *   dx [N,D] bf16 out (may be dresidual itself), summed in fp32 in k order. */
+moe_status moe_permute_backward(const moe_bf16* dx_perm, const int32_t* inv_perm, const moe_bf16* dresidual, int N,
+                                int D, int K, int rows, moe_bf16* dx, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of moe_route through the weights (the selection itself has none):
+ *   c = sum over k of topk_w[t,k] dtopk_w[t,k]
+ *   dl[t, topk_ids[t,k]] = topk_w[t,k] (dtopk_w[t,k] - c), and with sigmoid scores
+ *                          times 1 - sigmoid(logits[t, topk_ids[t,k]])
+ *   dx = dresidual + dl w_gate;  dw_gate = dl^T x;  dbias[e] = sum over t of dl[t,e]
+ *   dtopk_w, topk_w [N,K] fp32, topk_ids [N,K] int32 (ids outside 0..E-1 are
+ *   skipped and flagged; an id named twice counts twice); logits [N,E] fp32: what
+ *   moe_route wrote to logits_out, read with MOE_SCORE_SIGMOID_NORM only;
+ *   x [N,D], w_gate [E,D] bf16; dresidual [N,D] bf16 or NULL
+ *   dx [N,D] bf16 out or NULL (may be dresidual itself), dw_gate [E,D] bf16 out or
+ *   NULL, dbias [E] fp32 out or NULL (from the unrounded dl; dl is rounded to bf16
+ *   as an operand of the two products)
+ *   D a positive multiple of 8, any E up to 1024; ws as for "route_backward". */
+moe_status moe_route_backward(const float* dtopk_w, const int32_t* topk_ids, const float* topk_w, const float* logits,
+                              const moe_bf16* x, const moe_bf16* w_gate, const moe_bf16* dresidual, int N, int D, int E,
+                              int K, int mode, moe_bf16* dx, moe_bf16* dw_gate, float* dbias, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* e4m3 codes with one scale for each block of 128 of a bf16 tensor [mats, rows,
+ * cols]: block_rows = 1: 1 x 128 (activations), scale [mats, rows, ceil(cols/128)];
+ * block_rows = 128: 128 x 128 inside each matrix (weights), scale [mats,
+ * ceil(rows/128), ceil(cols/128)].  q has src's shape.  The rule of
+ * moe_quantize_e4m3, by block: scale = 2^k, k the smallest integer >= -126 with
+ * max|block| <= 448 * 2^k.  The last block of a row or column may be short; cols is
+ * a positive multiple of 16. */
+moe_status moe_quantize_e4m3_block(const moe_bf16* src, int mats, int rows, int cols, int block_rows, uint8_t* q,
+                                   float* scale, void* stream);
+
+/* Rows of the buffers below for total_rows rows of E experts, whatever the
+ * routing: (total_rows + 127 min(total_rows, E)) / 128 * 128; -1 on invalid sizes. */
+long long moe_segment_rows(int total_rows, int E);
+
+/* The same codes along an expert's rows, for the weight gradient, which sums over
+ * them: blocks of 128 x 1 inside each segment, whose rows start at a multiple of
+ * 128 in q_seg (segment e at 128 times the sum over e' < e of ceil(rows of e' / 128))
+ * with zero codes behind them up to the next one; and in the same pass the 1 x 128
+ * form that moe_quantize_e4m3_block writes.
+ *   src [total_rows, cols] bf16; expert_offsets [E+1] or NULL with E = 1 (all rows).
+ *   Offsets that do not start at 0, decrease or pass total_rows write nothing and
+ *   are flagged MOE_ERR_DEVICE_BOUNDS
+ *   q [total_rows, cols], scale [total_rows, ceil(cols/128)] out, or both NULL
+ *   q_seg [moe_segment_rows, cols], scale_seg [moe_segment_rows / 128, cols] out;
+ *   rows behind the last segment are left as they were (in q and scale too)
+ *   ws as for "combine". */
+moe_status moe_quantize_e4m3_segments(const moe_bf16* src, const int32_t* expert_offsets, int total_rows, int cols,
+                                      int E, uint8_t* q, float* scale, uint8_t* q_seg, float* scale_seg, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* The experts' product in e4m3 with a scale for each block of 128 of both operands:
+ *   y[r,f] = sum over blocks b of D of x_scale[s(r), b] w_scale[e, f/128, b]
+ *            * (sum over d in b of xq[r,d] wq[e,f,d])        for the rows r of expert e
+ *   xq [total_rows, D] codes; x_scale [x_scale_rows, ceil(D/128)] fp32, any value;
+ *   s(r) = x_scale_index[r], or r where that is NULL: perm_src of moe_permute_e4m3
+ *   finds the scales that stayed in token order (indices outside 0..x_scale_rows-1
+ *   are flagged and count as scale 0)
+ *   expert_offsets [E+1] (checked as above) or NULL with E = 1: a dense product
+ *   wq [E,F,D] codes, w_scale [E, ceil(F/128), ceil(D/128)] fp32
+ *   y [total_rows, F] bf16 out; rows behind the last segment are left as they were
+ * Each block's partial sum is scaled and added in fp32.  D and F are positive
+ * multiples of 16, E <= 1024. */
+moe_status moe_grouped_linear_e4m3_block(const uint8_t* xq, const float* x_scale, const int32_t* x_scale_index,
+                                         int x_scale_rows, const int32_t* expert_offsets, int total_rows,
+                                         const uint8_t* wq, const float* w_scale, int E, int D, int F, moe_bf16* y,
+                                         void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients, from quantised operands (the weights as in the forward pass):
+ *   dx[r,d]   = sum over blocks b of F of dy_scale[r,b] w_scale[e, b, d/128]
+ *               * (sum over f in b of dyq[r,f] wq[e,f,d])
+ *   dw[e,f,d] = sum over blocks b of e's padded rows of dy_scale_seg[b,f]
+ *               x_scale_seg[b,d] * (sum over r in b of dyq_seg[r,f] xq_seg[r,d])
+ *   dyq, dy_scale: the 1 x 128 form of dy [total_rows, F]; dyq_seg, dy_scale_seg and
+ *   xq_seg, x_scale_seg: what moe_quantize_e4m3_segments wrote for dy and x
+ *   dx [total_rows, D] bf16 out or NULL (then dyq, dy_scale, wq and w_scale may be
+ *   NULL); dw [E,F,D] bf16 out or NULL (then the four others may be NULL); experts
+ *   without rows get zeros. */
+moe_status moe_grouped_linear_e4m3_block_backward(const uint8_t* dyq, const float* dy_scale, const uint8_t* dyq_seg,
+                                                  const float* dy_scale_seg, const uint8_t* xq_seg,
+                                                  const float* x_scale_seg, const int32_t* expert_offsets,
+                                                  int total_rows, const uint8_t* wq, const float* w_scale, int E,
+                                                  int D, int F, moe_bf16* dx, moe_bf16* dw, void* ws,
+                                                  size_t ws_bytes, void* stream);
 
 /* Number of kernels moe_layer_forward (capacity < 0) or
  * moe_layer_forward_padded (capacity >= 0) launches for these sizes on the

@@ -1,0 +1,570 @@
+// block_gemm.cuh -- products in e4m3 with a scale for each block of 128, grouped over
+// the experts' segments, and their gradients (block_gemm.h has the formulas).
+//
+// A scale that changes along K cannot wait for the end of the sum: the tensor cores
+// sum 128 products, the block's partial sum is scaled and added in fp32 on the CUDA
+// cores, and so on.  So the accumulator lives in registers and TMEM holds a ring of
+// partial sums: the MMA warp fills slot after slot (four MMAs of 32 a slot, the first
+// one overwriting), and eight epilogue warps, one row a thread, read a slot, free it
+// and add scale * partial with paired fp32 arithmetic.  The additions have a fixed
+// order; the scales are any fp32 numbers.
+//
+// What bounds it.  A 256 x 256 x 128 step of a CTA pair is 512 clocks of MMA on each
+// SM; reading its 128 x 256 partial sums from TMEM and adding them is 256 clocks of
+// each, on other pipes, so the tensor pipe stays the limit for many rows.  For few
+// rows an expert the weights' stream is the limit, and a warp whose 32 rows all lie
+// behind the segment only frees its slots.
+//
+// Operands are read as stored, nothing is transposed in memory: FWD has both K-major,
+// DGRAD the weights MN-major, WGRAD both MN-major, its K being an expert's rows from a
+// multiple of 128 on with zero rows behind them (quant_block.cu).  Boxes are 128 x 128
+// bytes; what lies outside a matrix reads as zeros, so K needs no multiple.
+//
+// Warps: 0 copies A, 1 issues the MMAs, 2 copies B, 3 allocates TMEM, 4..11 epilogue.
+// Registers are dealt out anew at the start: the epilogue's accumulators take 128.
+// Barriers: full[s] the bytes of a stage (of both CTAs, on the even one's), empty[s]
+// its MMAs are done, tfull[i] a slot is filled, tempty[i] its readers are through.
+// Every wait is bounded (1 s); none spans more than one step of 128 along K.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include "activation.cuh"
+#include "block_gemm.h"
+#include "gemm_common.cuh"
+#include "settle.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 12 * 32;
+constexpr int kBoxBytes = kBlock * kRowBytes;  // 128 rows of 128 bytes
+constexpr int kStageRoom = 192 * 1024;
+constexpr int kChunk = 2048;                   // an epilogue warp's staging: 32 rows of 64 bytes
+constexpr int kMaxE = 1024;
+constexpr int kCopyRegs = 88, kEpiRegs = 208;  // registers a thread of warps 0..3 and 4..11
+
+template <int KIND, bool PAIR, int BN, int SPLITS>
+struct BlockCfg {
+    static constexpr bool A_MN = KIND == BLOCK_WGRAD;
+    static constexpr bool B_MN = KIND != BLOCK_FWD;
+    static constexpr int CTAS = PAIR ? 2 : 1;                  // that share a tile's MMAs
+    static constexpr int ROWS = CTAS * kBM;                    // rows of a tile
+    static constexpr int B_BOXES = PAIR ? 1 : BN / kBlock;     // of this CTA
+    static constexpr int STAGE = (1 + B_BOXES) * kBoxBytes;
+    static constexpr int STAGES = kStageRoom / STAGE;
+    static constexpr int SLOTS = 512 / BN;                     // partial sums in TMEM
+    static constexpr int COLS = BN / 2;                        // accumulator columns of an epilogue warp
+    static constexpr int CLUSTER = CTAS * SPLITS;
+    static_assert(!PAIR || (BN == 256 && SPLITS == 1), "pairs own whole 256 x 256 tiles");
+    static_assert(SPLITS == 1 || BN == 128, "parts of K are joined on 128 x 128 tiles");
+};
+
+constexpr size_t block_smem(int E) {
+    return 1024 + kStageRoom + kEpiWarps * kChunk + 48 * sizeof(uint64_t) + (3 * static_cast<size_t>(E) + 2) * sizeof(int);
+}
+
+__device__ __forceinline__ void load_box(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Descriptor of an MN-major byte operand: each k-row holds 128 consecutive M/N bytes,
+// 8 k-rows are a 1024-byte swizzle atom (stride offset), the next 128 M/N bytes start
+// one box further (leading offset).
+template <bool MN>
+__device__ __forceinline__ uint64_t byte_desc(uint32_t saddr) {
+    uint64_t d = sw128_kmajor_desc(saddr);
+    if (MN) d = (d & ~(static_cast<uint64_t>(0x3fff) << 16)) | static_cast<uint64_t>(kBoxBytes >> 4) << 16;
+    return d;
+}
+// step of one MMA's 32 K bytes, in 16-byte units: 32 bytes of a row, or 32 rows
+template <bool MN>
+constexpr uint64_t kByteStep = MN ? 32 * kRowBytes / 16 : 2;
+
+template <int KIND>
+__host__ __device__ constexpr uint32_t block_idesc(int M, int N) {
+    return idesc_e4m3_f32(M, N) | (KIND == BLOCK_WGRAD ? 1u << 15 : 0u) | (KIND != BLOCK_FWD ? 1u << 16 : 0u);
+}
+
+// A tile: expert, first output row and how many of its rows exist, first column, and
+// where its K begins (WGRAD: 128-row blocks of the padded rows).
+struct BlockTile {
+    int e, row0, rows, n0, k0, kbs;
+};
+
+struct TileList {
+    const int *goff, *pre, *ord;  // segments; FWD, DGRAD: row tiles before list position i; WGRAD: blocks before expert e
+    int E, nt, mt, kbs, tile_rows, bn, M;
+
+    template <int KIND>
+    __device__ __forceinline__ BlockTile at(int t) const {
+        BlockTile b;
+        if (KIND == BLOCK_WGRAD) {
+            const int per = mt * nt, i = t / per, local = t - i * per;
+            const int full = mt / kPairBand * kPairBand;
+            int m, n;
+            if (local < full * nt) {
+                const int band = local / (kPairBand * nt), in = local - band * kPairBand * nt;
+                n = in / kPairBand;
+                m = band * kPairBand + in - n * kPairBand;
+            } else {
+                const int in = local - full * nt, ms = mt - full;
+                n = in / ms;
+                m = full + in - n * ms;
+            }
+            b.e = ord[i];
+            b.row0 = m * tile_rows;
+            b.rows = min(tile_rows, M - b.row0);
+            b.n0 = n * bn;
+            b.k0 = pre[b.e];
+            b.kbs = (goff[b.e + 1] - goff[b.e] + kBlock - 1) / kBlock;
+        } else {
+            const TileInfo ti = decode_tile_banded(t, E, nt, pre, ord, goff, tile_rows);
+            b = {ti.g, ti.row0, ti.rows, ti.n_tile * bn, 0, kbs};
+        }
+        return b;
+    }
+};
+
+// 32 rows x 32 columns of a warp leave as 64-byte pieces of eight rows: stored as they
+// lie, one row a thread, a 16-byte store would touch 32 rows at once.
+__device__ __forceinline__ void store_chunk(uint8_t* smem, const float2 (&v)[16], uint16_t* out, long long row0, int rows, int col0,
+                                            int N, int lane) {
+    auto cell = [&](int r, int p) { return reinterpret_cast<uint4*>(smem + r * 64 + ((p ^ ((r >> 1) & 3)) << 4)); };
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *cell(lane, i) = make_uint4(pack_bf16x2(v[4 * i].x, v[4 * i].y), pack_bf16x2(v[4 * i + 1].x, v[4 * i + 1].y),
+                                    pack_bf16x2(v[4 * i + 2].x, v[4 * i + 2].y), pack_bf16x2(v[4 * i + 3].x, v[4 * i + 3].y));
+    __syncwarp();
+    const int col = col0 + (lane & 3) * 8;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + (lane >> 2);
+        if (r < rows && col < N) *reinterpret_cast<uint4*>(out + (row0 + r) * N + col) = *cell(r, lane & 3);
+    }
+}
+
+// The accumulator of one k-part, parked in shared memory: 128 rows of 128 fp32, the
+// 16-byte quads of a row permuted by its number.
+__device__ __forceinline__ uint32_t park_quad(int row, int quad) {
+    return static_cast<uint32_t>(row * 512 + ((quad ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ float4 ld_part(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int KIND, bool PAIR, int BN, int SPLITS>
+__global__ void __launch_bounds__(kThreads, 1)
+block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const BlockArgs args) {
+    using C = BlockCfg<KIND, PAIR, BN, SPLITS>;
+    constexpr int S = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = align1024(smem_raw);  // the same offset in every CTA of a cluster
+    uint8_t* chunks = smem + kStageRoom;
+    uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kEpiWarps * kChunk);
+    uint64_t* empty = full + S;
+    uint64_t* tfull = empty + S;
+    uint64_t* tempty = tfull + C::SLOTS;
+    uint64_t* drain = tempty + C::SLOTS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* s_goff = reinterpret_cast<int*>(full + 48);  // [E + 1]
+    int* s_pre = s_goff + args.E + 1;                 // [E + 1]
+    int* s_ord = s_pre + args.E + 1;                  // [E]
+    static_assert(2 * S + 2 * C::SLOTS + 1 + 1 <= 48, "barrier room");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = args.E;
+    uint32_t* err = args.err;
+    const uint32_t rank = C::CLUSTER > 1 ? cluster_ctarank() : 0u;
+    const bool leader = !PAIR || rank == 0;
+    const int part = SPLITS > 1 ? static_cast<int>(rank) : 0;
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&a_map);
+        tma_prefetch_desc(&b_map);
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < C::SLOTS; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], C::CTAS * kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 3) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(tmem_slot, 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(tmem_slot, 512);
+            tmem_relinquish();
+        }
+    }
+    pdl_wait();
+    for (int i = threadIdx.x; i <= E; i += kThreads) s_goff[i] = args.offsets ? args.offsets[i] : (i == 0 ? 0 : args.rows);
+    __syncthreads();
+    int bad = threadIdx.x == 0 && (s_goff[0] != 0 || s_goff[E] > args.rows);
+    for (int i = threadIdx.x; i < E; i += kThreads) bad |= s_goff[i] > s_goff[i + 1];
+    bad = __syncthreads_or(bad);
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) record_error(err, MOE_DEVERR_BOUNDS);
+    heaviest_first(s_goff, E, s_ord);
+    __syncthreads();
+    if (warp == 0) {  // exclusive prefix of row tiles in list order, or of the padded rows' blocks by expert
+        constexpr int UNIT = KIND == BLOCK_WGRAD ? kBlock : C::ROWS;
+        int carry = 0;
+        for (int base = 0; base < E; base += 32) {
+            const int i = base + lane;
+            const int g = i < E ? (KIND == BLOCK_WGRAD ? i : s_ord[i]) : 0;
+            int v = i < E ? (s_goff[g + 1] - s_goff[g] + UNIT - 1) / UNIT : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += up;
+            }
+            if (i < E) s_pre[i + 1] = carry + v;
+            carry += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) s_pre[0] = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (C::CLUSTER > 1) cluster_sync_all();  // every CTA's barriers exist before any remote arrive
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const TileList list = {s_goff, s_pre, s_ord, E, (args.N + BN - 1) / BN, (args.M + C::ROWS - 1) / C::ROWS,
+                           (args.K + kBlock - 1) / kBlock, C::ROWS, BN, args.M};
+    const int tiles = bad ? 0 : (KIND == BLOCK_WGRAD ? E * list.mt : s_pre[E]) * list.nt;
+    const int first = blockIdx.x / C::CLUSTER, step = gridDim.x / C::CLUSTER;
+    // this CTA's part of a tile's steps along K
+    auto k_lo = [&](const BlockTile& b) { return SPLITS > 1 ? b.kbs * part / SPLITS : 0; };
+    auto k_hi = [&](const BlockTile& b) { return SPLITS > 1 ? b.kbs * (part + 1) / SPLITS : b.kbs; };
+    const uint32_t full_lead = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
+
+    if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        // epilogue warp (q, half): TMEM lanes 32 q .., columns half * COLS ..
+        const int q = warp & 3, half = (warp - 4) >> 2;
+        uint8_t* chunk = chunks + (warp - 4) * kChunk;
+        const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), PAIR ? 0 : rank);
+        const uint32_t t_warp = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * C::COLS);
+        const int in_tile = (PAIR ? static_cast<int>(rank) * kBM : 0) + q * 32;  // this warp's first row of the tile
+        const long long a_ld = KIND == BLOCK_WGRAD ? args.M : list.kbs;
+        int slot = 0;
+        uint32_t slot_phase = 0;
+        bool ok = true;
+        float2 acc[C::COLS / 2];
+        for (int t = first; ok && t < tiles; t += step) {
+            const BlockTile b = list.at<KIND>(t);
+            const int lo = k_lo(b), hi = k_hi(b);
+            const int rows = min(32, b.rows - in_tile);  // of this warp; <= 0: none exist
+            const bool valid = lane < rows;
+            const int col0 = b.n0 + half * C::COLS;
+            // scales: one of the row a step, and one of the column block (WGRAD: one a column)
+            const float *sa = nullptr, *sb = nullptr;
+            long long sb_step = 0;
+            if constexpr (KIND == BLOCK_WGRAD) {
+                if (valid) sa = args.a_scale + static_cast<long long>(b.k0) * a_ld + b.row0 + in_tile + lane;
+                sb = args.b_scale + static_cast<long long>(b.k0) * args.N + col0;
+            } else {
+                const long long r = static_cast<long long>(b.row0) + in_tile + lane;
+                if (valid) {
+                    long long s = r;
+                    if (args.a_index) {
+                        s = args.a_index[r];
+                        if (s < 0 || s >= args.a_scale_rows) {
+                            record_error(err, MOE_DEVERR_BOUNDS);
+                            s = -1;
+                        }
+                    }
+                    if (s >= 0) sa = args.a_scale + s * a_ld;
+                }
+                // [blocks of F, blocks of D]: FWD walks along a row, DGRAD down a column
+                const int nb = min(col0, args.N - 1) / kBlock, nbs = (args.N + kBlock - 1) / kBlock;
+                sb = args.b_scale + static_cast<long long>(b.e) * list.kbs * nbs + (KIND == BLOCK_FWD ? static_cast<long long>(nb) * list.kbs : nb);
+                sb_step = KIND == BLOCK_FWD ? 1 : nbs;
+            }
+            auto a_of = [&](int kb) { return sa && kb < hi ? sa[KIND == BLOCK_WGRAD ? kb * a_ld : kb] : 0.0f; };
+            // WGRAD: this lane's four columns of the step's scales, zero outside
+            auto b4_of = [&](int kb) {
+                const int c = lane * 4;
+                return c < C::COLS && col0 + c < args.N && kb < hi
+                           ? *reinterpret_cast<const float4*>(sb + static_cast<long long>(kb) * args.N + c)
+                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            };
+            auto b_of = [&](int kb) { return kb < hi ? sb[kb * sb_step] : 0.0f; };
+            float a_next = a_of(lo), b_next = 0.0f;
+            float4 b4_next = {};
+            if constexpr (KIND == BLOCK_WGRAD) b4_next = b4_of(lo);
+            else b_next = b_of(lo);
+#pragma unroll
+            for (int i = 0; i < C::COLS / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+            for (int kb = lo; kb < hi; ++kb) {
+                const float s = KIND == BLOCK_WGRAD ? a_next : a_next * b_next;
+                float* s_cols = reinterpret_cast<float*>(chunk) + (kb & 1) * 128;
+                if constexpr (KIND == BLOCK_WGRAD) {
+                    if (lane * 4 < C::COLS) *reinterpret_cast<float4*>(s_cols + lane * 4) = b4_next;
+                    b4_next = b4_of(kb + 1);
+                } else {
+                    b_next = b_of(kb + 1);
+                }
+                a_next = a_of(kb + 1);
+                ok = __all_sync(0xffffffffu, mbar_wait(&tfull[slot], slot_phase, abort_flag, err));
+                if (!ok) break;
+                tc_fence_after();
+                if (rows > 0) {
+                    const uint32_t t_slot = t_warp + static_cast<uint32_t>(slot * BN);
+#pragma unroll
+                    for (int c = 0; c < C::COLS; c += 32) {
+                        uint32_t r[32];
+                        tmem_ld_32x32(t_slot + c, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float2 s2 = make_float2(s, s);
+                            if constexpr (KIND == BLOCK_WGRAD) s2 = mul2(s2, *reinterpret_cast<const float2*>(s_cols + c + 2 * j));
+                            acc[c / 2 + j] = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[c / 2 + j]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * slot);
+                if (++slot == C::SLOTS) { slot = 0; slot_phase ^= 1u; }
+            }
+            if (!ok) break;
+            if constexpr (SPLITS == 1) {
+                uint16_t* out = args.out + (KIND == BLOCK_WGRAD ? static_cast<long long>(b.e) * args.M * args.N : 0);
+                if (rows > 0)
+#pragma unroll
+                    for (int c = 0; c < C::COLS; c += 32)
+                        store_chunk(chunk, *reinterpret_cast<const float2(*)[16]>(&acc[c / 2]), out,
+                                    static_cast<long long>(b.row0) + in_tile, rows, col0 + c, args.N, lane);
+                __syncwarp();  // WGRAD: the next tile's scales go where the chunk was
+            } else if (valid) {  // the stages are free: every copy of this CTA's part was waited for
+#pragma unroll
+                for (int i = 0; i < C::COLS / 4; ++i)
+                    *reinterpret_cast<float4*>(smem + park_quad(in_tile + lane, half * (C::COLS / 4) + i)) =
+                        make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+        if (warp == 0 || warp == 2) {  // copies: warp 0 A (it announces the stage's bytes), warp 2 B
+            if (lane == 0) {
+                const bool is_a = warp == 0;
+                bool withhold = is_a && args.dbg && (*args.dbg & MOE_DBG_WITHHOLD_FIRST_LOAD) && blockIdx.x == 0;
+                uint32_t pending = 0, pend_parity = 0;
+                int stage = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                for (int t = first; ok && t < tiles; t += step) {
+                    const BlockTile b = list.at<KIND>(t);
+                    const int hi = k_hi(b);
+                    for (int kb = k_lo(b); kb < hi; ++kb) {
+                        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, err)) { ok = false; break; }
+                        uint8_t* dst = smem + stage * C::STAGE;
+                        const int k = (b.k0 + kb) * kBlock;
+                        const uint32_t bar = full_lead + 8u * stage;
+                        if (withhold) {
+                            withhold = false;  // test hook: this stage never fills
+                        } else if (is_a) {
+                            if (leader) {
+                                mbar_arrive_expect_tx(&full[stage], C::CTAS * C::STAGE);
+                                pending |= 1u << stage;
+                                pend_parity = (pend_parity & ~(1u << stage)) | (phase << stage);
+                            }
+                            const int row = b.row0 + (PAIR ? static_cast<int>(rank) * kBM : 0);
+                            const int x = C::A_MN ? row : k, y = C::A_MN ? k : row;
+                            if constexpr (PAIR) tma_load_3d_pair(&a_map, bar, dst, x, y, 0);
+                            else load_box(&a_map, &full[stage], dst, x, y, 0);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < C::B_BOXES; ++i) {
+                                const int n = b.n0 + (PAIR ? static_cast<int>(rank) : i) * kBlock;
+                                const int x = C::B_MN ? n : k, y = C::B_MN ? k : n, z = KIND == BLOCK_WGRAD ? 0 : b.e;
+                                if constexpr (PAIR) tma_load_3d_pair(&b_map, bar, dst + kBoxBytes, x, y, z);
+                                else load_box(&b_map, &full[stage], dst + (1 + i) * kBoxBytes, x, y, z);
+                            }
+                        }
+                        if (++stage == S) { stage = 0; phase ^= 1u; }
+                    }
+                }
+                for (int s = 0; s < S; ++s)
+                    if (pending & (1u << s)) drain_wait(&full[s], (pend_parity >> s) & 1u, err);
+                if (!ok) settle_copies();  // some may be of stages that were never announced
+            }
+        } else if (warp == 1) {
+            if (lane == 0 && leader) {
+                constexpr uint32_t idesc = block_idesc<KIND>(C::ROWS, BN);
+                int stage = 0, slot = 0;
+                uint32_t phase = 0, slot_phase = 0;
+                bool ok = true;
+                for (int t = first; ok && t < tiles; t += step) {
+                    const BlockTile b = list.at<KIND>(t);
+                    const int n = k_hi(b) - k_lo(b);
+                    for (int kb = 0; kb < n; ++kb) {
+                        if (!mbar_wait(&tempty[slot], slot_phase ^ 1u, abort_flag, err) ||
+                            !mbar_wait(&full[stage], phase, abort_flag, err)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t d = tmem + static_cast<uint32_t>(slot * BN);
+                        const uint64_t ad = byte_desc<C::A_MN>(smem_u32(smem + stage * C::STAGE));
+                        const uint64_t bd = byte_desc<C::B_MN>(smem_u32(smem + stage * C::STAGE + kBoxBytes));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (PAIR) umma_e4m3_pair(d, ad + k * kByteStep<C::A_MN>, bd + k * kByteStep<C::B_MN>, idesc, k != 0);
+                            else umma_e4m3(d, ad + k * kByteStep<C::A_MN>, bd + k * kByteStep<C::B_MN>, idesc, k != 0);
+                        }
+                        if constexpr (PAIR) {
+                            umma_commit_pair_multicast(&empty[stage], 0x3);
+                            umma_commit_pair_multicast(&tfull[slot], 0x3);
+                        } else {
+                            umma_commit(&empty[stage]);
+                            umma_commit(&tfull[slot]);
+                        }
+                        if (++stage == S) { stage = 0; phase ^= 1u; }
+                        if (++slot == C::SLOTS) { slot = 0; slot_phase ^= 1u; }
+                    }
+                }
+                if constexpr (PAIR) umma_commit_pair_multicast(drain, 0x3);
+                else umma_commit(drain);
+            }
+        }
+    }
+
+    __syncwarp();
+    pdl_trigger();
+    if constexpr (SPLITS > 1) {  // join the parts in rank order: CTA `part` takes every SPLITS-th row
+        cluster_sync_all();
+        if (warp >= 4 && first < tiles && !*abort_flag) {
+            const BlockTile b = list.at<KIND>(first);
+            const uint32_t park = smem_u32(smem);
+            uint16_t* out = args.out + (KIND == BLOCK_WGRAD ? static_cast<long long>(b.e) * args.M * args.N : 0);
+            const int items = (b.rows - part + SPLITS - 1) / SPLITS * 32;
+            for (int it = threadIdx.x - 128; it < items; it += kEpiWarps * 32) {
+                const int r = it / 32 * SPLITS + part, quad = it & 31, col = b.n0 + quad * 4;
+                if (col >= args.N) continue;
+                float4 v[SPLITS];
+#pragma unroll
+                for (int s = 0; s < SPLITS; ++s) v[s] = ld_part(mapa_shared(park + park_quad(r, quad), s));
+#pragma unroll
+                for (int s = 1; s < SPLITS; ++s) v[0].x += v[s].x, v[0].y += v[s].y, v[0].z += v[s].z, v[0].w += v[s].w;
+                *reinterpret_cast<uint2*>(out + (static_cast<long long>(b.row0) + r) * args.N + col) =
+                    make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[0].z, v[0].w));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 32) drain_wait(drain, 0, err);  // the MMAs that wrote this CTA's TMEM have ended
+    __syncwarp();
+    if constexpr (C::CLUSTER > 1) cluster_sync_all();  // no CTA leaves while another may still signal it or read its part
+    else __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int KIND, bool PAIR, int BN, int SPLITS>
+cudaLaunchConfig_t block_config(int E, long long clusters, cudaLaunchAttribute (&attr)[2], cudaStream_t st) {
+    using C = BlockCfg<KIND, PAIR, BN, SPLITS>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * C::CLUSTER));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = block_smem(E);
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(C::CLUSTER), 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    return cfg;
+}
+
+template <int KIND, bool PAIR, int BN, int SPLITS>
+cudaError_t block_prepare(int* clusters) {
+    static std::atomic<unsigned long long> done{0};
+    static int limit[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        auto kern = block_gemm_kernel<KIND, PAIR, BN, SPLITS>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(block_smem(kMaxE)));
+        if (e != cudaSuccess) return e;
+        cudaFuncAttributes fa = {};  // the shares that setmaxnreg deals out must fit what the launch gets
+        e = cudaFuncGetAttributes(&fa, kern);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs * kThreads < kCopyRegs * 128 + kEpiRegs * kEpiWarps * 32) return cudaErrorInvalidConfiguration;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = block_config<KIND, PAIR, BN, SPLITS>(kMaxE, 1, attr, nullptr);
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        limit[dev & 63] = n;
+        done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    *clusters = limit[dev & 63];
+    return *clusters > 0 ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
+// st_set: launch; else only tell how many clusters the device holds at once.
+template <int KIND, bool PAIR, int BN, int SPLITS>
+cudaError_t block_go(const BlockPlan& p, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs* a,
+                     cudaStream_t st, int* clusters) {
+    int limit = 0;
+    cudaError_t e = block_prepare<KIND, PAIR, BN, SPLITS>(&limit);
+    if (e != cudaSuccess) return e;
+    if (clusters) {
+        *clusters = limit;
+        return cudaSuccess;
+    }
+    // a part of K is joined once, so its cluster has one tile; whole tiles are walked
+    const long long n = SPLITS > 1 ? p.tiles : std::min<long long>(p.tiles, limit);
+    if (n < 1 || n * BlockCfg<KIND, PAIR, BN, SPLITS>::CLUSTER > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = block_config<KIND, PAIR, BN, SPLITS>(a->E, n, attr, st);
+    return cudaLaunchKernelEx(&cfg, block_gemm_kernel<KIND, PAIR, BN, SPLITS>, *a_map, *b_map, *a);
+}
+
+}  // namespace
+
+template <int KIND>
+cudaError_t block_pick(const BlockPlan& p, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs* a,
+                       cudaStream_t st, int* clusters) {
+    if (p.pair) return block_go<KIND, true, 256, 1>(p, a_map, b_map, a, st, clusters);
+    if (p.bn == 256) return block_go<KIND, false, 256, 1>(p, a_map, b_map, a, st, clusters);
+    switch (p.splits) {
+        case 1: return block_go<KIND, false, 128, 1>(p, a_map, b_map, a, st, clusters);
+        case 2: return block_go<KIND, false, 128, 2>(p, a_map, b_map, a, st, clusters);
+        case 4: return block_go<KIND, false, 128, 4>(p, a_map, b_map, a, st, clusters);
+        case 8: return block_go<KIND, false, 128, 8>(p, a_map, b_map, a, st, clusters);
+        default: return cudaErrorInvalidConfiguration;
+    }
+}
+
+}  // namespace moe

@@ -1,0 +1,11 @@
+// block_gemm_dgrad.cu -- the block-scaled e4m3 product's BLOCK_DGRAD kernels (block_gemm.cuh).
+#include "block_gemm.cuh"
+
+namespace moe {
+
+cudaError_t block_dgrad(const BlockPlan& p, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs* a, cudaStream_t st,
+                     int* clusters) {
+    return block_pick<BLOCK_DGRAD>(p, a_map, b_map, a, st, clusters);
+}
+
+}  // namespace moe

@@ -59,7 +59,7 @@ cudaError_t launch_linear_grad(const uint16_t* dy, const uint16_t* z, int fn, lo
 //   DENSE_GATED   A = x, B0 = W1, B1 = W3 (both K-major): h = act(g) u, and g, u where set
 //   DENSE_LINEAR  A = x, B0 = W (both K-major): y = residual + act(acc + bias), and z = acc + bias where set
 //   DENSE_DGRAD   A0|A1 = the incoming gradients (K-major), B0|B1 = the weights (MN-major); segs = 1 or 2
-//                 products summed into one output
+//                 products summed into one output, plus residual where set
 //   DENSE_WGRAD   A0|A1 = the gradients (MN-major), B0 = x (MN-major); mats = 1 or 2 outputs
 enum DenseKind { DENSE_GATED = 0, DENSE_LINEAR = 1, DENSE_DGRAD = 2, DENSE_WGRAD = 3 };
 
@@ -69,7 +69,7 @@ struct DenseArgs {
     int mats;      // outputs (WGRAD)
     int fn;
     const float* bias;          // [N] or NULL
-    const uint16_t* residual;   // [M, N] or NULL
+    const uint16_t* residual;   // [M, N] or NULL (LINEAR, DGRAD)
     uint16_t* out0;             // h, y, dx or dW
     uint16_t* out1;             // g, z or the second dW, or NULL
     uint16_t* out2;             // u or NULL
@@ -79,11 +79,19 @@ struct DenseArgs {
 
 struct DenseOperands {
     const uint16_t *a0, *a1, *b0, *b1;
+    long long lda = 0;  // elements between the rows of A as stored, where they are not tight
 };
 
+// One product: the choice of kernel and its launch (dense_api.cu); 0 or a moe_status.
+int dense_product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st);
+
 // Tensor map of a row-major [rows, cols] bf16 matrix with boxes of 64 columns
-// x box_rows rows, 128-byte swizzle (moe_api.cu); 0 or a moe_status.
-int make_bf16_map(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows);
+// x box_rows rows, 128-byte swizzle (moe_api.cu); 0 or a moe_status.  `ld`: elements
+// between rows (a multiple of 8), 0: cols.
+int make_bf16_map(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows, long long ld = 0);
+// The same for mats stacked [rows, cols] matrices of bytes: boxes of 128 columns x
+// 128 rows of one matrix; what lies outside a matrix reads as zeros.
+int make_byte_map(CUtensorMap* m, const void* base, long long mats, long long rows, long long cols);
 
 // moe_workspace_size of the dense operations (dense_api.cu); 0 for another name or invalid sizes.
 size_t dense_workspace_size(const char* op, int N, int D, int F);

@@ -4,55 +4,16 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 
 #include "../../include/moe.h"
-#include "common.h"
+#include "api_checks.h"
 #include "dense.h"
 
 using namespace moe;
 
 namespace {
-
-moe_status refuse(moe_status s, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    set_error_detail(buf);
-    return s;
-}
-
-moe_status launched(cudaError_t e, const char* where) {
-    if (e == cudaSuccess) return MOE_OK;
-    return refuse(MOE_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-#define NEED(p)                                                                            \
-    do {                                                                                   \
-        if ((p) == nullptr) return refuse(MOE_ERR_INVALID_ARG, "%s is NULL", #p);          \
-        if (misaligned(p)) return refuse(MOE_ERR_INVALID_ARG, "%s not 16-byte aligned", #p); \
-    } while (0)
-
-#define MAY(p)                                                                             \
-    do {                                                                                   \
-        if ((p) != nullptr && misaligned(p))                                               \
-            return refuse(MOE_ERR_INVALID_ARG, "%s not 16-byte aligned", #p);              \
-    } while (0)
-
-#define NEED_WS(bytes)                                                                     \
-    do {                                                                                   \
-        NEED(ws);                                                                          \
-        const size_t need_ = (bytes);                                                      \
-        if (ws_bytes < need_)                                                              \
-            return refuse(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need_); \
-    } while (0)
 
 // Largest size of a dimension: rounded up to whole tiles, or walked past its end by a
 // batch of steps (up to 1600 columns, dense_gemv.cu), it stays below 2^31.
@@ -81,8 +42,6 @@ moe_status check_norm(int N, int D, float eps) {
     if (!(eps >= 0.0f) || eps > 1e30f) return refuse(MOE_ERR_INVALID_ARG, "eps=%g is not a finite number >= 0", eps);
     return MOE_OK;
 }
-
-size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // byte offsets of the backward workspaces (the header first)
 struct BackwardLayout {
@@ -198,8 +157,10 @@ moe_status plan_product(DenseKind kind, const DenseArgs& a, int kblocks, Plan* p
     return MOE_OK;
 }
 
+}  // namespace
+
 // One product: tensor maps, the choice of kernel, the launch.
-moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
+int moe::dense_product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
     const bool a_mn = kind == DENSE_WGRAD, b_mn = kind == DENSE_DGRAD || kind == DENSE_WGRAD;
     const int kblocks = (a.K + kBK - 1) / kBK * a.segs;
     Plan p;
@@ -210,7 +171,7 @@ moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, c
     const int b_rows = p.pairs ? 128 : (p.bn ? p.bn / 2 : (kind == DENSE_GATED ? 64 : 128));
     CUtensorMap m[4];
     auto map_a = [&](CUtensorMap* t, const uint16_t* q) {
-        return a_mn ? make_bf16_map(t, q, a.K, a.M, 64) : make_bf16_map(t, q, a.M, a.K, kBM);
+        return a_mn ? make_bf16_map(t, q, a.K, a.M, 64, o.lda) : make_bf16_map(t, q, a.M, a.K, kBM, o.lda);
     };
     auto map_b = [&](CUtensorMap* t, const uint16_t* q) {
         return b_mn ? make_bf16_map(t, q, a.K, a.N, 64) : make_bf16_map(t, q, a.N, a.K, b_rows);
@@ -224,6 +185,12 @@ moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, c
     if (!o.b1) m[3] = m[2];
     if (!p.pairs) return launched(dense_split(kind, m, a, p.bn, p.splits, st), "dense product launch");
     return launched(launch_dense_pair(kind, m, a, p.pairs, st), "dense pair product launch");
+}
+
+namespace {
+
+moe_status product(DenseKind kind, const DenseOperands& o, const DenseArgs& a, cudaStream_t st) {
+    return static_cast<moe_status>(dense_product(kind, o, a, st));
 }
 
 DenseArgs args_of(int M, int N, int K, void* ws) {

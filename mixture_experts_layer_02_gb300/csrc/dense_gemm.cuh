@@ -307,7 +307,14 @@ __device__ __forceinline__ void join_parts(const DenseArgs& a, int mat, uint8_t*
         else if constexpr (KIND == DENSE_LINEAR) linear_quad(a, row, col, v[0],
                                                             *reinterpret_cast<const uint2*>(
                                                                 res + residual_at<BN>(r / SPLITS, q >> 1) + (q & 1) * 8));
-        else *quad_of(mat ? a.out1 : a.out0, row, a.N, col) = pack_quad(v[0]);
+        else {
+            if (KIND == DENSE_DGRAD && a.residual) {
+                const uint2 r2 = *reinterpret_cast<const uint2*>(a.residual + row * a.N + col);
+                v[0][0] += __uint_as_float(r2.x << 16), v[0][1] += __uint_as_float(r2.x & 0xffff0000u);
+                v[0][2] += __uint_as_float(r2.y << 16), v[0][3] += __uint_as_float(r2.y & 0xffff0000u);
+            }
+            *quad_of(mat ? a.out1 : a.out0, row, a.N, col) = pack_quad(v[0]);
+        }
     }
 }
 
@@ -406,9 +413,10 @@ __device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk&
     c.store(a.out0, z);
 }
 
-// A gradient's 32 rows x 64 columns: 128-byte lines of four rows a store.
-__device__ __forceinline__ void plain_chunk(uint8_t* smem, uint32_t taddr, uint16_t* base, long long row0, int col0, int M,
-                                            int N, int lane) {
+// A gradient's 32 rows x 64 columns: 128-byte lines of four rows a store.  `residual`
+// (or NULL) is added to the unrounded sums.
+__device__ __forceinline__ void plain_chunk(uint8_t* smem, uint32_t taddr, uint16_t* base, const uint16_t* residual,
+                                            long long row0, int col0, int M, int N, int lane) {
     uint32_t r[64];
     {
         uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[0]);
@@ -419,11 +427,27 @@ __device__ __forceinline__ void plain_chunk(uint8_t* smem, uint32_t taddr, uint1
     }
     auto cell = [&](int row, int p) { return reinterpret_cast<uint4*>(smem + row * 128 + ((p ^ (row & 7)) << 4)); };
     auto two = [&](int j) { return pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])); };
+    const int col = col0 + (lane & 7) * 8;
+    if (residual) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const long long row = row0 + i * 4 + (lane >> 3);
+            *cell(i * 4 + (lane >> 3), lane & 7) = row < M && col < N ? *octet(residual, row, N, col) : make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float f[8];
+            unpack_bf16x8(*cell(lane, i), f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[8 * i + j] = __float_as_uint(__uint_as_float(r[8 * i + j]) + f[j]);
+        }
+    }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 8; ++i) *cell(lane, i) = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
     __syncwarp();
-    const int col = col0 + (lane & 7) * 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const long long row = row0 + i * 4 + (lane >> 3);
@@ -456,8 +480,8 @@ struct WholeEpilogue {
         if constexpr (KIND == DENSE_DGRAD || KIND == DENSE_WGRAD) {
 #pragma unroll 1
             for (int c = 0; c < COLS; c += 64)
-                plain_chunk(smem, t + c, mat ? a.out1 : a.out0, static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M,
-                            a.N, lane);
+                plain_chunk(smem, t + c, mat ? a.out1 : a.out0, KIND == DENSE_DGRAD ? a.residual : nullptr,
+                            static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M, a.N, lane);
         } else {
 #pragma unroll 1
             for (int c = 0; c < COLS; c += 32) {

@@ -17,6 +17,7 @@
 #include "../../include/moe.h"
 #include "common.h"
 #include "dense.h"
+#include "train.h"
 
 using namespace moe;
 
@@ -87,12 +88,12 @@ EncodeTiledFn encode_fn() {
 // 128 bytes of columns], 128-byte swizzle (the layout the tcgen05
 // shared-memory descriptors expect).
 moe_status make_tmap(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows,
-                     bool e4m3 = false) {
+                     bool e4m3 = false, long long ld = 0) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
     const int esize = e4m3 ? 1 : 2;
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * esize};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld ? ld : cols) * esize};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(kRowBytes / esize), static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
@@ -155,8 +156,25 @@ moe_status check_sizes(int N, int D, int E, int K, int Dff, bool need_dff) {
 int moe::check_permute_sizes(int N, int D, int E, int K) { return check_sizes(N, D, E, K, 64, false); }
 
 // The tensor map of a bf16 matrix, for the dense products (dense_api.cu).
-int moe::make_bf16_map(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows) {
-    return make_tmap(m, base, rows, cols, box_rows);
+int moe::make_bf16_map(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows, long long ld) {
+    return make_tmap(m, base, rows, cols, box_rows, false, ld);
+}
+
+// The tensor map of stacked byte matrices, for the block-scaled products (train_api.cu).
+int moe::make_byte_map(CUtensorMap* m, const void* base, long long mats, long long rows, long long cols) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(cols) * rows};
+    cuuint32_t box[3] = {kRowBytes, kBM, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (bytes) failed (%d) mats=%lld rows=%lld cols=%lld", (int)r, mats,
+                    rows, cols);
+    return MOE_OK;
 }
 
 namespace {
@@ -1006,7 +1024,8 @@ size_t moe_workspace_size(const char* op, int N, int D, int E, int K, int Dff) {
         if (check_sizes(N, D, E, K, Dff, true) != MOE_OK || D % 128 || Dff % 128) return 0;
         return e4m3_layout(N, D, E, K, Dff).total;
     }
-    return dense_workspace_size(op, N, D, Dff);
+    const size_t train = train_workspace_size(op, N, D, E, Dff);
+    return train ? train : dense_workspace_size(op, N, D, Dff);
 }
 
 int moe_layer_workspace_layout(int N, int D, int E, int K, int Dff, size_t out[8]) {

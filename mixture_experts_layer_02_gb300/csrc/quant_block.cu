@@ -1,0 +1,247 @@
+// quant_block.cu -- e4m3 codes with one power-of-two scale for each block of 128:
+//   rows      1 x 128 of an activation: the operand of a product over that dimension
+//   tiles     128 x 128 of a weight
+//   segments  1 x 128 and 128 x 1 of an activation from one read of it; the second
+//             form runs down the rows of one expert at a time, whose segments then
+//             start at multiples of 128 with zero rows behind them: the operands of
+//             the weight gradient, which sums over an expert's rows
+// The rule is the row quantiser's (quant.cu): scale = 2^k, k the smallest integer
+// >= -126 with max|block| <= 448 2^k; x 2^-k is exact, so the e4m3 rounding is the
+// only one.  A block's values stay in registers between the maximum and the codes:
+// each is read once.  Bound by HBM.  Coherent loads only: the launch before may still
+// be writing the source when blocks start.
+#include <algorithm>
+
+#include "quant.cuh"
+#include "train.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+int sms() {
+    int dev = 0, n = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
+
+__device__ __forceinline__ float scale_of(int k) { return __uint_as_float(static_cast<uint32_t>(127 + k) << 23); }
+__device__ __forceinline__ float inverse_of(int k) { return __uint_as_float(static_cast<uint32_t>(127 - k) << 23); }
+
+// Sixteen lanes a block of 128 values; a warp has 2 U blocks in flight.
+__global__ void __launch_bounds__(kThreads)
+quant_rows_block_kernel(const uint16_t* src, long long rows, int cols, int nb, uint8_t* q, float* scale) {
+    constexpr int U = 4;
+    pdl_wait();
+    const int sub = threadIdx.x & 15;
+    const long long total = rows * nb, step = static_cast<long long>(gridDim.x) * (kThreads / 16);
+    const long long first = static_cast<long long>(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 4);
+    // every lane of a warp takes the same number of turns (the shuffles are the whole warp's)
+    for (long long base = first; base - (first & 1) < total; base += U * step) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long i = base + u * step;
+            const long long r = i / nb;
+            const int col = static_cast<int>(i - r * nb) * kBlock + sub * 8;
+            v[u] = i < total && col < cols ? *reinterpret_cast<const uint4*>(src + r * cols + col) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long i = base + u * step;
+            uint32_t m = absmax8(v[u]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (i >= total) continue;
+            const int k = scale_exp_of(m);
+            const long long r = i / nb;
+            const int col = static_cast<int>(i - r * nb) * kBlock + sub * 8;
+            if (sub == 0) scale[i] = scale_of(k);
+            if (col < cols) *reinterpret_cast<uint2*>(q + r * cols + col) = to_e4m3x8(v[u], inverse_of(k));
+        }
+    }
+    pdl_trigger();
+}
+
+// One 128 x 128 block a turn: thread (y, x) of 16 x 16 holds rows y, y + 16, ... of an octet of columns.
+__global__ void __launch_bounds__(kThreads)
+quant_tiles_kernel(const uint16_t* src, long long tiles, int rows, int cols, int rb, int nb, uint8_t* q, float* scale) {
+    __shared__ uint32_t s_max[2][kThreads / 32];
+    pdl_wait();
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+    int turn = 0;
+    for (long long i = blockIdx.x; i < tiles; i += gridDim.x, turn ^= 1) {
+        const long long mr = i / nb, mat = mr / rb;
+        const int row0 = static_cast<int>(mr - mat * rb) * kBlock;
+        const int col = static_cast<int>(i - mr * nb) * kBlock + x * 8;
+        const long long at = (mat * rows + row0 + y) * cols + col;
+        uint4 v[8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool in = row0 + y + 16 * j < rows && col < cols;
+            v[j] = in ? *reinterpret_cast<const uint4*>(src + at + static_cast<long long>(16 * j) * cols) : make_uint4(0, 0, 0, 0);
+            m = max(m, absmax8(v[j]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if ((threadIdx.x & 31) == 0) s_max[turn][threadIdx.x >> 5] = m;
+        __syncthreads();  // the other half of s_max is rewritten a turn later, behind the next one
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) m = max(m, s_max[turn][w]);
+        const int k = scale_exp_of(m);
+        if (threadIdx.x == 0) scale[i] = scale_of(k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (row0 + y + 16 * j < rows && col < cols)
+                *reinterpret_cast<uint2*>(q + at + static_cast<long long>(16 * j) * cols) = to_e4m3x8(v[j], inverse_of(k));
+    }
+    pdl_trigger();
+}
+
+// magnitudes of two bf16, larger of each
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7fff7fffu); }
+
+// A block takes 128 rows of one segment and every gridDim.y-th block of 128 columns.
+__global__ void __launch_bounds__(kThreads)
+quant_segments_kernel(const QuantSegArgs a) {
+    __shared__ int s_warp[kThreads / 32];
+    __shared__ int s_place[3];                      // first row, rows, first padded row; rows < 0: nothing here
+    __shared__ __align__(16) uint32_t s_col[2][8][kBlock / 2];  // maxima of column pairs, by warp
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x < 3) s_place[threadIdx.x] = -1;
+    // which expert's rows start at padded block blockIdx.x: a running sum of the segments' blocks
+    int carry = 0;
+    bool bad = false;
+    for (int e0 = 0; e0 < a.E; e0 += kThreads) {
+        const int e = e0 + static_cast<int>(threadIdx.x);
+        int lo = 0, n = 0;
+        if (e < a.E) {
+            lo = a.offsets ? a.offsets[e] : 0;
+            const int hi = a.offsets ? a.offsets[e + 1] : a.rows;
+            n = hi - lo;
+            if (lo < 0 || hi < lo || hi > a.rows || (e == 0 && lo != 0)) bad = true;
+        }
+        if (__syncthreads_or(bad)) break;
+        int v = (n + kBlock - 1) / kBlock;
+        const int mine = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += up;
+        }
+        if (lane == 31) s_warp[warp] = v;
+        __syncthreads();
+        int before = carry;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s_warp[w];
+            carry += s_warp[w];
+        }
+        const int start = before + v - mine, b = static_cast<int>(blockIdx.x) - start;
+        if (b >= 0 && b < mine) {
+            s_place[0] = lo + b * kBlock;
+            s_place[1] = min(kBlock, n - b * kBlock);
+            s_place[2] = static_cast<int>(blockIdx.x) * kBlock;
+        }
+        __syncthreads();
+    }
+    if (__syncthreads_or(bad)) {  // offsets that are not a prefix sum within the rows: nothing is written
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(a.err, MOE_DEVERR_BOUNDS);
+        return;
+    }
+    const int n = s_place[1];
+    if (n < 0) return;  // behind the last segment
+    const long long row0 = s_place[0], pad0 = s_place[2];
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+    const int nb = (a.cols + kBlock - 1) / kBlock;
+    int turn = 0;
+    for (int cb = blockIdx.y; cb < nb; cb += gridDim.y, turn ^= 1) {
+        const int col = cb * kBlock + x * 8;
+        const bool inside = col < a.cols;
+        uint4 v[8];
+        uint32_t c[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = y + 16 * j;
+            v[j] = r < n && inside ? *reinterpret_cast<const uint4*>(a.src + (row0 + r) * a.cols + col) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            c[0] = max_pair(c[0], v[j].x), c[1] = max_pair(c[1], v[j].y);
+            c[2] = max_pair(c[2], v[j].z), c[3] = max_pair(c[3], v[j].w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = max_pair(c[i], __shfl_xor_sync(0xffffffffu, c[i], 16));
+        if (lane < 16) *reinterpret_cast<uint4*>(&s_col[turn][warp][lane * 4]) = make_uint4(c[0], c[1], c[2], c[3]);
+        if (a.q) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t m = absmax8(v[j]);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const int r = y + 16 * j, k = scale_exp_of(m);
+                if (r >= n) continue;
+                if (x == 0) a.scale[(row0 + r) * nb + cb] = scale_of(k);
+                if (inside) *reinterpret_cast<uint2*>(a.q + (row0 + r) * a.cols + col) = to_e4m3x8(v[j], inverse_of(k));
+            }
+        }
+        __syncthreads();  // the other half of s_col is rewritten a turn later, behind the next one
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const uint4 m = *reinterpret_cast<const uint4*>(&s_col[turn][w][x * 4]);
+            c[0] = max_pair(c[0], m.x), c[1] = max_pair(c[1], m.y), c[2] = max_pair(c[2], m.z), c[3] = max_pair(c[3], m.w);
+        }
+        if (!inside) continue;
+        float s[8], back[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = scale_exp_of((c[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+            s[i] = scale_of(k);
+            back[i] = inverse_of(k);
+        }
+        if (y == 0) {
+            float4* p = reinterpret_cast<float4*>(a.scale_seg + pad0 / kBlock * a.cols + col);
+            p[0] = make_float4(s[0], s[1], s[2], s[3]);
+            p[1] = make_float4(s[4], s[5], s[6], s[7]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // rows behind the segment's last are zeros
+            const uint32_t w4[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = fp8x2(bf16_lo(w4[i]) * back[2 * i], bf16_hi(w4[i]) * back[2 * i + 1]);
+            *reinterpret_cast<uint2*>(a.q_seg + (pad0 + y + 16 * j) * a.cols + col) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        }
+    }
+    pdl_trigger();
+}
+
+}  // namespace
+
+cudaError_t launch_quant_rows_block(const uint16_t* src, long long rows, int cols, uint8_t* q, float* scale,
+                                    cudaStream_t st) {
+    const int nb = static_cast<int>(blocks_of(cols));
+    const long long want = (rows * nb + kThreads / 16 - 1) / (kThreads / 16);
+    const int grid = static_cast<int>(std::min<long long>(want, static_cast<long long>(sms()) * 8));
+    return launch_kernel(quant_rows_block_kernel, dim3(grid), dim3(kThreads), 0, st, src, rows, cols, nb, q, scale);
+}
+
+cudaError_t launch_quant_tiles(const uint16_t* src, long long mats, int rows, int cols, uint8_t* q, float* scale,
+                               cudaStream_t st) {
+    const int rb = static_cast<int>(blocks_of(rows)), nb = static_cast<int>(blocks_of(cols));
+    const long long tiles = mats * rb * nb;
+    const int grid = static_cast<int>(std::min<long long>(tiles, static_cast<long long>(sms()) * 6));
+    return launch_kernel(quant_tiles_kernel, dim3(grid), dim3(kThreads), 0, st, src, tiles, rows, cols, rb, nb, q, scale);
+}
+
+cudaError_t launch_quant_segments(const QuantSegArgs& a, cudaStream_t st) {
+    const int blocks = static_cast<int>(segment_rows_of(a.rows, a.E) / kBlock);
+    const int nb = static_cast<int>(blocks_of(a.cols));
+    const int slices = std::max(1, std::min(nb, sms() * 12 / std::max(1, blocks)));
+    return launch_kernel(quant_segments_kernel, dim3(blocks, slices), dim3(kThreads), 0, st, a);
+}
+
+}  // namespace moe

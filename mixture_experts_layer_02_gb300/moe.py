@@ -54,6 +54,8 @@ EXPORTED = (
     "moe_grouped_ffn_gathered", "moe_grouped_ffn_e4m3_gathered",
     "moe_rmsnorm", "moe_rmsnorm_backward", "moe_gated_linear", "moe_gated_linear_backward",
     "moe_linear", "moe_linear_backward",
+    "moe_combine_backward", "moe_permute_backward", "moe_route_backward", "moe_quantize_e4m3_block", "moe_segment_rows",
+    "moe_quantize_e4m3_segments", "moe_grouped_linear_e4m3_block", "moe_grouped_linear_e4m3_block_backward",
 )
 
 _lock = threading.Lock()
@@ -143,6 +145,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.moe_linear.argtypes = [p, p, p, p, i, i, i, i, p, p, p, sz, p]
         L.moe_linear_backward.restype = i
         L.moe_linear_backward.argtypes = [p, p, p, p, i, i, i, i, p, p, p, p, sz, p]
+        L.moe_combine_backward.restype = i
+        L.moe_combine_backward.argtypes = [p, p, p, p, i, i, i, i, p, p, p, sz, p]
+        L.moe_permute_backward.restype = i
+        L.moe_permute_backward.argtypes = [p, p, p, i, i, i, i, p, p, sz, p]
+        L.moe_route_backward.restype = i
+        L.moe_route_backward.argtypes = [p, p, p, p, p, p, p, i, i, i, i, i, p, p, p, p, sz, p]
+        L.moe_quantize_e4m3_block.restype = i
+        L.moe_quantize_e4m3_block.argtypes = [p, i, i, i, i, p, p, p]
+        L.moe_segment_rows.restype = ctypes.c_longlong
+        L.moe_segment_rows.argtypes = [i, i]
+        L.moe_quantize_e4m3_segments.restype = i
+        L.moe_quantize_e4m3_segments.argtypes = [p, p, i, i, i, p, p, p, p, p, sz, p]
+        L.moe_grouped_linear_e4m3_block.restype = i
+        L.moe_grouped_linear_e4m3_block.argtypes = [p, p, p, i, p, i, p, p, i, i, i, p, p, sz, p]
+        L.moe_grouped_linear_e4m3_block_backward.restype = i
+        L.moe_grouped_linear_e4m3_block_backward.argtypes = [p, p, p, p, p, p, p, i, p, p, i, i, i, p, p, p, sz, p]
         L.moe_read_device_error.restype = i
         L.moe_read_device_error.argtypes = [p, p]
         L.moe_clear_device_error.restype = i
@@ -879,3 +897,222 @@ def moe_linear_backward(dy, x, w, z=None, fn: int = FN_NONE, need_dbias: bool = 
     if s:
         _check("moe_linear_backward", s)
     return dx, dw, dbias
+
+
+# ---------------------------------------------------------------- training the routed layer
+_I32 = torch.int32
+BLOCK = 128  # values that share a scale, along each blocked dimension
+
+
+def _blocks(n):
+    return -(-n // BLOCK)
+
+
+def _ready(fn, ws, *specs):
+    """Check (tensor or None, dtype, shape, name) of one call: contiguous CUDA tensors of one device, the current one."""
+    dev = specs[0][0].get_device()
+    for t, dtype, shape, name in specs:
+        if t is not None and not (_fits(t, dtype, shape) and t.get_device() == dev):
+            _need(t, dtype, shape, name)
+            raise ValueError(f"{name}: on cuda:{t.get_device()}, {specs[0][3]} on cuda:{dev}")
+    if ws is not None and not (ws.is_cuda and ws.get_device() == dev and ws.dtype is _U8 and ws.is_contiguous()):
+        raise ValueError(f"ws: must be a contiguous uint8 tensor on cuda:{dev}")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{fn}: its tensors are on cuda:{dev}, not on the current device")
+
+
+def _header(stream, op, device, **sizes):
+    """A workspace of one call, only its header zeroed (see _scratch)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _header(None, op, device, **sizes)
+    ws = torch.empty(max(workspace_size(op, **sizes), 256), dtype=_U8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def moe_combine_backward(dout, y_perm, inv_perm, topk_w, dy_perm=None, dtopk_w=None, ws=None, stream=None):
+    """Gradient of moe_combine, or of moe_combine_padded with its slot as inv_perm: (dy_perm, dtopk_w).
+    Rows of dy_perm that no assignment names are left as they were (zero in a buffer made here)."""
+    shape = _rows(dout, "dout")
+    N, D = shape
+    K = _rows(inv_perm, "inv_perm")[1]
+    rows = _rows(y_perm, "y_perm")[0]
+    if dy_perm is None:
+        dy_perm, = _new(stream, ((rows, D), _BF16, dout.device))
+        if rows != N * K:
+            with torch.cuda.stream(stream):
+                dy_perm.zero_()
+    if dtopk_w is None:
+        dtopk_w, = _new(stream, ((N, K), _F32, dout.device))
+    if ws is None:
+        ws = _header(stream, "combine", dout.device)
+    _ready("moe_combine_backward", ws, (dout, _BF16, shape, "dout"), (y_perm, _BF16, (rows, D), "y_perm"),
+           (inv_perm, _I32, (N, K), "inv_perm"), (topk_w, _F32, (N, K), "topk_w"), (dy_perm, _BF16, (rows, D), "dy_perm"),
+           (dtopk_w, _F32, (N, K), "dtopk_w"))
+    s = (_lib or load()).moe_combine_backward(_addr(dout), _addr(y_perm), _addr(inv_perm), _addr(topk_w), N, D, K, rows,
+                                              _addr(dy_perm), _addr(dtopk_w), _addr(ws), ws.numel(), _stream_of(dout, stream))
+    if s:
+        _check("moe_combine_backward", s)
+    return dy_perm, dtopk_w
+
+
+def moe_permute_backward(dx_perm, inv_perm, dresidual=None, dx=None, ws=None, stream=None):
+    """Gradient of moe_permute (or, with its slot, of moe_permute_padded) for the tokens, added to dresidual: dx."""
+    rows, D = _rows(dx_perm, "dx_perm")
+    N, K = _rows(inv_perm, "inv_perm")
+    if dx is None:
+        dx, = _new(stream, ((N, D), _BF16, dx_perm.device))
+    if ws is None:
+        ws = _header(stream, "combine", dx_perm.device)
+    _ready("moe_permute_backward", ws, (dx_perm, _BF16, (rows, D), "dx_perm"), (inv_perm, _I32, (N, K), "inv_perm"),
+           (dresidual, _BF16, (N, D), "dresidual"), (dx, _BF16, (N, D), "dx"))
+    s = (_lib or load()).moe_permute_backward(_addr(dx_perm), _addr(inv_perm), _addr(dresidual), N, D, K, rows, _addr(dx),
+                                              _addr(ws), ws.numel(), _stream_of(dx_perm, stream))
+    if s:
+        _check("moe_permute_backward", s)
+    return dx
+
+
+def moe_route_backward(dtopk_w, topk_ids, topk_w, logits, x, w_gate, mode: int, dresidual=None, need_dbias: bool = False,
+                       dx=None, dw_gate=None, dbias=None, ws=None, stream=None):
+    """Gradient of moe_route through its weights: (dx, dw_gate, dbias).  logits is moe_route's logits_out (may be None
+    for SOFTMAX_TOPK); dx is added to dresidual; dbias is fp32, None unless need_dbias=True or it is passed."""
+    N, D = _rows(x, "x")
+    E = _rows(w_gate, "w_gate")[0]
+    K = _rows(topk_ids, "topk_ids")[1]
+    if logits is None and mode == SIGMOID_NORM:
+        raise ValueError("logits: needed with SIGMOID_NORM")
+    if dx is None:
+        dx, = _new(stream, ((N, D), _BF16, x.device))
+    if dw_gate is None:
+        dw_gate, = _new(stream, ((E, D), _BF16, x.device))
+    if need_dbias and dbias is None:
+        dbias, = _new(stream, ((E,), _F32, x.device))
+    if ws is None:
+        ws = _header(stream, "route_backward", x.device, N=N, D=D, E=E)
+    _ready("moe_route_backward", ws, (x, _BF16, (N, D), "x"), (w_gate, _BF16, (E, D), "w_gate"),
+           (dtopk_w, _F32, (N, K), "dtopk_w"), (topk_ids, _I32, (N, K), "topk_ids"), (topk_w, _F32, (N, K), "topk_w"),
+           (logits, _F32, (N, E), "logits"), (dresidual, _BF16, (N, D), "dresidual"), (dx, _BF16, (N, D), "dx"),
+           (dw_gate, _BF16, (E, D), "dw_gate"), (dbias, _F32, (E,), "dbias"))
+    s = (_lib or load()).moe_route_backward(_addr(dtopk_w), _addr(topk_ids), _addr(topk_w), _addr(logits), _addr(x),
+                                            _addr(w_gate), _addr(dresidual), N, D, E, K, mode, _addr(dx), _addr(dw_gate),
+                                            _addr(dbias), _addr(ws), ws.numel(), _stream_of(x, stream))
+    if s:
+        _check("moe_route_backward", s)
+    return dx, dw_gate, dbias
+
+
+def moe_quantize_e4m3_block(src, block_rows: int = 1, q=None, scale=None, stream=None):
+    """e4m3 codes of a bf16 tensor [rows, cols] or [mats, rows, cols] with a scale for each 1 x 128 (block_rows=1) or
+    128 x 128 (block_rows=128) of each matrix: (q uint8 of src's shape, scale fp32)."""
+    if src.dim() not in (2, 3):
+        raise ValueError(f"src: expected [rows, cols] or [mats, rows, cols], got {tuple(src.shape)}")
+    mats = src.shape[0] if src.dim() == 3 else 1
+    rows, cols = src.shape[-2:]
+    grid = (*src.shape[:-2], _blocks(rows) if block_rows == BLOCK else rows, _blocks(cols))
+    if q is None:
+        q, = _new(stream, (src.shape, _U8, src.device))
+    if scale is None:
+        scale, = _new(stream, (grid, _F32, src.device))
+    _ready("moe_quantize_e4m3_block", None, (src, _BF16, src.shape, "src"), (q, _U8, src.shape, "q"), (scale, _F32, grid, "scale"))
+    s = (_lib or load()).moe_quantize_e4m3_block(_addr(src), mats, rows, cols, block_rows, _addr(q), _addr(scale),
+                                                 _stream_of(src, stream))
+    if s:
+        _check("moe_quantize_e4m3_block", s)
+    return q, scale
+
+
+def segment_rows(rows: int, E: int) -> int:
+    """Rows of the buffers whose segments start at multiples of 128, whatever the routing."""
+    n = int(load().moe_segment_rows(rows, E))
+    if n < 0:
+        raise ValueError(f"invalid sizes: rows={rows}, E={E}")
+    return n
+
+
+def moe_quantize_e4m3_segments(src, expert_offsets, both: bool = True, q=None, scale=None, q_seg=None, scale_seg=None,
+                               ws=None, stream=None):
+    """e4m3 codes of src [rows, cols] along each expert's rows, as the weight gradient reads them, and (with both=True,
+    or where passed) along its columns: (q, scale, q_seg, scale_seg).  expert_offsets [E+1], or None for one segment."""
+    rows, cols = _rows(src, "src")
+    E = 1 if expert_offsets is None else expert_offsets.shape[0] - 1
+    seg = segment_rows(rows, E)
+    dev = src.device
+    if (both or scale is not None) and q is None:
+        q, = _new(stream, ((rows, cols), _U8, dev))
+    if q is not None and scale is None:
+        scale, = _new(stream, ((rows, _blocks(cols)), _F32, dev))
+    if q_seg is None:
+        q_seg, = _new(stream, ((seg, cols), _U8, dev))
+    if scale_seg is None:
+        scale_seg, = _new(stream, ((seg // BLOCK, cols), _F32, dev))
+    if ws is None:
+        ws = _header(stream, "combine", dev)
+    _ready("moe_quantize_e4m3_segments", ws, (src, _BF16, (rows, cols), "src"), (expert_offsets, _I32, (E + 1,), "expert_offsets"),
+           (q, _U8, (rows, cols), "q"), (scale, _F32, (rows, _blocks(cols)), "scale"), (q_seg, _U8, (seg, cols), "q_seg"),
+           (scale_seg, _F32, (seg // BLOCK, cols), "scale_seg"))
+    s = (_lib or load()).moe_quantize_e4m3_segments(_addr(src), _addr(expert_offsets), rows, cols, E, _addr(q), _addr(scale),
+                                                    _addr(q_seg), _addr(scale_seg), _addr(ws), ws.numel(),
+                                                    _stream_of(src, stream))
+    if s:
+        _check("moe_quantize_e4m3_segments", s)
+    return q, scale, q_seg, scale_seg
+
+
+def _weights(wq):
+    if wq.dim() != 3:
+        raise ValueError(f"wq: expected [E, F, D], got {tuple(wq.shape)}")
+    return wq.shape
+
+
+def moe_grouped_linear_e4m3_block(xq, x_scale, wq, w_scale, expert_offsets=None, x_scale_index=None, y=None, ws=None,
+                                  stream=None):
+    """y = x w^T of each expert's rows, both in e4m3 with a scale for each block of 128 (as moe_quantize_e4m3_block makes
+    them, or any fp32 scales): xq [rows, D], wq [E, F, D].  x_scale_index (perm_src) finds the row of x_scale; without
+    expert_offsets E is 1: a dense product."""
+    rows, D = _rows(xq, "xq")
+    E, F, _ = _weights(wq)
+    n = _rows(x_scale, "x_scale")[0]
+    if y is None:
+        y, = _new(stream, ((rows, F), _BF16, xq.device))
+    if ws is None:
+        ws = _header(stream, "combine", xq.device)
+    _ready("moe_grouped_linear_e4m3_block", ws, (xq, _U8, (rows, D), "xq"), (x_scale, _F32, (n, _blocks(D)), "x_scale"),
+           (wq, _U8, (E, F, D), "wq"), (w_scale, _F32, (E, _blocks(F), _blocks(D)), "w_scale"),
+           (expert_offsets, _I32, (E + 1,), "expert_offsets"), (x_scale_index, _I32, (rows,), "x_scale_index"),
+           (y, _BF16, (rows, F), "y"))
+    s = (_lib or load()).moe_grouped_linear_e4m3_block(_addr(xq), _addr(x_scale), _addr(x_scale_index), n,
+                                                       _addr(expert_offsets), rows, _addr(wq), _addr(w_scale), E, D, F, _addr(y),
+                                                       _addr(ws), ws.numel(), _stream_of(xq, stream))
+    if s:
+        _check("moe_grouped_linear_e4m3_block", s)
+    return y
+
+
+def moe_grouped_linear_e4m3_block_backward(wq, w_scale, dyq, dy_scale, dyq_seg, dy_scale_seg, xq_seg, x_scale_seg,
+                                           expert_offsets=None, dx=None, dw=None, ws=None, stream=None):
+    """Gradients (dx, dw) of moe_grouped_linear_e4m3_block from quantised operands: the incoming gradient along its columns
+    (dyq, dy_scale) for dx and along its rows (dyq_seg, dy_scale_seg) for dw, x along its rows (xq_seg, x_scale_seg)."""
+    E, F, D = _weights(wq)
+    rows = _rows(dyq, "dyq")[0]
+    seg = segment_rows(rows, E)
+    if dx is None:
+        dx, = _new(stream, ((rows, D), _BF16, wq.device))
+    if dw is None:
+        dw, = _new(stream, ((E, F, D), _BF16, wq.device))
+    if ws is None:
+        ws = _header(stream, "combine", wq.device)
+    _ready("moe_grouped_linear_e4m3_block_backward", ws, (wq, _U8, (E, F, D), "wq"),
+           (w_scale, _F32, (E, _blocks(F), _blocks(D)), "w_scale"), (dyq, _U8, (rows, F), "dyq"),
+           (dy_scale, _F32, (rows, _blocks(F)), "dy_scale"), (dyq_seg, _U8, (seg, F), "dyq_seg"),
+           (dy_scale_seg, _F32, (seg // BLOCK, F), "dy_scale_seg"), (xq_seg, _U8, (seg, D), "xq_seg"),
+           (x_scale_seg, _F32, (seg // BLOCK, D), "x_scale_seg"), (expert_offsets, _I32, (E + 1,), "expert_offsets"),
+           (dx, _BF16, (rows, D), "dx"), (dw, _BF16, (E, F, D), "dw"))
+    s = (_lib or load()).moe_grouped_linear_e4m3_block_backward(
+        _addr(dyq), _addr(dy_scale), _addr(dyq_seg), _addr(dy_scale_seg), _addr(xq_seg), _addr(x_scale_seg),
+        _addr(expert_offsets), rows, _addr(wq), _addr(w_scale), E, D, F, _addr(dx), _addr(dw), _addr(ws), ws.numel(),
+        _stream_of(wq, stream))
+    if s:
+        _check("moe_grouped_linear_e4m3_block_backward", s)
+    return dx, dw
