@@ -32,8 +32,7 @@
 
 #include "activation.cuh"
 #include "block_gemm.h"
-#include "gemm_common.cuh"
-#include "settle.cuh"
+#include "dense_gemm.cuh"
 
 namespace moe {
 
@@ -45,7 +44,7 @@ constexpr int kBoxBytes = kBlock * kRowBytes;  // 128 rows of 128 bytes
 constexpr int kStageRoom = 192 * 1024;
 constexpr int kChunk = 2048;                   // an epilogue warp's staging: 32 rows of 64 bytes
 constexpr int kMaxE = 1024;
-constexpr int kCopyRegs = 88, kEpiRegs = 208;  // registers a thread of warps 0..3 and 4..11
+constexpr int kCopyRegs = 72, kEpiRegs = 216;  // registers a thread of warps 0..3 and 4..11
 
 template <int KIND, bool PAIR, int BN, int SPLITS>
 struct BlockCfg {
@@ -75,6 +74,25 @@ __device__ __forceinline__ void load_box(const CUtensorMap* map, uint64_t* bar, 
         : "memory");
 }
 
+// "This warp has read the slot", to the even CTA's barrier.  What it orders are TMEM
+// reads, which the fence before it covers, and no memory: a release at cluster scope
+// waits for every access in flight and took 1 us a step.
+__device__ __forceinline__ void slot_arrive(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Wait for the tcgen05.ld that fills r; what uses r stays behind it.
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
 // Descriptor of an MN-major byte operand: each k-row holds 128 consecutive M/N bytes,
 // 8 k-rows are a 1024-byte swizzle atom (stride offset), the next 128 M/N bytes start
 // one box further (leading offset).
@@ -92,6 +110,33 @@ template <int KIND>
 __host__ __device__ constexpr uint32_t block_idesc(int M, int N) {
     return idesc_e4m3_f32(M, N) | (KIND == BLOCK_WGRAD ? 1u << 15 : 0u) | (KIND != BLOCK_FWD ? 1u << 16 : 0u);
 }
+
+// The MMA warp's walk over a ring of barriers, executed by all of its lanes.  A wait
+// on an mbarrier that is complete still takes about 200 clocks to answer, so the next
+// one is asked before this step's MMAs are issued.
+struct BarrierWalk {
+    uint64_t* bar;
+    int n, at;
+    uint32_t parity;
+    bool ready;  // the barrier at `at` has been seen complete
+
+    __device__ __forceinline__ BarrierWalk(uint64_t* b, int count, uint32_t first) : bar(b), n(count), at(0), parity(first), ready(false) {}
+    // false: given up, by all lanes
+    __device__ __forceinline__ bool wait(volatile int* abort, uint32_t* err) {
+        const bool ok = ready || mbar_wait(&bar[at], parity, abort, err);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        __syncwarp();
+        const int next = at + 1 == n ? 0 : at + 1;
+        ready = mbar_test_wait(&bar[next], next == 0 ? parity ^ 1u : parity);
+        return true;
+    }
+    __device__ __forceinline__ void advance() {
+        if (++at == n) {
+            at = 0;
+            parity ^= 1u;
+        }
+    }
+};
 
 // A tile: expert, first output row and how many of its rows exist, first column, and
 // where its K begins (WGRAD: 128-row blocks of the padded rows).
@@ -261,7 +306,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
         // epilogue warp (q, half): TMEM lanes 32 q .., columns half * COLS ..
         const int q = warp & 3, half = (warp - 4) >> 2;
         uint8_t* chunk = chunks + (warp - 4) * kChunk;
-        const uint32_t tempty_lead = mapa_shared(smem_u32(tempty), PAIR ? 0 : rank);
+        const uint32_t tempty_lead = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
         const uint32_t t_warp = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * C::COLS);
         const int in_tile = (PAIR ? static_cast<int>(rank) * kBM : 0) + q * 32;  // this warp's first row of the tile
         const long long a_ld = KIND == BLOCK_WGRAD ? args.M : list.kbs;
@@ -328,24 +373,34 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                 ok = __all_sync(0xffffffffu, mbar_wait(&tfull[slot], slot_phase, abort_flag, err));
                 if (!ok) break;
                 tc_fence_after();
+                auto release = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) slot_arrive(tempty_lead + 8u * slot);
+                        else mbar_arrive(&tempty[slot]);
+                    }
+                };
                 if (rows > 0) {
                     const uint32_t t_slot = t_warp + static_cast<uint32_t>(slot * BN);
+                    uint32_t r[2][32];
+                    tmem_ld_32x32(t_slot, r[0]);
 #pragma unroll
                     for (int c = 0; c < C::COLS; c += 32) {
-                        uint32_t r[32];
-                        tmem_ld_32x32(t_slot + c, r);
-                        tmem_ld_wait();
+                        uint32_t(&now)[32] = r[c / 32 & 1];
+                        tmem_landed(now);
+                        if (c + 32 < C::COLS) tmem_ld_32x32(t_slot + c + 32, r[(c / 32 + 1) & 1]);
+                        else release();  // the whole slot is in registers
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             float2 s2 = make_float2(s, s);
                             if constexpr (KIND == BLOCK_WGRAD) s2 = mul2(s2, *reinterpret_cast<const float2*>(s_cols + c + 2 * j));
-                            acc[c / 2 + j] = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[c / 2 + j]);
+                            acc[c / 2 + j] = fma2(make_float2(__uint_as_float(now[2 * j]), __uint_as_float(now[2 * j + 1])), s2, acc[c / 2 + j]);
                         }
                     }
+                } else {
+                    release();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(tempty_lead + 8u * slot);
                 if (++slot == C::SLOTS) { slot = 0; slot_phase ^= 1u; }
             }
             if (!ok) break;
@@ -411,42 +466,44 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                 if (!ok) settle_copies();  // some may be of stages that were never announced
             }
         } else if (warp == 1) {
-            if (lane == 0 && leader) {
+            if (leader) {
                 constexpr uint32_t idesc = block_idesc<KIND>(C::ROWS, BN);
-                int stage = 0, slot = 0;
-                uint32_t phase = 0, slot_phase = 0;
+                BarrierWalk stages(full, S, 0), slots(tempty, C::SLOTS, 1);
                 bool ok = true;
                 for (int t = first; ok && t < tiles; t += step) {
                     const BlockTile b = list.at<KIND>(t);
                     const int n = k_hi(b) - k_lo(b);
                     for (int kb = 0; kb < n; ++kb) {
-                        if (!mbar_wait(&tempty[slot], slot_phase ^ 1u, abort_flag, err) ||
-                            !mbar_wait(&full[stage], phase, abort_flag, err)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = stages.wait(abort_flag, err) && slots.wait(abort_flag, err);
+                        if (!ok) break;
                         tc_fence_after();
-                        const uint32_t d = tmem + static_cast<uint32_t>(slot * BN);
-                        const uint64_t ad = byte_desc<C::A_MN>(smem_u32(smem + stage * C::STAGE));
-                        const uint64_t bd = byte_desc<C::B_MN>(smem_u32(smem + stage * C::STAGE + kBoxBytes));
+                        const uint32_t d = tmem + static_cast<uint32_t>(slots.at * BN);
+                        const uint64_t ad = byte_desc<C::A_MN>(smem_u32(smem + stages.at * C::STAGE));
+                        const uint64_t bd = byte_desc<C::B_MN>(smem_u32(smem + stages.at * C::STAGE + kBoxBytes));
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if constexpr (PAIR) umma_e4m3_pair(d, ad + k * kByteStep<C::A_MN>, bd + k * kByteStep<C::B_MN>, idesc, k != 0);
-                            else umma_e4m3(d, ad + k * kByteStep<C::A_MN>, bd + k * kByteStep<C::B_MN>, idesc, k != 0);
+                            for (int k = 0; k < 4; ++k) {
+                                if constexpr (PAIR) umma_e4m3_pair(d, ad + k * kByteStep<C::A_MN>, bd + k * kByteStep<C::B_MN>, idesc, k != 0);
+                                else umma_e4m3(d, ad + k * kByteStep<C::A_MN>, bd + k * kByteStep<C::B_MN>, idesc, k != 0);
+                            }
+                            if constexpr (PAIR) {
+                                umma_commit_pair_multicast(&tfull[slots.at], 0x3);
+                                umma_commit_pair_multicast(&empty[stages.at], 0x3);
+                            } else {
+                                umma_commit(&tfull[slots.at]);
+                                umma_commit(&empty[stages.at]);
+                            }
                         }
-                        if constexpr (PAIR) {
-                            umma_commit_pair_multicast(&empty[stage], 0x3);
-                            umma_commit_pair_multicast(&tfull[slot], 0x3);
-                        } else {
-                            umma_commit(&empty[stage]);
-                            umma_commit(&tfull[slot]);
-                        }
-                        if (++stage == S) { stage = 0; phase ^= 1u; }
-                        if (++slot == C::SLOTS) { slot = 0; slot_phase ^= 1u; }
+                        __syncwarp();
+                        stages.advance();
+                        slots.advance();
                     }
                 }
-                if constexpr (PAIR) umma_commit_pair_multicast(drain, 0x3);
-                else umma_commit(drain);
+                if (elect_one()) {
+                    if constexpr (PAIR) umma_commit_pair_multicast(drain, 0x3);
+                    else umma_commit(drain);
+                }
+                __syncwarp();
             }
         }
     }
