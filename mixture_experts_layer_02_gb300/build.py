@@ -30,7 +30,7 @@ SOURCES = ["grouped_gemm.cu", "grouped_gemm_e4m3.cu", "grouped_gemm_2sm.cu", "gr
            "dense_gemm_pairsplit_gated.cu", "dense_gemm_pairsplit_linear.cu", "dense_gemm_pairsplit_dgrad.cu",
            "dense_gemm_pairsplit_wgrad.cu",
            "dense_gemm_pair.cu", "dense_gemv.cu", "dense_api.cu",
-           "routing_grad.cu", "quant_block.cu", "block_gemm_fwd.cu", "block_gemm_dgrad.cu", "block_gemm_wgrad.cu",
+           "routing_grad.cu", "quant_block.cu", "block_gemm_fwd.cu", "block_gemm_dgrad.cu", "block_gemm_wgrad.cu", "block_gemv.cu",
            "train_api.cu",
            "moe_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -267,7 +267,10 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
     for (int i = threadIdx.x; i < E; i += kThreads) bad |= s_goff[i] > s_goff[i + 1];
     bad = __syncthreads_or(bad);
     if (bad && blockIdx.x == 0 && threadIdx.x == 0) record_error(err, MOE_DEVERR_BOUNDS);
-    heaviest_first(s_goff, E, s_ord);
+    // tiles of FWD and DGRAD cost the same; WGRAD's go by their expert's rows, the longest first
+    if constexpr (KIND == BLOCK_WGRAD) heaviest_first(s_goff, E, s_ord);
+    else
+        for (int i = threadIdx.x; i < E; i += kThreads) s_ord[i] = i;
     __syncthreads();
     if (warp == 0) {  // exclusive prefix of row tiles in list order, or of the padded rows' blocks by expert
         constexpr int UNIT = KIND == BLOCK_WGRAD ? kBlock : C::ROWS;
@@ -314,62 +317,83 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
         uint32_t slot_phase = 0;
         bool ok = true;
         float2 acc[C::COLS / 2];
+        // The scales of a tile: one of the row a step, and one of the column block (WGRAD: one a
+        // column).  The row's index comes in during the tile before, the first step's scales
+        // under its stores: read when they are needed, they cost 1.2 us a tile.
+        struct Scales {
+            const float *sa, *sb;
+            float a;
+            union {
+                float b;
+                float4 b4;
+            };
+        };
+        const int nbs = (args.N + kBlock - 1) / kBlock;
+        const long long sb_step = KIND == BLOCK_WGRAD ? args.N : (KIND == BLOCK_FWD ? 1 : nbs);
+        auto index_of = [&](const BlockTile& b) {  // the row of a_scale, -1: none
+            const bool valid = in_tile + lane < b.rows;
+            if constexpr (KIND == BLOCK_WGRAD) return valid ? b.row0 + in_tile + lane : -1;
+            const int r = b.row0 + in_tile + lane;
+            return !valid ? -1 : (args.a_index ? args.a_index[r] : r);
+        };
+        auto a_of = [&](const Scales& c, int kb, int hi) { return c.sa && kb < hi ? c.sa[KIND == BLOCK_WGRAD ? kb * a_ld : kb] : 0.0f; };
+        auto b_of = [&](const Scales& c, int kb, int hi) { return kb < hi ? c.sb[kb * sb_step] : 0.0f; };
+        // WGRAD: this lane's four columns of the step's scales, zero outside
+        auto b4_of = [&](const Scales& c, int col0, int kb, int hi) {
+            const int j = lane * 4;
+            return j < C::COLS && col0 + j < args.N && kb < hi ? *reinterpret_cast<const float4*>(c.sb + kb * sb_step + j)
+                                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        };
+        auto scales_of = [&](const BlockTile& b, int index) {
+            Scales c;
+            const int col0 = b.n0 + half * C::COLS, lo = k_lo(b), hi = k_hi(b);
+            c.sa = nullptr;
+            if constexpr (KIND == BLOCK_WGRAD) {
+                if (index >= 0) c.sa = args.a_scale + static_cast<long long>(b.k0) * a_ld + index;
+                c.sb = args.b_scale + static_cast<long long>(b.k0) * args.N + col0;
+                c.b4 = b4_of(c, col0, lo, hi);
+            } else {
+                if (index >= 0 && index < args.a_scale_rows) c.sa = args.a_scale + index * a_ld;
+                else if (in_tile + lane < b.rows) record_error(err, MOE_DEVERR_BOUNDS);
+                // [blocks of F, blocks of D]: FWD walks along a row, DGRAD down a column
+                const int nb = min(col0, args.N - 1) / kBlock;
+                c.sb = args.b_scale + static_cast<long long>(b.e) * list.kbs * nbs + (KIND == BLOCK_FWD ? static_cast<long long>(nb) * list.kbs : nb);
+                c.b = b_of(c, lo, hi);
+            }
+            c.a = a_of(c, lo, hi);
+            return c;
+        };
+        BlockTile b = {};
+        Scales sc = {};
+        if (first < tiles) {
+            b = list.at<KIND>(first);
+            sc = scales_of(b, index_of(b));
+        }
         for (int t = first; ok && t < tiles; t += step) {
-            const BlockTile b = list.at<KIND>(t);
             const int lo = k_lo(b), hi = k_hi(b);
             const int rows = min(32, b.rows - in_tile);  // of this warp; <= 0: none exist
-            const bool valid = lane < rows;
             const int col0 = b.n0 + half * C::COLS;
-            // scales: one of the row a step, and one of the column block (WGRAD: one a column)
-            const float *sa = nullptr, *sb = nullptr;
-            long long sb_step = 0;
-            if constexpr (KIND == BLOCK_WGRAD) {
-                if (valid) sa = args.a_scale + static_cast<long long>(b.k0) * a_ld + b.row0 + in_tile + lane;
-                sb = args.b_scale + static_cast<long long>(b.k0) * args.N + col0;
-            } else {
-                const long long r = static_cast<long long>(b.row0) + in_tile + lane;
-                if (valid) {
-                    long long s = r;
-                    if (args.a_index) {
-                        s = args.a_index[r];
-                        if (s < 0 || s >= args.a_scale_rows) {
-                            record_error(err, MOE_DEVERR_BOUNDS);
-                            s = -1;
-                        }
-                    }
-                    if (s >= 0) sa = args.a_scale + s * a_ld;
-                }
-                // [blocks of F, blocks of D]: FWD walks along a row, DGRAD down a column
-                const int nb = min(col0, args.N - 1) / kBlock, nbs = (args.N + kBlock - 1) / kBlock;
-                sb = args.b_scale + static_cast<long long>(b.e) * list.kbs * nbs + (KIND == BLOCK_FWD ? static_cast<long long>(nb) * list.kbs : nb);
-                sb_step = KIND == BLOCK_FWD ? 1 : nbs;
+            const bool more = SPLITS == 1 && t + step < tiles;
+            BlockTile next = {};
+            int next_index = -1;
+            if (more) {
+                next = list.at<KIND>(t + step);
+                next_index = index_of(next);
             }
-            auto a_of = [&](int kb) { return sa && kb < hi ? sa[KIND == BLOCK_WGRAD ? kb * a_ld : kb] : 0.0f; };
-            // WGRAD: this lane's four columns of the step's scales, zero outside
-            auto b4_of = [&](int kb) {
-                const int c = lane * 4;
-                return c < C::COLS && col0 + c < args.N && kb < hi
-                           ? *reinterpret_cast<const float4*>(sb + static_cast<long long>(kb) * args.N + c)
-                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            };
-            auto b_of = [&](int kb) { return kb < hi ? sb[kb * sb_step] : 0.0f; };
-            float a_next = a_of(lo), b_next = 0.0f;
-            float4 b4_next = {};
-            if constexpr (KIND == BLOCK_WGRAD) b4_next = b4_of(lo);
-            else b_next = b_of(lo);
 #pragma unroll
             for (int i = 0; i < C::COLS / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
             for (int kb = lo; kb < hi; ++kb) {
-                const float s = KIND == BLOCK_WGRAD ? a_next : a_next * b_next;
+                const float s = KIND == BLOCK_WGRAD ? sc.a : sc.a * sc.b;
                 float* s_cols = reinterpret_cast<float*>(chunk) + (kb & 1) * 128;
                 if constexpr (KIND == BLOCK_WGRAD) {
-                    if (lane * 4 < C::COLS) *reinterpret_cast<float4*>(s_cols + lane * 4) = b4_next;
-                    b4_next = b4_of(kb + 1);
+                    if (lane * 4 < C::COLS) *reinterpret_cast<float4*>(s_cols + lane * 4) = sc.b4;
+                    sc.b4 = b4_of(sc, col0, kb + 1, hi);
+                    __syncwarp();
                 } else {
-                    b_next = b_of(kb + 1);
+                    sc.b = b_of(sc, kb + 1, hi);
                 }
-                a_next = a_of(kb + 1);
+                sc.a = a_of(sc, kb + 1, hi);
                 ok = __all_sync(0xffffffffu, mbar_wait(&tfull[slot], slot_phase, abort_flag, err));
                 if (!ok) break;
                 tc_fence_after();
@@ -404,6 +428,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                 if (++slot == C::SLOTS) { slot = 0; slot_phase ^= 1u; }
             }
             if (!ok) break;
+            if (more) sc = scales_of(next, next_index);
             if constexpr (SPLITS == 1) {
                 uint16_t* out = args.out + (KIND == BLOCK_WGRAD ? static_cast<long long>(b.e) * args.M * args.N : 0);
                 if (rows > 0)
@@ -412,12 +437,13 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                         store_chunk(chunk, *reinterpret_cast<const float2(*)[16]>(&acc[c / 2]), out,
                                     static_cast<long long>(b.row0) + in_tile, rows, col0 + c, args.N, lane);
                 __syncwarp();  // WGRAD: the next tile's scales go where the chunk was
-            } else if (valid) {  // the stages are free: every copy of this CTA's part was waited for
+            } else if (lane < rows) {  // the stages are free: every copy of this CTA's part was waited for
 #pragma unroll
                 for (int i = 0; i < C::COLS / 4; ++i)
                     *reinterpret_cast<float4*>(smem + park_quad(in_tile + lane, half * (C::COLS / 4) + i)) =
                         make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
             }
+            b = next;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));

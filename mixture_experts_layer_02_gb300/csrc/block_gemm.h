@@ -28,6 +28,7 @@ struct BlockArgs {
 // over K in `splits` parts joined over a cluster (bn = 128; then at most one tile a
 // cluster).  `tiles` bounds the number of tiles.
 struct BlockPlan {
+    int stream;  // not 0: no tiles but the stream of weight rows, with this many warps a row (FWD)
     bool pair;
     int bn, splits;
     long long tiles;
@@ -40,5 +41,9 @@ cudaError_t block_dgrad(const BlockPlan&, const CUtensorMap* a_map, const CUtens
                         int* clusters);
 cudaError_t block_wgrad(const BlockPlan&, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs*, cudaStream_t,
                         int* clusters);
+
+// BLOCK_FWD of a few rows an expert as a stream of weight rows, `warps` (1, 2, 4 or 8)
+// of a block's 8 sharing the same rows (block_gemv.cu).
+cudaError_t launch_block_gemv(const uint8_t* x, const uint8_t* w, const BlockArgs& a, int warps, cudaStream_t st);
 
 }  // namespace moe

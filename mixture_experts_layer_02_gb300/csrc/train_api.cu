@@ -103,37 +103,43 @@ long long row_tiles(const BlockArgs& a, int height) {
     return some + (a.rows - some) / height;
 }
 
-// MOE_BLOCK_KERNEL = 1 (128 x 128), 2 (128 x 256) or 3 (pairs), and with 1
-// MOE_BLOCK_SPLIT = parts of K, force a choice, for tuning and test coverage.
-moe_status plan_block(BlockKind kind, const BlockArgs& a, BlockPlan* p) {
+// MOE_BLOCK_KERNEL = 1 (128 x 128), 2 (128 x 256), 3 (pairs) or 4 (stream, FWD only), and
+// MOE_BLOCK_SPLIT = parts of K (1) or warps a row (4), force a choice, for tuning and test
+// coverage.
+BlockPlan plan_block(BlockKind kind, const BlockArgs& a) {
     auto tiles = [&](int height, int width) {
         const long long n = (a.N + width - 1) / width;
         return kind == BLOCK_WGRAD ? a.E * ((a.M + height - 1) / static_cast<long long>(height)) * n : row_tiles(a, height) * n;
     };
-    const int kernel = env_int("MOE_BLOCK_KERNEL", 0);
-    *p = {false, 128, 1, tiles(kBM, 128)};
+    int kernel = env_int("MOE_BLOCK_KERNEL", 0);
+    const int fixed = kernel ? env_int("MOE_BLOCK_SPLIT", 1) : 0;
     const long long mean = kind == BLOCK_WGRAD ? a.M : a.rows / a.E;
-    int want = kernel;
-    if (want == 0) want = mean >= 160 && tiles(2 * kBM, 256) >= 38 ? 3 : (tiles(kBM, 256) >= 120 ? 2 : 1);
-    if (want == 3) *p = {true, 256, 1, tiles(2 * kBM, 256)};
-    else if (want == 2) *p = {false, 256, 1, tiles(kBM, 256)};
-    else {
-        int splits = kernel ? env_int("MOE_BLOCK_SPLIT", 1) : 0;
-        const long long kbs = kind == BLOCK_WGRAD ? blocks_of(a.rows) : blocks_of(a.K);
-        if (!splits) {
-            splits = 1;
-            while (splits < 8 && p->tiles * splits * 2 <= 152 && kbs >= 4 * splits) splits *= 2;
+    if (kernel == 4 && kind != BLOCK_FWD) kernel = 1;
+    if (kernel == 0) kernel = kind == BLOCK_FWD && (a.rows <= 8 || mean <= 1) ? 4 : (mean >= 160 && tiles(2 * kBM, 256) >= 38 ? 3 : (tiles(kBM, 256) >= 120 ? 2 : 1));
+    if (kernel == 4) {
+        int warps = fixed;
+        if (!warps) {  // enough warps for the GPU, each with a few blocks
+            const long long units = static_cast<long long>(std::min(a.rows, a.E)) * ((a.N + 15) / 16);
+            warps = 1;
+            while (warps < 8 && units * warps < 152 * 12 && blocks_of(a.K) >= 4 * warps) warps *= 2;
         }
-        p->splits = splits;
+        return {warps, false, 0, 0, 0};
     }
-    return MOE_OK;
+    if (kernel == 3) return {0, true, 256, 1, tiles(2 * kBM, 256)};
+    if (kernel == 2) return {0, false, 256, 1, tiles(kBM, 256)};
+    int splits = fixed;
+    const long long n = tiles(kBM, 128), kbs = kind == BLOCK_WGRAD ? blocks_of(a.rows) : blocks_of(a.K);
+    if (!splits) {
+        splits = 1;
+        while (splits < 4 && n * splits * 2 <= 152 && kbs >= 4 * splits) splits *= 2;
+    }
+    return {0, false, 128, splits, n};
 }
 
 moe_status product(BlockKind kind, const uint8_t* a_codes, long long a_rows, long long a_cols, const uint8_t* b_codes,
                    long long b_mats, long long b_rows, long long b_cols, const BlockArgs& a, cudaStream_t st) {
-    BlockPlan p;
-    moe_status s = plan_block(kind, a, &p);
-    if (s != MOE_OK) return s;
+    const BlockPlan p = plan_block(kind, a);
+    if (p.stream) return launched(launch_block_gemv(a_codes, b_codes, a, p.stream, st), "block-scaled product launch");
     CUtensorMap am, bm;
     int e = make_byte_map(&am, a_codes, 1, a_rows, a_cols);
     if (e == 0) e = make_byte_map(&bm, b_codes, b_mats, b_rows, b_cols);
