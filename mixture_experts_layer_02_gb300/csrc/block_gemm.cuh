@@ -20,10 +20,12 @@
 // multiple of 128 on with zero rows behind them (quant_block.cu).  Boxes are 128 x 128
 // bytes; what lies outside a matrix reads as zeros, so K needs no multiple.
 //
-// Warps: 0 copies A, 1 issues the MMAs, 2 copies B, 3 allocates TMEM, 4..11 epilogue.
+// Warps: 0 copies A, 1 issues the MMAs, 2 copies B, 3 allocates TMEM and brings a step's
+// scales to shared memory, 4..11 epilogue.
 // Registers are dealt out anew at the start: the epilogue's accumulators take 128.
 // Barriers: full[s] the bytes of a stage (of both CTAs, on the even one's), empty[s]
-// its MMAs are done, tfull[i] a slot is filled, tempty[i] its readers are through.
+// its MMAs are done, tfull[i] a slot and its scales are filled, tempty[i] (of the pair) and
+// sempty[i] (of a CTA) its readers are through.
 // Every wait is bounded (1 s); none spans more than one step of 128 along K.
 #pragma once
 
@@ -44,6 +46,7 @@ constexpr int kBoxBytes = kBlock * kRowBytes;  // 128 rows of 128 bytes
 constexpr int kStageRoom = 192 * 1024;
 constexpr int kChunk = 2048;                   // an epilogue warp's staging: 32 rows of 64 bytes
 constexpr int kMaxE = 1024;
+constexpr int kScaleRoom = 4096;               // a step's scales, for every slot
 constexpr int kCopyRegs = 72, kEpiRegs = 216;  // registers a thread of warps 0..3 and 4..11
 
 template <int KIND, bool PAIR, int BN, int SPLITS>
@@ -58,12 +61,16 @@ struct BlockCfg {
     static constexpr int SLOTS = 512 / BN;                     // partial sums in TMEM
     static constexpr int COLS = BN / 2;                        // accumulator columns of an epilogue warp
     static constexpr int CLUSTER = CTAS * SPLITS;
+    // a slot's scales: FWD and DGRAD one of each row for either half of the columns, WGRAD
+    // one of each row, then one of each column
+    static constexpr int SCALES = A_MN ? kBM + BN : 2 * kBM;
+    static_assert(SLOTS * SCALES * 4 <= kScaleRoom, "scale room");
     static_assert(!PAIR || (BN == 256 && SPLITS == 1), "pairs own whole 256 x 256 tiles");
     static_assert(SPLITS == 1 || BN == 128, "parts of K are joined on 128 x 128 tiles");
 };
 
 constexpr size_t block_smem(int E) {
-    return 1024 + kStageRoom + kEpiWarps * kChunk + 48 * sizeof(uint64_t) + (3 * static_cast<size_t>(E) + 2) * sizeof(int);
+    return 1024 + kStageRoom + kEpiWarps * kChunk + kScaleRoom + 48 * sizeof(uint64_t) + (3 * static_cast<size_t>(E) + 2) * sizeof(int);
 }
 
 __device__ __forceinline__ void load_box(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
@@ -89,6 +96,21 @@ __device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
                    "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
                    "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
                    "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[64]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]),
+                   "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]), "+r"(r[40]), "+r"(r[41]), "+r"(r[42]),
+                   "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]), "+r"(r[48]), "+r"(r[49]),
+                   "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]), "+r"(r[56]),
+                   "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
                  :
                  : "memory");
 }
@@ -178,23 +200,92 @@ struct TileList {
     }
 };
 
+// 32 lanes x 64 consecutive fp32 columns, a row a thread; and 32 of them.
+__device__ __forceinline__ void tmem_ld_wide(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+        "}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+          "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+          "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
+          "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_wide(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+        "}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// 16 lanes x 128 consecutive fp32 columns in the layout of an MMA's accumulator: thread T
+// gets columns 8 j + 2 (T % 4) and the next of rows T / 4 (r[4 j], r[4 j + 1]) and T / 4 + 8
+// (r[4 j + 2], r[4 j + 3]); and 64 of them.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x16.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
+        "}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+          "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+          "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
+          "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
+        "}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Four 8 x 8 blocks of 16-bit values, in the same layout, to rows of 16 bytes: thread T
+// has the address of row T % 8 of block T / 8.
+__device__ __forceinline__ void st_blocks(void* row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(row)), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 // 32 rows x 32 columns of a warp leave as 64-byte pieces of eight rows: stored as they
 // lie, one row a thread, a 16-byte store would touch 32 rows at once.
-__device__ __forceinline__ void store_chunk(uint8_t* smem, const float2 (&v)[16], uint16_t* out, long long row0, int rows, int col0,
-                                            int N, int lane) {
-    auto cell = [&](int r, int p) { return reinterpret_cast<uint4*>(smem + r * 64 + ((p ^ ((r >> 1) & 3)) << 4)); };
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *cell(lane, i) = make_uint4(pack_bf16x2(v[4 * i].x, v[4 * i].y), pack_bf16x2(v[4 * i + 1].x, v[4 * i + 1].y),
-                                    pack_bf16x2(v[4 * i + 2].x, v[4 * i + 2].y), pack_bf16x2(v[4 * i + 3].x, v[4 * i + 3].y));
+__device__ __forceinline__ uint4* chunk_cell(uint8_t* smem, int r, int piece) {
+    return reinterpret_cast<uint4*>(smem + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ void store_chunk(uint8_t* smem, uint16_t* out, long long row0, int rows, int col0, int N, int lane) {
     __syncwarp();
     const int col = col0 + (lane & 3) * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + (lane >> 2);
-        if (r < rows && col < N) *reinterpret_cast<uint4*>(out + (row0 + r) * N + col) = *cell(r, lane & 3);
+        if (r < rows && col < N) *reinterpret_cast<uint4*>(out + (row0 + r) * N + col) = *chunk_cell(smem, r, lane & 3);
     }
+    __syncwarp();
 }
 
 // The accumulator of one k-part, parked in shared memory: 128 rows of 128 fp32, the
@@ -217,17 +308,19 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);  // the same offset in every CTA of a cluster
     uint8_t* chunks = smem + kStageRoom;
-    uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kEpiWarps * kChunk);
+    float* scales = reinterpret_cast<float*>(chunks + kEpiWarps * kChunk);
+    uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kEpiWarps * kChunk + kScaleRoom);
     uint64_t* empty = full + S;
     uint64_t* tfull = empty + S;
     uint64_t* tempty = tfull + C::SLOTS;
-    uint64_t* drain = tempty + C::SLOTS;
+    uint64_t* sempty = PAIR ? tempty + C::SLOTS : tempty;
+    uint64_t* drain = tempty + 2 * C::SLOTS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* s_goff = reinterpret_cast<int*>(full + 48);  // [E + 1]
     int* s_pre = s_goff + args.E + 1;                 // [E + 1]
     int* s_ord = s_pre + args.E + 1;                  // [E]
-    static_assert(2 * S + 2 * C::SLOTS + 1 + 1 <= 48, "barrier room");
+    static_assert(2 * S + 3 * C::SLOTS + 1 + 1 <= 48, "barrier room");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = args.E;
@@ -244,8 +337,9 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
             mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < C::SLOTS; ++i) {
-            mbar_init(&tfull[i], 1);
+            mbar_init(&tfull[i], 2);  // the MMAs' commit, the scales
             mbar_init(&tempty[i], C::CTAS * kEpiWarps);
+            if (PAIR) mbar_init(&sempty[i], kEpiWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -312,88 +406,24 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
         const uint32_t tempty_lead = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
         const uint32_t t_warp = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * C::COLS);
         const int in_tile = (PAIR ? static_cast<int>(rank) * kBM : 0) + q * 32;  // this warp's first row of the tile
-        const long long a_ld = KIND == BLOCK_WGRAD ? args.M : list.kbs;
         int slot = 0;
         uint32_t slot_phase = 0;
         bool ok = true;
+        // Who holds what: in FWD and DGRAD a thread has one row, so that a step's two scales are
+        // one number to it.  In WGRAD, where every column has its own, it has four rows (lane /
+        // 4 and every 8th after it) and every fourth pair of columns: a quarter of the scales
+        // to read from shared memory, which the MMAs' operands keep busy as well.
+        constexpr int ROWS = KIND == BLOCK_WGRAD ? 4 : 1;
+        const float* my_scales = scales + (KIND == BLOCK_WGRAD ? q * 32 + (lane >> 2) : half * kBM + q * 32 + lane);
+        const float* my_columns = scales + kBM + half * C::COLS + (lane & 3) * 2;  // WGRAD
         float2 acc[C::COLS / 2];
-        // The scales of a tile: one of the row a step, and one of the column block (WGRAD: one a
-        // column).  The row's index comes in during the tile before, the first step's scales
-        // under its stores: read when they are needed, they cost 1.2 us a tile.
-        struct Scales {
-            const float *sa, *sb;
-            float a;
-            union {
-                float b;
-                float4 b4;
-            };
-        };
-        const int nbs = (args.N + kBlock - 1) / kBlock;
-        const long long sb_step = KIND == BLOCK_WGRAD ? args.N : (KIND == BLOCK_FWD ? 1 : nbs);
-        auto index_of = [&](const BlockTile& b) {  // the row of a_scale, -1: none
-            const bool valid = in_tile + lane < b.rows;
-            if constexpr (KIND == BLOCK_WGRAD) return valid ? b.row0 + in_tile + lane : -1;
-            const int r = b.row0 + in_tile + lane;
-            return !valid ? -1 : (args.a_index ? args.a_index[r] : r);
-        };
-        auto a_of = [&](const Scales& c, int kb, int hi) { return c.sa && kb < hi ? c.sa[KIND == BLOCK_WGRAD ? kb * a_ld : kb] : 0.0f; };
-        auto b_of = [&](const Scales& c, int kb, int hi) { return kb < hi ? c.sb[kb * sb_step] : 0.0f; };
-        // WGRAD: this lane's four columns of the step's scales, zero outside
-        auto b4_of = [&](const Scales& c, int col0, int kb, int hi) {
-            const int j = lane * 4;
-            return j < C::COLS && col0 + j < args.N && kb < hi ? *reinterpret_cast<const float4*>(c.sb + kb * sb_step + j)
-                                                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        };
-        auto scales_of = [&](const BlockTile& b, int index) {
-            Scales c;
-            const int col0 = b.n0 + half * C::COLS, lo = k_lo(b), hi = k_hi(b);
-            c.sa = nullptr;
-            if constexpr (KIND == BLOCK_WGRAD) {
-                if (index >= 0) c.sa = args.a_scale + static_cast<long long>(b.k0) * a_ld + index;
-                c.sb = args.b_scale + static_cast<long long>(b.k0) * args.N + col0;
-                c.b4 = b4_of(c, col0, lo, hi);
-            } else {
-                if (index >= 0 && index < args.a_scale_rows) c.sa = args.a_scale + index * a_ld;
-                else if (in_tile + lane < b.rows) record_error(err, MOE_DEVERR_BOUNDS);
-                // [blocks of F, blocks of D]: FWD walks along a row, DGRAD down a column
-                const int nb = min(col0, args.N - 1) / kBlock;
-                c.sb = args.b_scale + static_cast<long long>(b.e) * list.kbs * nbs + (KIND == BLOCK_FWD ? static_cast<long long>(nb) * list.kbs : nb);
-                c.b = b_of(c, lo, hi);
-            }
-            c.a = a_of(c, lo, hi);
-            return c;
-        };
-        BlockTile b = {};
-        Scales sc = {};
-        if (first < tiles) {
-            b = list.at<KIND>(first);
-            sc = scales_of(b, index_of(b));
-        }
         for (int t = first; ok && t < tiles; t += step) {
-            const int lo = k_lo(b), hi = k_hi(b);
+            const BlockTile b = list.at<KIND>(t);
             const int rows = min(32, b.rows - in_tile);  // of this warp; <= 0: none exist
-            const int col0 = b.n0 + half * C::COLS;
-            const bool more = SPLITS == 1 && t + step < tiles;
-            BlockTile next = {};
-            int next_index = -1;
-            if (more) {
-                next = list.at<KIND>(t + step);
-                next_index = index_of(next);
-            }
 #pragma unroll
             for (int i = 0; i < C::COLS / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
 #pragma unroll 1
-            for (int kb = lo; kb < hi; ++kb) {
-                const float s = KIND == BLOCK_WGRAD ? sc.a : sc.a * sc.b;
-                float* s_cols = reinterpret_cast<float*>(chunk) + (kb & 1) * 128;
-                if constexpr (KIND == BLOCK_WGRAD) {
-                    if (lane * 4 < C::COLS) *reinterpret_cast<float4*>(s_cols + lane * 4) = sc.b4;
-                    sc.b4 = b4_of(sc, col0, kb + 1, hi);
-                    __syncwarp();
-                } else {
-                    sc.b = b_of(sc, kb + 1, hi);
-                }
-                sc.a = a_of(sc, kb + 1, hi);
+            for (int n = k_hi(b) - k_lo(b); n > 0; --n) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&tfull[slot], slot_phase, abort_flag, err));
                 if (!ok) break;
                 tc_fence_after();
@@ -402,48 +432,80 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                     __syncwarp();
                     if (lane == 0) {
                         if constexpr (PAIR) slot_arrive(tempty_lead + 8u * slot);
-                        else mbar_arrive(&tempty[slot]);
+                        mbar_arrive(&sempty[slot]);
                     }
                 };
                 if (rows > 0) {
+                    float s[ROWS];
+#pragma unroll
+                    for (int i = 0; i < ROWS; ++i) s[i] = my_scales[slot * C::SCALES + 8 * i];
+                    // half of the columns at a time (WGRAD: half of the rows)
                     const uint32_t t_slot = t_warp + static_cast<uint32_t>(slot * BN);
-                    uint32_t r[2][32];
-                    tmem_ld_32x32(t_slot, r[0]);
 #pragma unroll
-                    for (int c = 0; c < C::COLS; c += 32) {
-                        uint32_t(&now)[32] = r[c / 32 & 1];
-                        tmem_landed(now);
-                        if (c + 32 < C::COLS) tmem_ld_32x32(t_slot + c + 32, r[(c / 32 + 1) & 1]);
-                        else release();  // the whole slot is in registers
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t r[C::COLS / 2];
+                        if constexpr (KIND == BLOCK_WGRAD) tmem_ld_frag(t_slot + (static_cast<uint32_t>(c * 16) << 16), r);
+                        else tmem_ld_wide(t_slot + c * (C::COLS / 2), r);
+                        tmem_landed(r);
+                        if (KIND != BLOCK_WGRAD && c == 1) release();  // all that this warp reads of the slot is in registers
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 s2 = make_float2(s, s);
-                            if constexpr (KIND == BLOCK_WGRAD) s2 = mul2(s2, *reinterpret_cast<const float2*>(s_cols + c + 2 * j));
-                            acc[c / 2 + j] = fma2(make_float2(__uint_as_float(now[2 * j]), __uint_as_float(now[2 * j + 1])), s2, acc[c / 2 + j]);
+                        for (int j = 0; j < C::COLS / 4; ++j) {
+                            float2 v = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                            float f = s[0];
+                            if constexpr (KIND == BLOCK_WGRAD) {
+                                v = mul2(v, *reinterpret_cast<const float2*>(my_columns + slot * C::SCALES + (j >> 1) * 8));
+                                f = s[c * 2 + (j & 1)];
+                            }
+                            acc[c * (C::COLS / 4) + j] = fma2(v, make_float2(f, f), acc[c * (C::COLS / 4) + j]);
                         }
                     }
+                    if (KIND == BLOCK_WGRAD) release();  // the columns' scales were read to the end
                 } else {
                     release();
                 }
                 if (++slot == C::SLOTS) { slot = 0; slot_phase ^= 1u; }
             }
             if (!ok) break;
-            if (more) sc = scales_of(next, next_index);
+            const int col0 = b.n0 + half * C::COLS;
             if constexpr (SPLITS == 1) {
                 uint16_t* out = args.out + (KIND == BLOCK_WGRAD ? static_cast<long long>(b.e) * args.M * args.N : 0);
+                const long long row0 = static_cast<long long>(b.row0) + in_tile;
                 if (rows > 0)
 #pragma unroll
-                    for (int c = 0; c < C::COLS; c += 32)
-                        store_chunk(chunk, *reinterpret_cast<const float2(*)[16]>(&acc[c / 2]), out,
-                                    static_cast<long long>(b.row0) + in_tile, rows, col0 + c, args.N, lane);
-                __syncwarp();  // WGRAD: the next tile's scales go where the chunk was
-            } else if (lane < rows) {  // the stages are free: every copy of this CTA's part was waited for
+                    for (int c = 0; c < C::COLS / 32; ++c) {
+                        if constexpr (KIND == BLOCK_WGRAD) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {  // eight columns of four times eight rows
+                                auto two = [&](int i) {
+                                    const float2 v = acc[(i >> 1) * (C::COLS / 4) + (c * 4 + j) * 2 + (i & 1)];
+                                    return pack_bf16x2(v.x, v.y);
+                                };
+                                st_blocks(chunk_cell(chunk, lane, j), two(0), two(1), two(2), two(3));
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2* v = &acc[c * 16 + i * 4];
+                                *chunk_cell(chunk, lane, i) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                                                         pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+                            }
+                        }
+                        store_chunk(chunk, out, row0, rows, col0 + c * 32, args.N, lane);
+                    }
+            } else if constexpr (KIND == BLOCK_WGRAD) {  // the stages are free: every copy of this CTA's part was waited for
+#pragma unroll
+                for (int i = 0; i < C::COLS / 2; ++i) {
+                    // acc[i]: 16 rows of i / (COLS / 4), columns 8 (i / 2) + 2 (lane % 4), rows lane / 4 + 8 (i % 2)
+                    const int j = i % (C::COLS / 4), r = (lane >> 2) + 8 * (j & 1) + 16 * (i / (C::COLS / 4));
+                    const int col = half * C::COLS + (j >> 1) * 8 + (lane & 3) * 2;
+                    if (r < rows) *reinterpret_cast<float2*>(smem + park_quad(in_tile + r, col >> 2) + (col & 2) * 4) = acc[i];
+                }
+            } else if (lane < rows) {
 #pragma unroll
                 for (int i = 0; i < C::COLS / 4; ++i)
                     *reinterpret_cast<float4*>(smem + park_quad(in_tile + lane, half * (C::COLS / 4) + i)) =
                         make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
             }
-            b = next;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
@@ -530,6 +592,88 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                     else umma_commit(drain);
                 }
                 __syncwarp();
+            }
+        } else {
+            // scales: rows 4 lane .. of this CTA, and the columns; loaded kAhead steps before their use
+            constexpr int kAhead = 2, COLS4 = BN / 128;  // WGRAD: column quads of a lane
+            BarrierWalk slots(sempty, C::SLOTS, 1);
+            bool ok = true;
+            const int nbs = (args.N + kBlock - 1) / kBlock;
+            const int in_tile = (PAIR ? static_cast<int>(rank) * kBM : 0) + lane * 4;  // this lane's first row of the tile
+            for (int t = first; ok && t < tiles; t += step) {
+                const BlockTile b = list.at<KIND>(t);
+                const int lo = k_lo(b), hi = k_hi(b);
+                const float *sa[4], *sb[2];
+                if constexpr (KIND == BLOCK_WGRAD) {
+                    sa[0] = args.a_scale + static_cast<long long>(b.k0) * args.M + b.row0 + in_tile;
+                    sb[0] = args.b_scale + static_cast<long long>(b.k0) * args.N + b.n0;
+                } else {
+                    int at[4];  // the row of a_scale, -1: no row
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = b.row0 + in_tile + i;
+                        at[i] = in_tile + i >= b.rows ? -1 : (args.a_index ? args.a_index[r] : r);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = at[i] >= 0 && at[i] < args.a_scale_rows;
+                        if (!in && in_tile + i < b.rows) record_error(err, MOE_DEVERR_BOUNDS);
+                        sa[i] = in ? args.a_scale + static_cast<long long>(at[i]) * list.kbs : nullptr;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // [blocks of F, blocks of D]: FWD walks along a row, DGRAD down a column
+                        const int nb = min(b.n0 + h * C::COLS, args.N - 1) / kBlock;
+                        sb[h] = args.b_scale + static_cast<long long>(b.e) * list.kbs * nbs + (KIND == BLOCK_FWD ? static_cast<long long>(nb) * list.kbs : nb);
+                    }
+                }
+                float va[kAhead][4], vb[kAhead][KIND == BLOCK_WGRAD ? 4 * COLS4 : 2];
+                auto load = [&](int u, int kb) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (KIND == BLOCK_WGRAD) va[u][i] = kb < hi && in_tile + i < b.rows ? sa[0][static_cast<long long>(kb) * args.M + i] : 0.0f;
+                        else va[u][i] = kb < hi && sa[i] ? sa[i][kb] : 0.0f;
+                    }
+                    if constexpr (KIND == BLOCK_WGRAD) {
+#pragma unroll
+                        for (int c = 0; c < COLS4; ++c) {
+                            const int col = c * 128 + lane * 4;
+                            const float4 v = kb < hi && b.n0 + col < args.N
+                                                 ? *reinterpret_cast<const float4*>(sb[0] + static_cast<long long>(kb) * args.N + col)
+                                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            vb[u][4 * c] = v.x, vb[u][4 * c + 1] = v.y, vb[u][4 * c + 2] = v.z, vb[u][4 * c + 3] = v.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) vb[u][h] = kb < hi ? sb[h][KIND == BLOCK_FWD ? kb : static_cast<long long>(kb) * nbs] : 0.0f;
+                    }
+                };
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) load(u, lo + u);
+                for (int kb = lo; ok && kb < hi; kb += kAhead) {
+#pragma unroll
+                    for (int u = 0; u < kAhead; ++u) {
+                        if (kb + u >= hi) break;
+                        ok = slots.wait(abort_flag, err);
+                        if (!ok) break;
+                        float* dst = scales + slots.at * C::SCALES;
+                        if constexpr (KIND == BLOCK_WGRAD) {
+                            *reinterpret_cast<float4*>(dst + lane * 4) = make_float4(va[u][0], va[u][1], va[u][2], va[u][3]);
+#pragma unroll
+                            for (int c = 0; c < COLS4; ++c)
+                                *reinterpret_cast<float4*>(dst + kBM + c * 128 + lane * 4) =
+                                    make_float4(vb[u][4 * c], vb[u][4 * c + 1], vb[u][4 * c + 2], vb[u][4 * c + 3]);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                *reinterpret_cast<float4*>(dst + h * kBM + lane * 4) = make_float4(
+                                    va[u][0] * vb[u][h], va[u][1] * vb[u][h], va[u][2] * vb[u][h], va[u][3] * vb[u][h]);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tfull[slots.at]);
+                        slots.advance();
+                        load(u, kb + u + kAhead);
+                    }
+                }
             }
         }
     }

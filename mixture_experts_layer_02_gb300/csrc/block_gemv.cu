@@ -28,13 +28,30 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBatch = 4;
+constexpr int kBatch = 3;
 
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four e4m3 codes as f16 (exact): the first two in lo, the others in hi.
+__device__ __forceinline__ void to_f16(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
+
+// c += the products of four K codes of weight rows g and g + 8 and of this lane's row of x
+__device__ __forceinline__ void mma_word(float (&c)[4], uint32_t wl, uint32_t wh, uint32_t xw) {
+    uint32_t a0, a1, a2, a3, b0, b1;
+    to_f16(wl, a0, a2);
+    to_f16(wh, a1, a3);
+    to_f16(xw, b0, b1);
+    mma_f16(c, a0, a1, a2, a3, b0, b1);
 }
 
 // Read once: not kept in L1.  Coherent, as the launch before may still be writing.
@@ -143,8 +160,10 @@ block_gemv_kernel(const uint8_t* x, const uint8_t* w, const BlockArgs a) {
                 float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    mma_e4m3(p, wl[b][j].x, wh[b][j].x, wl[b][j].y, wh[b][j].y, xv[b][j].x, xv[b][j].y);
-                    mma_e4m3(p, wl[b][j].z, wh[b][j].z, wl[b][j].w, wh[b][j].w, xv[b][j].z, xv[b][j].w);
+                    mma_word(p, wl[b][j].x, wh[b][j].x, xv[b][j].x);
+                    mma_word(p, wl[b][j].y, wh[b][j].y, xv[b][j].y);
+                    mma_word(p, wl[b][j].z, wh[b][j].z, xv[b][j].z);
+                    mma_word(p, wl[b][j].w, wh[b][j].w, xv[b][j].w);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[i] = fmaf(s[b][i & 1], p[i], acc[i]);  // rows g, g + 8; columns 2 t, 2 t + 1
