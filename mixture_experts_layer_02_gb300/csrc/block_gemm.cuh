@@ -24,8 +24,8 @@
 // scales to shared memory, 4..11 epilogue.
 // Registers are dealt out anew at the start: the epilogue's accumulators take 128.
 // Barriers: full[s] the bytes of a stage (of both CTAs, on the even one's), empty[s]
-// its MMAs are done, tfull[i] a slot and its scales are filled, tempty[i] (of the pair) and
-// sempty[i] (of a CTA) its readers are through.
+// its MMAs are done, tfull[i] a slot and its scales are filled, tempty[i] a slot and sempty[i]
+// its scales are read.
 // Every wait is bounded (1 s); none spans more than one step of 128 along K.
 #pragma once
 
@@ -313,7 +313,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
     uint64_t* empty = full + S;
     uint64_t* tfull = empty + S;
     uint64_t* tempty = tfull + C::SLOTS;
-    uint64_t* sempty = PAIR ? tempty + C::SLOTS : tempty;
+    uint64_t* sempty = tempty + C::SLOTS;
     uint64_t* drain = tempty + 2 * C::SLOTS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -339,7 +339,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(&tfull[i], 2);  // the MMAs' commit, the scales
             mbar_init(&tempty[i], C::CTAS * kEpiWarps);
-            if (PAIR) mbar_init(&sempty[i], kEpiWarps);
+            mbar_init(&sempty[i], kEpiWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -432,7 +432,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                     __syncwarp();
                     if (lane == 0) {
                         if constexpr (PAIR) slot_arrive(tempty_lead + 8u * slot);
-                        mbar_arrive(&sempty[slot]);
+                        else mbar_arrive(&tempty[slot]);
+                        if (KIND != BLOCK_WGRAD || rows <= 0) mbar_arrive(&sempty[slot]);
                     }
                 };
                 if (rows > 0) {
@@ -447,7 +448,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                         if constexpr (KIND == BLOCK_WGRAD) tmem_ld_frag(t_slot + (static_cast<uint32_t>(c * 16) << 16), r);
                         else tmem_ld_wide(t_slot + c * (C::COLS / 2), r);
                         tmem_landed(r);
-                        if (KIND != BLOCK_WGRAD && c == 1) release();  // all that this warp reads of the slot is in registers
+                        if (c == 1) release();  // all that this warp reads of the slot is in registers
 #pragma unroll
                         for (int j = 0; j < C::COLS / 4; ++j) {
                             float2 v = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
@@ -459,7 +460,10 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                             acc[c * (C::COLS / 4) + j] = fma2(v, make_float2(f, f), acc[c * (C::COLS / 4) + j]);
                         }
                     }
-                    if (KIND == BLOCK_WGRAD) release();  // the columns' scales were read to the end
+                    if constexpr (KIND == BLOCK_WGRAD) {  // the columns' scales are read to the end
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sempty[slot]);
+                    }
                 } else {
                     release();
                 }
