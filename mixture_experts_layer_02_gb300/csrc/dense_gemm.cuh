@@ -413,10 +413,26 @@ __device__ __forceinline__ void linear_chunk(const DenseArgs& a, const RowChunk&
     c.store(a.out0, z);
 }
 
-// A gradient's 32 rows x 64 columns: 128-byte lines of four rows a store.  `residual`
-// (or NULL) is added to the unrounded sums.
-__device__ __forceinline__ void plain_chunk(uint8_t* smem, uint32_t taddr, uint16_t* base, const uint16_t* residual,
-                                            long long row0, int col0, int M, int N, int lane) {
+// A gradient's 32 rows x 64 columns: 128-byte lines of four rows a store, and of the
+// residual (or NULL) a load.
+struct PlainChunk {
+    long long row0;
+    int col0, M, N, lane;
+
+    __device__ __forceinline__ long long row(int i) const { return row0 + i * 4 + (lane >> 3); }
+    __device__ __forceinline__ int col() const { return col0 + (lane & 7) * 8; }
+    __device__ __forceinline__ void fetch(const uint16_t* base, uint4 (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = row(i) < M && col() < N ? *octet(base, row(i), N, col()) : make_uint4(0, 0, 0, 0);
+    }
+};
+
+__device__ __forceinline__ uint4* plain_cell(uint8_t* smem, int row, int p) {
+    return reinterpret_cast<uint4*>(smem + row * 128 + ((p ^ (row & 7)) << 4));
+}
+
+// `add`: smem holds the residual's chunk, which is added to the unrounded sums.
+__device__ __forceinline__ void plain_chunk(uint8_t* smem, uint32_t taddr, uint16_t* base, const PlainChunk& at, bool add) {
     uint32_t r[64];
     {
         uint32_t(&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&r[0]);
@@ -425,17 +441,10 @@ __device__ __forceinline__ void plain_chunk(uint8_t* smem, uint32_t taddr, uint1
         tmem_ld_32x32(taddr + 32, hi);
         tmem_ld_wait();
     }
-    auto cell = [&](int row, int p) { return reinterpret_cast<uint4*>(smem + row * 128 + ((p ^ (row & 7)) << 4)); };
+    const int lane = at.lane;
+    auto cell = [&](int row, int p) { return plain_cell(smem, row, p); };
     auto two = [&](int j) { return pack_bf16x2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])); };
-    const int col = col0 + (lane & 7) * 8;
-    if (residual) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const long long row = row0 + i * 4 + (lane >> 3);
-            *cell(i * 4 + (lane >> 3), lane & 7) = row < M && col < N ? *octet(residual, row, N, col) : make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
+    if (add) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float f[8];
@@ -449,10 +458,8 @@ __device__ __forceinline__ void plain_chunk(uint8_t* smem, uint32_t taddr, uint1
     for (int i = 0; i < 8; ++i) *cell(lane, i) = make_uint4(two(8 * i), two(8 * i + 2), two(8 * i + 4), two(8 * i + 6));
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const long long row = row0 + i * 4 + (lane >> 3);
-        if (row < M && col < N) *octet(base, row, N, col) = *cell(i * 4 + (lane >> 3), lane & 7);
-    }
+    for (int i = 0; i < 8; ++i)
+        if (at.row(i) < at.M && at.col() < at.N) *octet(base, at.row(i), at.N, at.col()) = *cell(i * 4 + (lane >> 3), lane & 7);
 }
 
 // The epilogue of a whole accumulator of 128 rows x BN columns by eight warps:
@@ -467,21 +474,39 @@ struct WholeEpilogue {
     const DenseArgs& a;
     uint8_t* smem;  // this warp's kChunkBytes
     int m0, n0, q, half, lane;
-    uint4 ahead[4];
+    uint4 ahead[KIND == DENSE_DGRAD ? 8 : 4];
 
     __device__ __forceinline__ RowChunk chunk(int c) const {
         return RowChunk{smem, static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M, a.N, lane};
     }
+    __device__ __forceinline__ PlainChunk plain(int c) const {
+        return PlainChunk{static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M, a.N, lane};
+    }
     __device__ __forceinline__ void fetch_ahead() {
-        if (KIND == DENSE_LINEAR && a.residual) chunk(0).fetch(a.residual, ahead);
+        if constexpr (KIND == DENSE_LINEAR) {
+            if (a.residual) chunk(0).fetch(a.residual, ahead);
+        }
+        if constexpr (KIND == DENSE_DGRAD) {
+            if (a.residual) plain(0).fetch(a.residual, ahead);
+        }
     }
     __device__ __forceinline__ void run(int mat, uint32_t tmem, const uint8_t* res) {
         const uint32_t t = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * COLS);
         if constexpr (KIND == DENSE_DGRAD || KIND == DENSE_WGRAD) {
 #pragma unroll 1
-            for (int c = 0; c < COLS; c += 64)
-                plain_chunk(smem, t + c, mat ? a.out1 : a.out0, KIND == DENSE_DGRAD ? a.residual : nullptr,
-                            static_cast<long long>(m0) + q * 32, n0 + half * COLS + c, a.M, a.N, lane);
+            for (int c = 0; c < COLS; c += 64) {
+                const bool add = KIND == DENSE_DGRAD && a.residual;
+                if constexpr (KIND == DENSE_DGRAD) {
+                    if (add) {  // a chunk ahead in registers, the present one in shared memory
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) *plain_cell(smem, i * 4 + (lane >> 3), lane & 7) = ahead[i];
+                        __syncwarp();
+                        if (c + 64 < COLS) plain(c + 64).fetch(a.residual, ahead);
+                    }
+                }
+                plain_chunk(smem, t + c, mat ? a.out1 : a.out0, plain(c), add);
+            }
         } else {
 #pragma unroll 1
             for (int c = 0; c < COLS; c += 32) {

@@ -198,6 +198,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         // nothing to join: from TMEM through the epilogue, 32 x 32 at a time
         if (ok) {
             WholeEpilogue<KIND, kSplitBN> e{a, smem + warp * kChunkBytes, m0, n0, q, half, lane, {}};
+            if (KIND == DENSE_DGRAD) e.fetch_ahead();
             e.run(mat, tmem, RES > 0 && a.residual ? res : nullptr);
         }
         __syncwarp();

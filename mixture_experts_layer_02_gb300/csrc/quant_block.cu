@@ -30,36 +30,36 @@ int sms() {
 __device__ __forceinline__ float scale_of(int k) { return __uint_as_float(static_cast<uint32_t>(127 + k) << 23); }
 __device__ __forceinline__ float inverse_of(int k) { return __uint_as_float(static_cast<uint32_t>(127 - k) << 23); }
 
-// Sixteen lanes a block of 128 values; a warp has 2 U blocks in flight.
+// Sixteen lanes a block of 128 values, HPR such groups a row, each with U blocks of it in
+// flight; a thread block's 16 groups take 16 / HPR rows at a time.
+template <int HPR>
 __global__ void __launch_bounds__(kThreads)
 quant_rows_block_kernel(const uint16_t* src, long long rows, int cols, int nb, uint8_t* q, float* scale) {
-    constexpr int U = 4;
+    constexpr int U = 4, RPB = kThreads / 16 / HPR;
     pdl_wait();
-    const int sub = threadIdx.x & 15;
-    const long long total = rows * nb, step = static_cast<long long>(gridDim.x) * (kThreads / 16);
-    const long long first = static_cast<long long>(blockIdx.x) * (kThreads / 16) + (threadIdx.x >> 4);
-    // every lane of a warp takes the same number of turns (the shuffles are the whole warp's)
-    for (long long base = first; base - (first & 1) < total; base += U * step) {
-        uint4 v[U];
+    const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
+    for (long long r0 = static_cast<long long>(blockIdx.x) * RPB; r0 < rows; r0 += static_cast<long long>(gridDim.x) * RPB) {
+        const long long r = r0 + group / HPR;
+        const bool row = r < rows;
+        // every lane of a warp takes the same number of turns (the shuffles are the whole warp's)
+        for (int b0 = 0; b0 < nb; b0 += U * HPR) {
+            uint4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long i = base + u * step;
-            const long long r = i / nb;
-            const int col = static_cast<int>(i - r * nb) * kBlock + sub * 8;
-            v[u] = i < total && col < cols ? *reinterpret_cast<const uint4*>(src + r * cols + col) : make_uint4(0, 0, 0, 0);
-        }
+            for (int u = 0; u < U; ++u) {
+                const int col = (b0 + u * HPR + group % HPR) * kBlock + sub * 8;
+                v[u] = row && col < cols ? *reinterpret_cast<const uint4*>(src + r * cols + col) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const long long i = base + u * step;
-            uint32_t m = absmax8(v[u]);
+            for (int u = 0; u < U; ++u) {
+                uint32_t m = absmax8(v[u]);
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if (i >= total) continue;
-            const int k = scale_exp_of(m);
-            const long long r = i / nb;
-            const int col = static_cast<int>(i - r * nb) * kBlock + sub * 8;
-            if (sub == 0) scale[i] = scale_of(k);
-            if (col < cols) *reinterpret_cast<uint2*>(q + r * cols + col) = to_e4m3x8(v[u], inverse_of(k));
+                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const int b = b0 + u * HPR + group % HPR, col = b * kBlock + sub * 8;
+                if (!row || b >= nb) continue;
+                const int k = scale_exp_of(m);
+                if (sub == 0) scale[r * nb + b] = scale_of(k);
+                if (col < cols) *reinterpret_cast<uint2*>(q + r * cols + col) = to_e4m3x8(v[u], inverse_of(k));
+            }
         }
     }
     pdl_trigger();
@@ -105,58 +105,58 @@ quant_tiles_kernel(const uint16_t* src, long long tiles, int rows, int cols, int
 __device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7fff7fffu); }
 
 // A block takes 128 rows of one segment and every gridDim.y-th block of 128 columns.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 quant_segments_kernel(const QuantSegArgs a) {
-    __shared__ int s_warp[kThreads / 32];
-    __shared__ int s_place[3];                      // first row, rows, first padded row; rows < 0: nothing here
     __shared__ __align__(16) uint32_t s_col[2][8][kBlock / 2];  // maxima of column pairs, by warp
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < 3) s_place[threadIdx.x] = -1;
-    // which expert's rows start at padded block blockIdx.x: a running sum of the segments' blocks
-    int carry = 0;
+    // which expert's rows start at padded block blockIdx.x: every warp finds it for itself, by a
+    // running sum of the segments' blocks (barriers would cost more)
+    int carry = 0, first = -1, n = -1;  // first row, rows; n < 0: nothing here
     bool bad = false;
-    for (int e0 = 0; e0 < a.E; e0 += kThreads) {
-        const int e = e0 + static_cast<int>(threadIdx.x);
-        int lo = 0, n = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane;
+        int lo = 0, len = 0;
         if (e < a.E) {
             lo = a.offsets ? a.offsets[e] : 0;
             const int hi = a.offsets ? a.offsets[e + 1] : a.rows;
-            n = hi - lo;
-            if (lo < 0 || hi < lo || hi > a.rows || (e == 0 && lo != 0)) bad = true;
+            len = hi - lo;
+            bad |= lo < 0 || hi < lo || hi > a.rows || (e == 0 && lo != 0);
         }
-        if (__syncthreads_or(bad)) break;
-        int v = (n + kBlock - 1) / kBlock;
-        const int mine = v;
+        const int mine = len > 0 ? (len + kBlock - 1) / kBlock : 0;
+        int v = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, v, o);
             if (lane >= o) v += up;
         }
-        if (lane == 31) s_warp[warp] = v;
-        __syncthreads();
-        int before = carry;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += s_warp[w];
-            carry += s_warp[w];
+        const int b = static_cast<int>(blockIdx.x) - (carry + v - mine);
+        const unsigned here = __ballot_sync(0xffffffffu, b >= 0 && b < mine);
+        if (here) {
+            const int from = __ffs(here) - 1;
+            first = __shfl_sync(0xffffffffu, lo + b * kBlock, from);
+            n = __shfl_sync(0xffffffffu, min(kBlock, len - b * kBlock), from);
         }
-        const int start = before + v - mine, b = static_cast<int>(blockIdx.x) - start;
-        if (b >= 0 && b < mine) {
-            s_place[0] = lo + b * kBlock;
-            s_place[1] = min(kBlock, n - b * kBlock);
-            s_place[2] = static_cast<int>(blockIdx.x) * kBlock;
-        }
-        __syncthreads();
+        carry += __shfl_sync(0xffffffffu, v, 31);
     }
-    if (__syncthreads_or(bad)) {  // offsets that are not a prefix sum within the rows: nothing is written
+    if (__any_sync(0xffffffffu, bad)) {  // offsets that are not a prefix sum within the rows: nothing is written
         if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) record_error(a.err, MOE_DEVERR_BOUNDS);
         return;
     }
-    const int n = s_place[1];
     if (n < 0) return;  // behind the last segment
-    const long long row0 = s_place[0], pad0 = s_place[2];
+    const long long row0 = first, pad0 = static_cast<long long>(blockIdx.x) * kBlock;
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
     const int nb = (a.cols + kBlock - 1) / kBlock;
+    uint4 next[8];
+    auto fetch = [&](int cb) {  // rows y, y + 16, ... of an octet of columns
+        const int col = cb * kBlock + x * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = y + 16 * j;
+            next[j] = r < n && col < a.cols ? *reinterpret_cast<const uint4*>(a.src + (row0 + r) * a.cols + col) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    fetch(blockIdx.y);
     int turn = 0;
     for (int cb = blockIdx.y; cb < nb; cb += gridDim.y, turn ^= 1) {
         const int col = cb * kBlock + x * 8;
@@ -164,10 +164,8 @@ quant_segments_kernel(const QuantSegArgs a) {
         uint4 v[8];
         uint32_t c[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int r = y + 16 * j;
-            v[j] = r < n && inside ? *reinterpret_cast<const uint4*>(a.src + (row0 + r) * a.cols + col) : make_uint4(0, 0, 0, 0);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = next[j];
+        fetch(cb + gridDim.y);  // past the last column: nothing is read
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             c[0] = max_pair(c[0], v[j].x), c[1] = max_pair(c[1], v[j].y);
@@ -224,9 +222,14 @@ quant_segments_kernel(const QuantSegArgs a) {
 cudaError_t launch_quant_rows_block(const uint16_t* src, long long rows, int cols, uint8_t* q, float* scale,
                                     cudaStream_t st) {
     const int nb = static_cast<int>(blocks_of(cols));
-    const long long want = (rows * nb + kThreads / 16 - 1) / (kThreads / 16);
-    const int grid = static_cast<int>(std::min<long long>(want, static_cast<long long>(sms()) * 8));
-    return launch_kernel(quant_rows_block_kernel, dim3(grid), dim3(kThreads), 0, st, src, rows, cols, nb, q, scale);
+    auto go = [&](auto kernel, int hpr) {
+        const int rpb = kThreads / 16 / hpr;
+        const int grid = static_cast<int>(std::min<long long>((rows + rpb - 1) / rpb, static_cast<long long>(sms()) * 8));
+        return launch_kernel(kernel, dim3(grid), dim3(kThreads), 0, st, src, rows, cols, nb, q, scale);
+    };
+    if (nb <= 4) return go(quant_rows_block_kernel<1>, 1);
+    if (nb <= 16) return go(quant_rows_block_kernel<4>, 4);
+    return go(quant_rows_block_kernel<16>, 16);
 }
 
 cudaError_t launch_quant_tiles(const uint16_t* src, long long mats, int rows, int cols, uint8_t* q, float* scale,
@@ -240,7 +243,8 @@ cudaError_t launch_quant_tiles(const uint16_t* src, long long mats, int rows, in
 cudaError_t launch_quant_segments(const QuantSegArgs& a, cudaStream_t st) {
     const int blocks = static_cast<int>(segment_rows_of(a.rows, a.E) / kBlock);
     const int nb = static_cast<int>(blocks_of(a.cols));
-    const int slices = std::max(1, std::min(nb, sms() * 12 / std::max(1, blocks)));
+    // one wave: a block's way to its rows costs as much as a 128 x 128 piece of them
+    const int slices = std::max(1, std::min(nb, sms() * 2 / std::max(1, blocks)));
     return launch_kernel(quant_segments_kernel, dim3(blocks, slices), dim3(kThreads), 0, st, a);
 }
 

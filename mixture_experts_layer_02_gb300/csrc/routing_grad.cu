@@ -14,7 +14,6 @@
 // sizes.  Sums are fp32; dy and dx are rounded once.  Coherent loads only (no const
 // __restrict__): the launch before may still be writing them when blocks start.
 #include <algorithm>
-#include <atomic>
 
 #include "activation.cuh"
 #include "train.h"
@@ -146,7 +145,7 @@ permute_bwd_kernel(const uint16_t* dx_perm, const int32_t* inv, const uint16_t* 
     pdl_trigger();
 }
 
-// A block owns 16 tokens.  Their rows of dl are built in shared memory in fp32 (a
+// A block owns eight tokens, a warp each.  Their rows of dl are built in shared memory in fp32 (a
 // token may name an expert twice: its first lane adds up the others, in order),
 // leave as bf16 (an operand of tensor-core products) and are summed over the
 // tokens, unrounded and in order, for dbias.
@@ -157,8 +156,9 @@ route_bwd_kernel(const RouteBwdArgs a) {
     pdl_wait();
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    static_assert(kRouteBwdTokens == kWarps, "a warp a token");
     const int t0 = static_cast<int>(blockIdx.x) * kRouteBwdTokens, tokens = min(kRouteBwdTokens, a.N - t0);
-    for (int i = warp; i < tokens; i += kWarps) {
+    if (const int i = warp; i < tokens) {
         const long long t = t0 + i, at = t * a.K + lane;
         const bool on = lane < a.K;
         int id = on ? a.ids[at] : -1;
@@ -254,19 +254,9 @@ cudaError_t launch_permute_bwd(const uint16_t* dx_perm, const int32_t* inv, cons
 }
 
 cudaError_t launch_route_bwd(const RouteBwdArgs& a, cudaStream_t st) {
-    const size_t smem = static_cast<size_t>(kRouteBwdTokens) * a.ld * sizeof(float);  // at most 64 KB
-    static std::atomic<unsigned long long> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (!(done.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(route_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
-        if (e != cudaSuccess) return e;
-        done.fetch_or(bit, std::memory_order_acq_rel);
-    }
+    const size_t smem = static_cast<size_t>(kRouteBwdTokens) * a.ld * sizeof(float);  // at most 32 KB
     const long long parts = route_bwd_parts(a.N);
-    e = launch_kernel(route_bwd_kernel, dim3(static_cast<unsigned>(parts)), dim3(kThreads), smem, st, a);
+    const cudaError_t e = launch_kernel(route_bwd_kernel, dim3(static_cast<unsigned>(parts)), dim3(kThreads), smem, st, a);
     if (e != cudaSuccess || !a.dbias) return e;
     return launch_kernel(dbias_kernel, dim3((a.E + 31) / 32), dim3(1024), 0, st, a.partial, parts, a.E, a.dbias);
 }

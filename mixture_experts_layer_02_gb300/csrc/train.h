@@ -24,7 +24,7 @@ cudaError_t launch_permute_bwd(const uint16_t* dx_perm, const int32_t* inv, cons
 // Gradient of the selected logits, scattered into dl [N, ld] bf16 (ld = E rounded up to 8,
 // zero elsewhere) and, where dbias is set, summed over the tokens through `partial`
 // [route_bwd_parts(N)][E].
-constexpr int kRouteBwdTokens = 16;  // tokens a block
+constexpr int kRouteBwdTokens = 8;  // tokens a block: one a warp
 inline long long route_bwd_parts(int N) { return (static_cast<long long>(N) + kRouteBwdTokens - 1) / kRouteBwdTokens; }
 struct RouteBwdArgs {
     const float* dw;        // [N, K]

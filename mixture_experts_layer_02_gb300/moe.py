@@ -902,6 +902,7 @@ def moe_linear_backward(dy, x, w, z=None, fn: int = FN_NONE, need_dbias: bool = 
 # ---------------------------------------------------------------- training the routed layer
 _I32 = torch.int32
 BLOCK = 128  # values that share a scale, along each blocked dimension
+_current_device = torch._C._cuda_getDevice
 
 
 def _blocks(n):
@@ -912,12 +913,14 @@ def _ready(fn, ws, *specs):
     """Check (tensor or None, dtype, shape, name) of one call: contiguous CUDA tensors of one device, the current one."""
     dev = specs[0][0].get_device()
     for t, dtype, shape, name in specs:
-        if t is not None and not (_fits(t, dtype, shape) and t.get_device() == dev):
+        if t is not None and not (t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()):
             _need(t, dtype, shape, name)
             raise ValueError(f"{name}: on cuda:{t.get_device()}, {specs[0][3]} on cuda:{dev}")
-    if ws is not None and not (ws.is_cuda and ws.get_device() == dev and ws.dtype is _U8 and ws.is_contiguous()):
+    if dev < 0:
+        _need(*specs[0])
+    if ws is not None and not (ws.get_device() == dev and ws.dtype is _U8 and ws.is_contiguous()):
         raise ValueError(f"ws: must be a contiguous uint8 tensor on cuda:{dev}")
-    if dev != torch._C._cuda_getDevice():
+    if dev != _current_device():
         raise ValueError(f"{fn}: its tensors are on cuda:{dev}, not on the current device")
 
 
@@ -1006,16 +1009,20 @@ def moe_route_backward(dtopk_w, topk_ids, topk_w, logits, x, w_gate, mode: int, 
 def moe_quantize_e4m3_block(src, block_rows: int = 1, q=None, scale=None, stream=None):
     """e4m3 codes of a bf16 tensor [rows, cols] or [mats, rows, cols] with a scale for each 1 x 128 (block_rows=1) or
     128 x 128 (block_rows=128) of each matrix: (q uint8 of src's shape, scale fp32)."""
-    if src.dim() not in (2, 3):
-        raise ValueError(f"src: expected [rows, cols] or [mats, rows, cols], got {tuple(src.shape)}")
-    mats = src.shape[0] if src.dim() == 3 else 1
-    rows, cols = src.shape[-2:]
-    grid = (*src.shape[:-2], _blocks(rows) if block_rows == BLOCK else rows, _blocks(cols))
+    shape = src.shape
+    if len(shape) == 2:
+        (rows, cols), mats = shape, 1
+        grid = (_blocks(rows) if block_rows == BLOCK else rows, _blocks(cols))
+    elif len(shape) == 3:
+        mats, rows, cols = shape
+        grid = (mats, _blocks(rows) if block_rows == BLOCK else rows, _blocks(cols))
+    else:
+        raise ValueError(f"src: expected [rows, cols] or [mats, rows, cols], got {tuple(shape)}")
     if q is None:
-        q, = _new(stream, (src.shape, _U8, src.device))
+        q, = _new(stream, (shape, _U8, src.device))
     if scale is None:
         scale, = _new(stream, (grid, _F32, src.device))
-    _ready("moe_quantize_e4m3_block", None, (src, _BF16, src.shape, "src"), (q, _U8, src.shape, "q"), (scale, _F32, grid, "scale"))
+    _ready("moe_quantize_e4m3_block", None, (src, _BF16, shape, "src"), (q, _U8, shape, "q"), (scale, _F32, grid, "scale"))
     s = (_lib or load()).moe_quantize_e4m3_block(_addr(src), mats, rows, cols, block_rows, _addr(q), _addr(scale),
                                                  _stream_of(src, stream))
     if s:
