@@ -43,10 +43,7 @@ namespace {
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 12 * 32;
 constexpr int kBoxBytes = kBlock * kRowBytes;  // 128 rows of 128 bytes
-constexpr int kStageRoom = 192 * 1024;
-constexpr int kChunk = 2048;                   // an epilogue warp's staging: 32 rows of 64 bytes
 constexpr int kMaxE = 1024;
-constexpr int kScaleRoom = 4096;               // a step's scales, for every slot
 constexpr int kCopyRegs = 72, kEpiRegs = 216;  // registers a thread of warps 0..3 and 4..11
 
 template <int KIND, bool PAIR, int BN, int SPLITS>
@@ -57,21 +54,32 @@ struct BlockCfg {
     static constexpr int ROWS = CTAS * kBM;                    // rows of a tile
     static constexpr int B_BOXES = PAIR ? 1 : BN / kBlock;     // of this CTA
     static constexpr int STAGE = (1 + B_BOXES) * kBoxBytes;
-    static constexpr int STAGES = kStageRoom / STAGE;
     static constexpr int SLOTS = 512 / BN;                     // partial sums in TMEM
     static constexpr int COLS = BN / 2;                        // accumulator columns of an epilogue warp
+    // How the output leaves: in 64-byte pieces of eight rows, through 32 rows x 32 columns of
+    // shared memory a warp; or (the weight gradient of many rows, whose output is large and
+    // whose tiles are short) as bulk copies of 256 bytes under the next tile, for which all
+    // 32 rows x 128 columns wait in shared memory.  4093 rows x 4096 x 14336 by 8 experts, both
+    // gradients: 1080 us with bulk copies, 1128 without; pieces of 128 bytes or a stage less
+    // where the weights' stream is the limit cost more than they gain (229 for 162 us at 256
+    // tokens, 128 x 128 tiles; 782 for 718 us at 4096 x 7168 x 2048, 128 x 256).
+    static constexpr bool BULK = PAIR && KIND == BLOCK_WGRAD;
+    static constexpr int PITCH = BULK ? COLS * 2 + 16 : 64;    // bytes; BULK: eight rows' pieces on all banks
+    static constexpr int OUT = kEpiWarps * 32 * PITCH;
+    static constexpr int STAGES = BULK ? 4 : 192 * 1024 / STAGE;
     static constexpr int CLUSTER = CTAS * SPLITS;
     // a slot's scales: FWD and DGRAD one of each row for either half of the columns, WGRAD
     // one of each row, then one of each column
     static constexpr int SCALES = A_MN ? kBM + BN : 2 * kBM;
-    static_assert(SLOTS * SCALES * 4 <= kScaleRoom, "scale room");
+    static constexpr size_t smem(int E) {
+        return 1024 + STAGES * STAGE + OUT + SLOTS * SCALES * 4 + 48 * sizeof(uint64_t) + (2 * static_cast<size_t>(E) + 2) * sizeof(int) +
+               (KIND == BLOCK_WGRAD ? E * sizeof(uint16_t) : 0);
+    }
+    static_assert(smem(kMaxE) <= 227 * 1024, "shared memory");
+    static_assert(SPLITS == 1 || STAGES * STAGE >= kBM * 128 * 4, "the parked accumulator reuses the stages");
     static_assert(!PAIR || (BN == 256 && SPLITS == 1), "pairs own whole 256 x 256 tiles");
     static_assert(SPLITS == 1 || BN == 128, "parts of K are joined on 128 x 128 tiles");
 };
-
-constexpr size_t block_smem(int E) {
-    return 1024 + kStageRoom + kEpiWarps * kChunk + kScaleRoom + 48 * sizeof(uint64_t) + (3 * static_cast<size_t>(E) + 2) * sizeof(int);
-}
 
 __device__ __forceinline__ void load_box(const CUtensorMap* map, uint64_t* bar, void* dst, int x, int y, int z) {
     asm volatile(
@@ -166,41 +174,49 @@ struct BlockTile {
     int e, row0, rows, n0, k0, kbs;
 };
 
+// Tiles are numbered expert by expert, inside an expert in bands of kPairBand row tiles,
+// inside a band column by column, the band's row tiles innermost: what runs at a time
+// shares weight columns and rows in L2.
 struct TileList {
-    const int *goff, *pre, *ord;  // segments; FWD, DGRAD: row tiles before list position i; WGRAD: blocks before expert e
+    const int *goff, *pre;  // segments; FWD, DGRAD: row tiles before an expert; WGRAD: 128-row blocks before it
+    const uint16_t* ord;    // WGRAD: the experts' order
     int E, nt, mt, kbs, tile_rows, bn, M;
 
     template <int KIND>
     __device__ __forceinline__ BlockTile at(int t) const {
         BlockTile b;
-        if (KIND == BLOCK_WGRAD) {
-            const int per = mt * nt, i = t / per, local = t - i * per;
-            const int full = mt / kPairBand * kPairBand;
-            int m, n;
-            if (local < full * nt) {
-                const int band = local / (kPairBand * nt), in = local - band * kPairBand * nt;
-                n = in / kPairBand;
-                m = band * kPairBand + in - n * kPairBand;
-            } else {
-                const int in = local - full * nt, ms = mt - full;
-                n = in / ms;
-                m = full + in - n * ms;
-            }
+        int rows = M, first = 0, tiles = mt;  // of this expert's output
+        if constexpr (KIND == BLOCK_WGRAD) {
+            const int i = t / (mt * nt);
+            t -= i * mt * nt;
             b.e = ord[i];
-            b.row0 = m * tile_rows;
-            b.rows = min(tile_rows, M - b.row0);
-            b.n0 = n * bn;
             b.k0 = pre[b.e];
             b.kbs = (goff[b.e + 1] - goff[b.e] + kBlock - 1) / kBlock;
         } else {
-            const TileInfo ti = decode_tile_banded(t, E, nt, pre, ord, goff, tile_rows);
-            b = {ti.g, ti.row0, ti.rows, ti.n_tile * bn, 0, kbs};
+            int lo = 0, hi = E - 1;
+            while (lo < hi) {  // the last expert with pre * nt <= t
+                const int mid = (lo + hi + 1) >> 1;
+                if (pre[mid] * nt <= t) lo = mid; else hi = mid - 1;
+            }
+            t -= pre[lo] * nt;
+            tiles = pre[lo + 1] - pre[lo];
+            first = goff[lo];
+            rows = goff[lo + 1] - first;
+            b.e = lo;
+            b.k0 = 0;
+            b.kbs = kbs;
         }
+        const int band = t / (kPairBand * nt), in = t - band * kPairBand * nt;
+        const int high = min(kPairBand, tiles - band * kPairBand), n = in / high;
+        const int m = band * kPairBand + in - n * high;
+        b.row0 = first + m * tile_rows;
+        b.rows = min(tile_rows, rows - m * tile_rows);
+        b.n0 = n * bn;
         return b;
     }
 };
 
-// 32 lanes x 64 consecutive fp32 columns, a row a thread; and 32 of them.
+// 32 lanes x 64 (or 32) consecutive fp32 columns, a row a thread.
 __device__ __forceinline__ void tmem_ld_wide(uint32_t taddr, uint32_t (&r)[64]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
@@ -231,27 +247,10 @@ __device__ __forceinline__ void tmem_ld_wide(uint32_t taddr, uint32_t (&r)[32]) 
         : "r"(taddr));
 }
 
-// 16 lanes x 128 consecutive fp32 columns in the layout of an MMA's accumulator: thread T
-// gets columns 8 j + 2 (T % 4) and the next of rows T / 4 (r[4 j], r[4 j + 1]) and T / 4 + 8
-// (r[4 j + 2], r[4 j + 3]); and 64 of them.
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[64]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x16.b32 {"
-        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63"
-        "}, [%64];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
-          "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
-          "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
-          "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
-          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 lanes x 64 (or 32) consecutive fp32 columns in the layout of an MMA's accumulator:
+// thread T gets columns 8 j + 2 (T % 4) and the next of rows T / 4 (r[4 j], r[4 j + 1]) and
+// T / 4 + 8 (r[4 j + 2], r[4 j + 3]).
+__device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, uint32_t* r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
         "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31"
@@ -264,6 +263,16 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&r)[32]) 
         : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15"
+        "}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
 // Four 8 x 8 blocks of 16-bit values, in the same layout, to rows of 16 bytes: thread T
 // has the address of row T % 8 of block T / 8.
 __device__ __forceinline__ void st_blocks(void* row, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -271,22 +280,29 @@ __device__ __forceinline__ void st_blocks(void* row, uint32_t a, uint32_t b, uin
                  : "memory");
 }
 
-// 32 rows x 32 columns of a warp leave as 64-byte pieces of eight rows: stored as they
-// lie, one row a thread, a 16-byte store would touch 32 rows at once.
+// A cell of 16 bytes of a warp's 32 rows x 32 columns, permuted so that both directions use all banks.
 __device__ __forceinline__ uint4* chunk_cell(uint8_t* smem, int r, int piece) {
     return reinterpret_cast<uint4*>(smem + r * 64 + ((piece ^ ((r >> 1) & 3)) << 4));
 }
 
+// Stored as they lie, one row a thread, a 16-byte store would touch 32 rows at once.
 __device__ __forceinline__ void store_chunk(uint8_t* smem, uint16_t* out, long long row0, int rows, int col0, int N, int lane) {
-    __syncwarp();
     const int col = col0 + (lane & 3) * 8;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + (lane >> 2);
         if (r < rows && col < N) *reinterpret_cast<uint4*>(out + (row0 + r) * N + col) = *chunk_cell(smem, r, lane & 3);
     }
-    __syncwarp();
 }
+
+// A row of `bytes` (a multiple of 16) from shared to global memory, in the background.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// This thread's copies have read shared memory; or have ended.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // The accumulator of one k-part, parked in shared memory: 128 rows of 128 fp32, the
 // 16-byte quads of a row permuted by its number.
@@ -307,9 +323,9 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
     constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);  // the same offset in every CTA of a cluster
-    uint8_t* chunks = smem + kStageRoom;
-    float* scales = reinterpret_cast<float*>(chunks + kEpiWarps * kChunk);
-    uint64_t* full = reinterpret_cast<uint64_t*>(chunks + kEpiWarps * kChunk + kScaleRoom);
+    uint8_t* outs = smem + S * C::STAGE;
+    float* scales = reinterpret_cast<float*>(outs + C::OUT);
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + C::SLOTS * C::SCALES);
     uint64_t* empty = full + S;
     uint64_t* tfull = empty + S;
     uint64_t* tempty = tfull + C::SLOTS;
@@ -319,7 +335,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* s_goff = reinterpret_cast<int*>(full + 48);  // [E + 1]
     int* s_pre = s_goff + args.E + 1;                 // [E + 1]
-    int* s_ord = s_pre + args.E + 1;                  // [E]
+    uint16_t* s_ord = reinterpret_cast<uint16_t*>(s_pre + args.E + 1);  // [E], WGRAD: the experts, most rows first
     static_assert(2 * S + 3 * C::SLOTS + 1 + 1 <= 48, "barrier room");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -362,17 +378,27 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
     bad = __syncthreads_or(bad);
     if (bad && blockIdx.x == 0 && threadIdx.x == 0) record_error(err, MOE_DEVERR_BOUNDS);
     // tiles of FWD and DGRAD cost the same; WGRAD's go by their expert's rows, the longest first
-    if constexpr (KIND == BLOCK_WGRAD) heaviest_first(s_goff, E, s_ord);
-    else
-        for (int i = threadIdx.x; i < E; i += kThreads) s_ord[i] = i;
+    // (above kSortMaxGroups experts in the experts' order)
+    if constexpr (KIND == BLOCK_WGRAD)
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+            int at = e;
+            if (E <= kSortMaxGroups) {
+                const int mine = s_goff[e + 1] - s_goff[e];
+                at = 0;
+                for (int o = 0; o < E; ++o) {
+                    const int other = s_goff[o + 1] - s_goff[o];
+                    at += (other > mine) | ((other == mine) & (o < e));
+                }
+            }
+            s_ord[at] = static_cast<uint16_t>(e);
+        }
     __syncthreads();
-    if (warp == 0) {  // exclusive prefix of row tiles in list order, or of the padded rows' blocks by expert
+    if (warp == 0) {  // exclusive prefix of the experts' row tiles, or of their padded rows' blocks
         constexpr int UNIT = KIND == BLOCK_WGRAD ? kBlock : C::ROWS;
         int carry = 0;
         for (int base = 0; base < E; base += 32) {
             const int i = base + lane;
-            const int g = i < E ? (KIND == BLOCK_WGRAD ? i : s_ord[i]) : 0;
-            int v = i < E ? (s_goff[g + 1] - s_goff[g] + UNIT - 1) / UNIT : 0;
+            int v = i < E ? (s_goff[i + 1] - s_goff[i] + UNIT - 1) / UNIT : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(0xffffffffu, v, o);
@@ -402,7 +428,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // epilogue warp (q, half): TMEM lanes 32 q .., columns half * COLS ..
         const int q = warp & 3, half = (warp - 4) >> 2;
-        uint8_t* chunk = chunks + (warp - 4) * kChunk;
+        uint8_t* out_rows = outs + (warp - 4) * 32 * C::PITCH;
         const uint32_t tempty_lead = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
         const uint32_t t_warp = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(half * C::COLS);
         const int in_tile = (PAIR ? static_cast<int>(rank) * kBM : 0) + q * 32;  // this warp's first row of the tile
@@ -440,24 +466,39 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                     float s[ROWS];
 #pragma unroll
                     for (int i = 0; i < ROWS; ++i) s[i] = my_scales[slot * C::SCALES + 8 * i];
-                    // half of the columns at a time (WGRAD: half of the rows)
                     const uint32_t t_slot = t_warp + static_cast<uint32_t>(slot * BN);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t r[C::COLS / 2];
-                        if constexpr (KIND == BLOCK_WGRAD) tmem_ld_frag(t_slot + (static_cast<uint32_t>(c * 16) << 16), r);
-                        else tmem_ld_wide(t_slot + c * (C::COLS / 2), r);
+                    for (int c = 0; c < 2; ++c) {  // half of the columns at a time
+                        constexpr int W = C::COLS / 2;
+                        uint32_t r[W];
+                        if constexpr (KIND == BLOCK_WGRAD) {  // first rows 0..15, then 16..31
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t at = t_slot + c * W + (static_cast<uint32_t>(h * 16) << 16);
+                                if constexpr (W == 64) tmem_ld_frag64(at, r + h * 32);
+                                else tmem_ld_frag32(at, r + h * 16);
+                            }
+                        } else {
+                            tmem_ld_wide(t_slot + c * W, r);
+                        }
                         tmem_landed(r);
                         if (c == 1) release();  // all that this warp reads of the slot is in registers
+                        if constexpr (KIND == BLOCK_WGRAD) {
 #pragma unroll
-                        for (int j = 0; j < C::COLS / 4; ++j) {
-                            float2 v = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
-                            float f = s[0];
-                            if constexpr (KIND == BLOCK_WGRAD) {
-                                v = mul2(v, *reinterpret_cast<const float2*>(my_columns + slot * C::SCALES + (j >> 1) * 8));
-                                f = s[c * 2 + (j & 1)];
+                            for (int j = 0; j < W / 8; ++j) {
+                                const float2 col = *reinterpret_cast<const float2*>(my_columns + slot * C::SCALES + c * W + j * 8);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {  // rows lane / 4 + 8 i
+                                    const int at = (i >> 1) * (W / 2) + j * 4 + (i & 1) * 2;
+                                    const float2 v = mul2(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), col);
+                                    acc[c * (W / 2) + at / 2] = fma2(v, make_float2(s[i], s[i]), acc[c * (W / 2) + at / 2]);
+                                }
                             }
-                            acc[c * (C::COLS / 4) + j] = fma2(v, make_float2(f, f), acc[c * (C::COLS / 4) + j]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < W / 2; ++j)
+                                acc[c * (W / 2) + j] = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])),
+                                                            make_float2(s[0], s[0]), acc[c * (W / 2) + j]);
                         }
                     }
                     if constexpr (KIND == BLOCK_WGRAD) {  // the columns' scales are read to the end
@@ -472,36 +513,52 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
             if (!ok) break;
             const int col0 = b.n0 + half * C::COLS;
             if constexpr (SPLITS == 1) {
-                uint16_t* out = args.out + (KIND == BLOCK_WGRAD ? static_cast<long long>(b.e) * args.M * args.N : 0);
-                const long long row0 = static_cast<long long>(b.row0) + in_tile;
-                if (rows > 0)
+                if (rows > 0) {
+                    uint16_t* out = args.out + (KIND == BLOCK_WGRAD ? static_cast<long long>(b.e) * args.M * args.N : 0LL);
+                    const long long row0 = static_cast<long long>(b.row0) + in_tile;
+                    if constexpr (C::BULK) bulk_wait_read();  // the last tile's
+                    __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < C::COLS / 32; ++c) {
+                    for (int p = 0; p < C::COLS / 8; ++p) {  // eight columns
+                        auto cell = [&](int r) {
+                            return C::BULK ? reinterpret_cast<uint4*>(out_rows + r * C::PITCH + p * 16) : chunk_cell(out_rows, r, p & 3);
+                        };
                         if constexpr (KIND == BLOCK_WGRAD) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {  // eight columns of four times eight rows
-                                auto two = [&](int i) {
-                                    const float2 v = acc[(i >> 1) * (C::COLS / 4) + (c * 4 + j) * 2 + (i & 1)];
-                                    return pack_bf16x2(v.x, v.y);
-                                };
-                                st_blocks(chunk_cell(chunk, lane, j), two(0), two(1), two(2), two(3));
-                            }
+                            constexpr int W = C::COLS / 2;
+                            auto two = [&](int i) {
+                                const float2 v = acc[p / (W / 8) * (W / 2) + (i >> 1) * (W / 4) + p % (W / 8) * 2 + (i & 1)];
+                                return pack_bf16x2(v.x, v.y);
+                            };
+                            st_blocks(cell(lane), two(0), two(1), two(2), two(3));
                         } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2* v = &acc[c * 16 + i * 4];
-                                *chunk_cell(chunk, lane, i) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
-                                                                         pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+                            const float2* v = &acc[p * 4];
+                            *cell(lane) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                                                     pack_bf16x2(v[3].x, v[3].y));
+                        }
+                        if constexpr (!C::BULK) {
+                            if ((p & 3) == 3) {
+                                __syncwarp();
+                                store_chunk(out_rows, out, row0, rows, col0 + (p - 3) * 8, args.N, lane);
+                                __syncwarp();
                             }
                         }
-                        store_chunk(chunk, out, row0, rows, col0 + c * 32, args.N, lane);
                     }
+                    if constexpr (C::BULK) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        const int cols = min(C::COLS, args.N - col0);
+                        if (lane < rows && cols > 0)
+                            bulk_store(out + (row0 + lane) * args.N + col0, out_rows + lane * C::PITCH, static_cast<uint32_t>(cols) * 2);
+                        bulk_commit();
+                    }
+                }
             } else if constexpr (KIND == BLOCK_WGRAD) {  // the stages are free: every copy of this CTA's part was waited for
 #pragma unroll
                 for (int i = 0; i < C::COLS / 2; ++i) {
-                    // acc[i]: 16 rows of i / (COLS / 4), columns 8 (i / 2) + 2 (lane % 4), rows lane / 4 + 8 (i % 2)
-                    const int j = i % (C::COLS / 4), r = (lane >> 2) + 8 * (j & 1) + 16 * (i / (C::COLS / 4));
-                    const int col = half * C::COLS + (j >> 1) * 8 + (lane & 3) * 2;
+                    // acc[i]: COLS / 2 columns, of them 16 rows at a time, then pairs of columns of rows lane / 4 and 8 further
+                    constexpr int W = C::COLS / 2;
+                    const int c = i / (W / 2), h = i / (W / 4) % 2, j = i % (W / 4);
+                    const int r = (lane >> 2) + 8 * (j & 1) + 16 * h, col = half * C::COLS + c * W + (j >> 1) * 8 + (lane & 3) * 2;
                     if (r < rows) *reinterpret_cast<float2*>(smem + park_quad(in_tile + r, col >> 2) + (col & 2) * 4) = acc[i];
                 }
             } else if (lane < rows) {
@@ -511,6 +568,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                         make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
             }
         }
+        if constexpr (C::BULK) bulk_wait();  // shared memory is given back, and the rows are written
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
         if (warp == 0 || warp == 2) {  // copies: warp 0 A (it announces the stage's bytes), warp 2 B
@@ -723,7 +781,7 @@ cudaLaunchConfig_t block_config(int E, long long clusters, cudaLaunchAttribute (
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * C::CLUSTER));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = block_smem(E);
+    cfg.dynamicSmemBytes = C::smem(E);
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim = {static_cast<unsigned>(C::CLUSTER), 1, 1};
@@ -744,7 +802,7 @@ cudaError_t block_prepare(int* clusters) {
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(done.load(std::memory_order_acquire) & bit)) {
         auto kern = block_gemm_kernel<KIND, PAIR, BN, SPLITS>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(block_smem(kMaxE)));
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(BlockCfg<KIND, PAIR, BN, SPLITS>::smem(kMaxE)));
         if (e != cudaSuccess) return e;
         cudaFuncAttributes fa = {};  // the shares that setmaxnreg deals out must fit what the launch gets
         e = cudaFuncGetAttributes(&fa, kern);
