@@ -496,7 +496,9 @@ moe_status moe_linear_backward(const moe_bf16* dy, const moe_bf16* x, const moe_
  * passage to cite: the formulas below are the definitions.  Sums are fp32 and in
  * a fixed order (the same call gives the same bits); outputs overlap no input
  * except where said.  Gradient entry points compute each output whose pointer is
- * not NULL; of no rows, weight gradients are zero. */
+ * not NULL; of no rows, weight gradients are zero.  Widths are at most 2^30 where
+ * they count e4m3 codes.  moe_route_backward keeps intermediates in its workspace:
+ * calls (or replayed graphs) that may run at the same time need one each. */
 
 /* Gradient of moe_combine (and of moe_combine_padded, inv_perm being its slot):
  *   dy_perm[inv_perm[t,k], :] = topk_w[t,k] * dout[t, :]

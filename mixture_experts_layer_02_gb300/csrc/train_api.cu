@@ -43,7 +43,7 @@ moe_status check_route(int N, int D, int E, int K) {
 // rows of codes whose width is a multiple of 16 bytes
 moe_status check_codes(const char* name, int width) {
     if (width < 16 || width % 16) return refuse(MOE_ERR_INVALID_ARG, "%s=%d not a positive multiple of 16", name, width);
-    if (width > kRowsLimit) return refuse(MOE_ERR_INVALID_ARG, "%s=%d too large", name, width);
+    if (width > (1 << 30)) return refuse(MOE_ERR_INVALID_ARG, "%s=%d above %d", name, width, 1 << 30);  // column numbers past the end stay in 32 bits
     return MOE_OK;
 }
 
