@@ -28,7 +28,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBatch = 3;
+constexpr int kBatch = 2;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -155,19 +155,22 @@ block_gemv_kernel(const uint8_t* x, const uint8_t* w, const BlockArgs a) {
                     s[b][j] = on ? scale * a.a_scale[static_cast<long long>(index[j]) * kbs + kb + b] : 0.0f;
                 }
             }
+            float p[kBatch][4] = {};  // the blocks' MMAs in turn: a block's eight wait for one another
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    mma_word(p, wl[b][j].x, wh[b][j].x, xv[b][j].x);
-                    mma_word(p, wl[b][j].y, wh[b][j].y, xv[b][j].y);
-                    mma_word(p, wl[b][j].z, wh[b][j].z, xv[b][j].z);
-                    mma_word(p, wl[b][j].w, wh[b][j].w, xv[b][j].w);
-                }
+                for (int b = 0; b < kBatch; ++b) mma_word(p[b], wl[b][j].x, wh[b][j].x, xv[b][j].x);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] = fmaf(s[b][i & 1], p[i], acc[i]);  // rows g, g + 8; columns 2 t, 2 t + 1
+                for (int b = 0; b < kBatch; ++b) mma_word(p[b], wl[b][j].y, wh[b][j].y, xv[b][j].y);
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) mma_word(p[b], wl[b][j].z, wh[b][j].z, xv[b][j].z);
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) mma_word(p[b], wl[b][j].w, wh[b][j].w, xv[b][j].w);
             }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i] = fmaf(s[b][i & 1], p[b][i], acc[i]);  // rows g, g + 8; columns 2 t, 2 t + 1
         }
         if (part == 0 && g == 0)
 #pragma unroll

@@ -101,9 +101,6 @@ quant_tiles_kernel(const uint16_t* src, long long tiles, int rows, int cols, int
     pdl_trigger();
 }
 
-// magnitudes of two bf16, larger of each
-__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7fff7fffu); }
-
 // A block takes 128 rows of one segment and every gridDim.y-th block of 128 columns.
 __global__ void __launch_bounds__(kThreads, 2)
 quant_segments_kernel(const QuantSegArgs a) {
@@ -166,21 +163,31 @@ quant_segments_kernel(const QuantSegArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = next[j];
         fetch(cb + gridDim.y);  // past the last column: nothing is read
+        // magnitudes, two to a register: the columns' maxima, and two rows' at a time
+        uint32_t rowmax[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            c[0] = max_pair(c[0], v[j].x), c[1] = max_pair(c[1], v[j].y);
-            c[2] = max_pair(c[2], v[j].z), c[3] = max_pair(c[3], v[j].w);
+        for (int j = 0; j < 8; j += 2) {
+            uint32_t pm[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t m[4] = {v[j + i].x & 0x7fff7fffu, v[j + i].y & 0x7fff7fffu, v[j + i].z & 0x7fff7fffu, v[j + i].w & 0x7fff7fffu};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) c[w] = __vmaxu2(c[w], m[w]);
+                pm[i] = __vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3]));
+            }
+            rowmax[j / 2] = __vmaxu2(__byte_perm(pm[0], pm[1], 0x5410), __byte_perm(pm[0], pm[1], 0x7632));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = max_pair(c[i], __shfl_xor_sync(0xffffffffu, c[i], 16));
+        for (int i = 0; i < 4; ++i) c[i] = __vmaxu2(c[i], __shfl_xor_sync(0xffffffffu, c[i], 16));
         if (lane < 16) *reinterpret_cast<uint4*>(&s_col[turn][warp][lane * 4]) = make_uint4(c[0], c[1], c[2], c[3]);
         if (a.q) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = absmax8(v[j]);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const int r = y + 16 * j, k = scale_exp_of(m);
+                for (int o = 8; o > 0; o >>= 1) rowmax[i] = __vmaxu2(rowmax[i], __shfl_xor_sync(0xffffffffu, rowmax[i], o));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = y + 16 * j, k = scale_exp_of((rowmax[j / 2] >> (16 * (j & 1))) & 0xffffu);
                 if (r >= n) continue;
                 if (x == 0) a.scale[(row0 + r) * nb + cb] = scale_of(k);
                 if (inside) *reinterpret_cast<uint2*>(a.q + (row0 + r) * a.cols + col) = to_e4m3x8(v[j], inverse_of(k));
@@ -190,7 +197,7 @@ quant_segments_kernel(const QuantSegArgs a) {
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
             const uint4 m = *reinterpret_cast<const uint4*>(&s_col[turn][w][x * 4]);
-            c[0] = max_pair(c[0], m.x), c[1] = max_pair(c[1], m.y), c[2] = max_pair(c[2], m.z), c[3] = max_pair(c[3], m.w);
+            c[0] = __vmaxu2(c[0], m.x), c[1] = __vmaxu2(c[1], m.y), c[2] = __vmaxu2(c[2], m.z), c[3] = __vmaxu2(c[3], m.w);
         }
         if (!inside) continue;
         float s[8], back[8];
