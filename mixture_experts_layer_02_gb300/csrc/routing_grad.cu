@@ -11,7 +11,11 @@
 // The first two move rows and are bound by HBM.  Both go by assignments, so dout is
 // read through L1/L2 by the K warps of a token that run side by side, each row of y
 // once, and nothing is summed through atomics: the order of additions is fixed by the
-// sizes.  Sums are fp32; dy and dx are rounded once.  Coherent loads only (no const
+// sizes.  Measured: combine 4096 x 7168, K = 8, 154 us (999 MB, 6.5 TB/s: 96 % of what a
+// copy reaches); permute 4093 x 4096, K = 2, with residual 22.6 us (134 MB, 5.9 TB/s).  The
+// router's gradient is two products of dl (256 experts: 15 GFLOP each): as sparse sums they
+// would gather 470 MB of W_gate's rows through L2.  4096 x 7168 x 256: 58 us, of which dl 5,
+// dx 33 and dW_gate 21.  Sums are fp32; dy and dx are rounded once.  Coherent loads only (no const
 // __restrict__): the launch before may still be writing them when blocks start.
 #include <algorithm>
 

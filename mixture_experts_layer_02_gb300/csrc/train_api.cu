@@ -103,6 +103,24 @@ long long row_tiles(const BlockArgs& a, int height) {
     return some + (a.rows - some) / height;
 }
 
+// The choice of kernel, from sizes that the host knows; times are microseconds on GB300.
+//   stream      up to 8 rows, or up to 128 and one an expert on average: 7168 x 2048 and
+//               one row 8, as tiles 11 to 24; 2048 x 768, 128 experts and 64 rows 21, tiles
+//               25 to 27.  An expert's rows are taken in turns of eight, each of which reads
+//               its weights again: tiles win from 16 rows an expert on (7168 x 2048 14
+//               against 12), and 128 rows bound the turns of a batch that all goes to one.
+//   pairs       where an expert fills most of a 256-row tile: 4096 x 4096 x 14336 by 8
+//               experts (1024 rows each) 418, one-CTA tiles 450; at 128 rows each 112 and
+//               117, but 4096 x 7168 x 2048 by 256 experts (128 rows on average, ragged)
+//               817 and 728.  The weight gradient's tiles are all whole and its K is the
+//               rows: pairs from 512 rows an expert on (both gradients 4096^2 by 8 experts:
+//               512 rows 222 and 219, 1024 rows 334 and 353, 64 rows 117 and 100).
+//   128 x 256   else, where its tiles fill most of the GPU: 2048 x 768, 128 experts, 16384
+//               rows 61 against 65 for 128 x 128.
+//   128 x 128   else, with K in up to four parts while its tiles leave SMs idle: 7168 x 2048
+//               and 64 rows 16 in four parts, 20 in two, 28 whole.  The
+//               weight gradient's K is an expert's rows, too short for parts to pay but with
+//               one expert: 1024^2 by 4000 rows 31 whole and in two parts.
 // MOE_BLOCK_KERNEL = 1 (128 x 128), 2 (128 x 256), 3 (pairs) or 4 (stream, FWD only), and
 // MOE_BLOCK_SPLIT = parts of K (1) or warps a row (4), force a choice, for tuning and test
 // coverage.
@@ -113,9 +131,14 @@ BlockPlan plan_block(BlockKind kind, const BlockArgs& a) {
     };
     int kernel = env_int("MOE_BLOCK_KERNEL", 0);
     const int fixed = kernel ? env_int("MOE_BLOCK_SPLIT", 1) : 0;
-    const long long mean = kind == BLOCK_WGRAD ? a.M : a.rows / a.E;
     if (kernel == 4 && kind != BLOCK_FWD) kernel = 1;
-    if (kernel == 0) kernel = kind == BLOCK_FWD && (a.rows <= 8 || mean <= 1) ? 4 : (mean >= 160 && tiles(2 * kBM, 256) >= 38 ? 3 : (tiles(kBM, 256) >= 120 ? 2 : 1));
+    if (kernel == 0) {
+        const int mean = a.rows / a.E;
+        const bool high = kind == BLOCK_WGRAD ? a.M >= 160 && mean >= 512 : mean >= 160;
+        if (kind == BLOCK_FWD && (a.rows <= 8 || (mean <= 1 && a.rows <= 128))) kernel = 4;
+        else if (high && tiles(2 * kBM, 256) >= 38) kernel = 3;
+        else kernel = tiles(kBM, 256) >= 120 ? 2 : 1;
+    }
     if (kernel == 4) {
         int warps = fixed;
         if (!warps) {  // enough warps for the GPU, each with a few blocks
@@ -128,7 +151,7 @@ BlockPlan plan_block(BlockKind kind, const BlockArgs& a) {
     if (kernel == 3) return {0, true, 256, 1, tiles(2 * kBM, 256)};
     if (kernel == 2) return {0, false, 256, 1, tiles(kBM, 256)};
     int splits = fixed;
-    const long long n = tiles(kBM, 128), kbs = kind == BLOCK_WGRAD ? blocks_of(a.rows) : blocks_of(a.K);
+    const long long n = tiles(kBM, 128), kbs = kind == BLOCK_WGRAD ? blocks_of(a.rows / a.E) : blocks_of(a.K);
     if (!splits) {
         splits = 1;
         while (splits < 4 && n * splits * 2 <= 152 && kbs >= 4 * splits) splits *= 2;
