@@ -130,7 +130,8 @@ BlockPlan plan_block(BlockKind kind, const BlockArgs& a) {
         return kind == BLOCK_WGRAD ? a.E * ((a.M + height - 1) / static_cast<long long>(height)) * n : row_tiles(a, height) * n;
     };
     int kernel = env_int("MOE_BLOCK_KERNEL", 0);
-    const int fixed = kernel ? env_int("MOE_BLOCK_SPLIT", 1) : 0;
+    const bool kernel_set = kernel != 0;
+    const int fixed = kernel_set ? env_int("MOE_BLOCK_SPLIT", 1) : 0;
     if (kernel == 4 && kind != BLOCK_FWD) kernel = 1;
     if (kernel == 0) {
         const int mean = a.rows / a.E;
@@ -150,7 +151,7 @@ BlockPlan plan_block(BlockKind kind, const BlockArgs& a) {
     }
     if (kernel == 3) return {0, true, 256, 1, tiles(2 * kBM, 256)};
     if (kernel == 2) return {0, false, 256, 1, tiles(kBM, 256)};
-    int splits = fixed;
+    int splits = kernel_set && fixed != 2 && fixed != 4 ? 1 : fixed;
     const long long n = tiles(kBM, 128), kbs = kind == BLOCK_WGRAD ? blocks_of(a.rows / a.E) : blocks_of(a.K);
     if (!splits) {
         splits = 1;
