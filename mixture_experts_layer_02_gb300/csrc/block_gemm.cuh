@@ -64,15 +64,12 @@ struct BlockCfg {
     static constexpr int STAGE = (1 + B_BOXES) * kBoxBytes;
     static constexpr int SLOTS = 512 / BN;                     // partial sums in TMEM
     static constexpr int COLS = BN / 2;                        // accumulator columns of an epilogue warp
-    // How the output leaves: in 64-byte pieces of eight rows, through 32 rows x 32 columns of
-    // shared memory a warp; or (the weight gradient of many rows, whose output is large and
-    // whose tiles are short) as bulk copies of 256 bytes under the next tile, for which all
-    // 32 rows x 128 columns wait in shared memory.  4093 rows x 4096 x 14336 by 8 experts, both
-    // gradients: 1080 us with bulk copies, 1128 without; pieces of 128 bytes or a stage less
-    // where the weights' stream is the limit cost more than they gain (229 for 162 us at 256
-    // tokens, 128 x 128 tiles; 782 for 718 us at 4096 x 7168 x 2048, 128 x 256).
-    static constexpr bool BULK = PAIR && KIND == BLOCK_WGRAD;
-    static constexpr int PITCH = BULK ? COLS * 2 + 16 : 64;    // bytes; BULK: eight rows' pieces on all banks
+    // How the output leaves: one-CTA tiles in 64-byte pieces of eight rows, through 32 rows x
+    // 32 columns of shared memory a warp.  Pairs keep all 32 rows x 128 columns there and let
+    // them leave as two tensor copies under the next tile, for two stages less; rows at the
+    // end of a segment, which a copy would not stop at, go by hand.
+    static constexpr bool BULK = PAIR;
+    static constexpr int PITCH = BULK ? COLS * 2 : 64;  // bytes of shared memory a row
     static constexpr int OUT = kEpiWarps * 32 * PITCH;
     static constexpr int STAGES = BULK ? 4 : 192 * 1024 / STAGE;
     static constexpr int CLUSTER = CTAS * SPLITS;
@@ -84,6 +81,7 @@ struct BlockCfg {
                (KIND == BLOCK_WGRAD ? E * sizeof(uint16_t) : 0);
     }
     static_assert(smem(kMaxE) <= 227 * 1024, "shared memory");
+    static_assert(!BULK || (STAGES * STAGE) % 1024 == 0, "swizzled boxes start on 1024 bytes");
     static_assert(SPLITS == 1 || STAGES * STAGE >= kBM * 128 * 4, "the parked accumulator reuses the stages");
     static_assert(!PAIR || (BN == 256 && SPLITS == 1), "pairs own whole 256 x 256 tiles");
     static_assert(SPLITS == 1 || BN == 128, "parts of K are joined on 128 x 128 tiles");
@@ -303,9 +301,13 @@ __device__ __forceinline__ void store_chunk(uint8_t* smem, uint16_t* out, long l
     }
 }
 
-// A row of `bytes` (a multiple of 16) from shared to global memory, in the background.
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+// A box of 32 rows x 64 bf16 (128-byte swizzle) from shared to global memory, in the
+// background; what lies outside the matrix is not written.
+__device__ __forceinline__ void store_box(const CUtensorMap* map, const void* src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // This thread's copies have read shared memory; or have ended.
@@ -326,7 +328,8 @@ __device__ __forceinline__ float4 ld_part(uint32_t addr) {
 
 template <int KIND, bool PAIR, int BN, int SPLITS>
 __global__ void __launch_bounds__(kThreads, 1)
-block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const BlockArgs args) {
+block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map,
+                  const __grid_constant__ CUtensorMap out_map, const BlockArgs args) {
     using C = BlockCfg<KIND, PAIR, BN, SPLITS>;
     constexpr int S = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -356,6 +359,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&a_map);
         tma_prefetch_desc(&b_map);
+        if (C::BULK) tma_prefetch_desc(&out_map);
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
@@ -524,24 +528,25 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                 if (rows > 0) {
                     uint16_t* out = args.out + (KIND == BLOCK_WGRAD ? static_cast<long long>(b.e) * args.M * args.N : 0LL);
                     const long long row0 = static_cast<long long>(b.row0) + in_tile;
+                    // the cell of 16 bytes that holds columns 8 p .. of row r
+                    auto cell = [&](int r, int p) {
+                        return C::BULK ? reinterpret_cast<uint4*>(out_rows + (p >> 3) * 4096 + sw128_offset(r, p & 7)) : chunk_cell(out_rows, r, p & 3);
+                    };
                     if constexpr (C::BULK) bulk_wait_read();  // the last tile's
                     __syncwarp();
 #pragma unroll
-                    for (int p = 0; p < C::COLS / 8; ++p) {  // eight columns
-                        auto cell = [&](int r) {
-                            return C::BULK ? reinterpret_cast<uint4*>(out_rows + r * C::PITCH + p * 16) : chunk_cell(out_rows, r, p & 3);
-                        };
+                    for (int p = 0; p < C::COLS / 8; ++p) {
                         if constexpr (KIND == BLOCK_WGRAD) {
                             constexpr int W = C::COLS / 2;
                             auto two = [&](int i) {
                                 const float2 v = acc[p / (W / 8) * (W / 2) + (i >> 1) * (W / 4) + p % (W / 8) * 2 + (i & 1)];
                                 return pack_bf16x2(v.x, v.y);
                             };
-                            st_blocks(cell(lane), two(0), two(1), two(2), two(3));
+                            st_blocks(cell(lane, p), two(0), two(1), two(2), two(3));
                         } else {
                             const float2* v = &acc[p * 4];
-                            *cell(lane) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
-                                                     pack_bf16x2(v[3].x, v[3].y));
+                            *cell(lane, p) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                                                        pack_bf16x2(v[3].x, v[3].y));
                         }
                         if constexpr (!C::BULK) {
                             if ((p & 3) == 3) {
@@ -552,12 +557,19 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
                         }
                     }
                     if constexpr (C::BULK) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        const int cols = min(C::COLS, args.N - col0);
-                        if (lane < rows && cols > 0)
-                            bulk_store(out + (row0 + lane) * args.N + col0, out_rows + lane * C::PITCH, static_cast<uint32_t>(cols) * 2);
-                        bulk_commit();
+                        if (KIND == BLOCK_WGRAD || rows == 32) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane < C::COLS / 64 && col0 + lane * 64 < args.N)
+                                store_box(&out_map, out_rows + lane * 4096, col0 + lane * 64, static_cast<int>(row0), KIND == BLOCK_WGRAD ? b.e : 0);
+                            bulk_commit();
+                        } else {
+                            __syncwarp();
+                            const int p = lane & 15;
+#pragma unroll 4
+                            for (int r = lane >> 4; r < rows; r += 2)
+                                if (col0 + p * 8 < args.N) *reinterpret_cast<uint4*>(out + (row0 + r) * args.N + col0 + p * 8) = *cell(r, p);
+                        }
                     }
                 }
             } else if constexpr (KIND == BLOCK_WGRAD) {  // the stages are free: every copy of this CTA's part was waited for
@@ -831,8 +843,7 @@ cudaError_t block_prepare(int* clusters) {
 
 // st_set: launch; else only tell how many clusters the device holds at once.
 template <int KIND, bool PAIR, int BN, int SPLITS>
-cudaError_t block_go(const BlockPlan& p, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs* a,
-                     cudaStream_t st, int* clusters) {
+cudaError_t block_go(const BlockPlan& p, const CUtensorMap* maps, const BlockArgs* a, cudaStream_t st, int* clusters) {
     int limit = 0;
     cudaError_t e = block_prepare<KIND, PAIR, BN, SPLITS>(&limit);
     if (e != cudaSuccess) return e;
@@ -845,20 +856,19 @@ cudaError_t block_go(const BlockPlan& p, const CUtensorMap* a_map, const CUtenso
     if (n < 1 || n * BlockCfg<KIND, PAIR, BN, SPLITS>::CLUSTER > 0x7fffffff) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = block_config<KIND, PAIR, BN, SPLITS>(a->E, n, attr, st);
-    return cudaLaunchKernelEx(&cfg, block_gemm_kernel<KIND, PAIR, BN, SPLITS>, *a_map, *b_map, *a);
+    return cudaLaunchKernelEx(&cfg, block_gemm_kernel<KIND, PAIR, BN, SPLITS>, maps[0], maps[1], maps[2], *a);
 }
 
 }  // namespace
 
 template <int KIND>
-cudaError_t block_pick(const BlockPlan& p, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs* a,
-                       cudaStream_t st, int* clusters) {
-    if (p.pair) return block_go<KIND, true, 256, 1>(p, a_map, b_map, a, st, clusters);
-    if (p.bn == 256) return block_go<KIND, false, 256, 1>(p, a_map, b_map, a, st, clusters);
+cudaError_t block_pick(const BlockPlan& p, const CUtensorMap* maps, const BlockArgs* a, cudaStream_t st, int* clusters) {
+    if (p.pair) return block_go<KIND, true, 256, 1>(p, maps, a, st, clusters);
+    if (p.bn == 256) return block_go<KIND, false, 256, 1>(p, maps, a, st, clusters);
     switch (p.splits) {
-        case 1: return block_go<KIND, false, 128, 1>(p, a_map, b_map, a, st, clusters);
-        case 2: return block_go<KIND, false, 128, 2>(p, a_map, b_map, a, st, clusters);
-        case 4: return block_go<KIND, false, 128, 4>(p, a_map, b_map, a, st, clusters);
+        case 1: return block_go<KIND, false, 128, 1>(p, maps, a, st, clusters);
+        case 2: return block_go<KIND, false, 128, 2>(p, maps, a, st, clusters);
+        case 4: return block_go<KIND, false, 128, 4>(p, maps, a, st, clusters);
         default: return cudaErrorInvalidConfiguration;
     }
 }

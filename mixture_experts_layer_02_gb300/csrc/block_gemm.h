@@ -33,14 +33,13 @@ struct BlockPlan {
     int bn, splits;
     long long tiles;
 };
-// Launches the product; clusters != NULL: launches nothing, tells how many clusters of
-// this kind the device holds at once (the maps and arguments may be NULL).
-cudaError_t block_fwd(const BlockPlan&, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs*, cudaStream_t,
-                      int* clusters);
-cudaError_t block_dgrad(const BlockPlan&, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs*, cudaStream_t,
-                        int* clusters);
-cudaError_t block_wgrad(const BlockPlan&, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs*, cudaStream_t,
-                        int* clusters);
+// Launches the product with the tensor maps of A and B (boxes of 128 x 128 bytes) and of
+// the output (boxes of 32 rows x 64 bf16; read by pairs only); clusters != NULL: launches
+// nothing, tells how many clusters of this kind the device holds at once (the maps and
+// arguments may be NULL).
+cudaError_t block_fwd(const BlockPlan&, const CUtensorMap* maps, const BlockArgs*, cudaStream_t, int* clusters);
+cudaError_t block_dgrad(const BlockPlan&, const CUtensorMap* maps, const BlockArgs*, cudaStream_t, int* clusters);
+cudaError_t block_wgrad(const BlockPlan&, const CUtensorMap* maps, const BlockArgs*, cudaStream_t, int* clusters);
 
 // BLOCK_FWD of a few rows an expert as a stream of weight rows, `warps` (1, 2, 4 or 8)
 // of a block's 8 sharing the same rows (block_gemv.cu).

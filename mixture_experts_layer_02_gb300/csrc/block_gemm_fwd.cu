@@ -3,9 +3,8 @@
 
 namespace moe {
 
-cudaError_t block_fwd(const BlockPlan& p, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs* a, cudaStream_t st,
-                     int* clusters) {
-    return block_pick<BLOCK_FWD>(p, a_map, b_map, a, st, clusters);
+cudaError_t block_fwd(const BlockPlan& p, const CUtensorMap* maps, const BlockArgs* a, cudaStream_t st, int* clusters) {
+    return block_pick<BLOCK_FWD>(p, maps, a, st, clusters);
 }
 
 }  // namespace moe

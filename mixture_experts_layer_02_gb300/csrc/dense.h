@@ -92,6 +92,8 @@ int make_bf16_map(CUtensorMap* m, const void* base, long long rows, long long co
 // The same for mats stacked [rows, cols] matrices of bytes: boxes of 128 columns x
 // 128 rows of one matrix; what lies outside a matrix reads as zeros.
 int make_byte_map(CUtensorMap* m, const void* base, long long mats, long long rows, long long cols);
+// Of bf16, with boxes of 64 columns x 32 rows, for output.
+int make_bf16_out_map(CUtensorMap* m, const void* base, long long mats, long long rows, long long cols);
 
 // moe_workspace_size of the dense operations (dense_api.cu); 0 for another name or invalid sizes.
 size_t dense_workspace_size(const char* op, int N, int D, int F);

@@ -160,21 +160,30 @@ int moe::make_bf16_map(CUtensorMap* m, const void* base, long long rows, long lo
     return make_tmap(m, base, rows, cols, box_rows, false, ld);
 }
 
-// The tensor map of stacked byte matrices, for the block-scaled products (train_api.cu).
-int moe::make_byte_map(CUtensorMap* m, const void* base, long long mats, long long rows, long long cols) {
+// Tensor maps of stacked matrices, boxes of 128 bytes of columns x box_rows rows of one.
+static moe_status make_stacked_map(CUtensorMap* m, const void* base, long long mats, long long rows, long long cols, int esize,
+                                   int box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(cols) * rows};
-    cuuint32_t box[3] = {kRowBytes, kBM, 1};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * esize, static_cast<cuuint64_t>(cols) * rows * esize};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(kRowBytes / esize), static_cast<cuuint32_t>(box_rows), 1};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = fn(m, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
-        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (bytes) failed (%d) mats=%lld rows=%lld cols=%lld", (int)r, mats,
-                    rows, cols);
+        return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (stacked) failed (%d) mats=%lld rows=%lld cols=%lld", (int)r, mats, rows,
+                    cols);
     return MOE_OK;
+}
+
+// For the block-scaled products (train_api.cu).
+int moe::make_byte_map(CUtensorMap* m, const void* base, long long mats, long long rows, long long cols) {
+    return make_stacked_map(m, base, mats, rows, cols, 1, kBM);
+}
+int moe::make_bf16_out_map(CUtensorMap* m, const void* base, long long mats, long long rows, long long cols) {
+    return make_stacked_map(m, base, mats, rows, cols, 2, 32);
 }
 
 namespace {

@@ -88,12 +88,11 @@ int env_int(const char* name, int dflt) {
     return f ? atoi(f) : dflt;
 }
 
-cudaError_t block(BlockKind kind, const BlockPlan& p, const CUtensorMap* a_map, const CUtensorMap* b_map, const BlockArgs* a,
-                  cudaStream_t st, int* clusters) {
+cudaError_t block(BlockKind kind, const BlockPlan& p, const CUtensorMap* maps, const BlockArgs* a, cudaStream_t st) {
     switch (kind) {
-        case BLOCK_FWD: return block_fwd(p, a_map, b_map, a, st, clusters);
-        case BLOCK_DGRAD: return block_dgrad(p, a_map, b_map, a, st, clusters);
-        default: return block_wgrad(p, a_map, b_map, a, st, clusters);
+        case BLOCK_FWD: return block_fwd(p, maps, a, st, nullptr);
+        case BLOCK_DGRAD: return block_dgrad(p, maps, a, st, nullptr);
+        default: return block_wgrad(p, maps, a, st, nullptr);
     }
 }
 
@@ -164,11 +163,13 @@ moe_status product(BlockKind kind, const uint8_t* a_codes, long long a_rows, lon
                    long long b_mats, long long b_rows, long long b_cols, const BlockArgs& a, cudaStream_t st) {
     const BlockPlan p = plan_block(kind, a);
     if (p.stream) return launched(launch_block_gemv(a_codes, b_codes, a, p.stream, st), "block-scaled product launch");
-    CUtensorMap am, bm;
-    int e = make_byte_map(&am, a_codes, 1, a_rows, a_cols);
-    if (e == 0) e = make_byte_map(&bm, b_codes, b_mats, b_rows, b_cols);
+    CUtensorMap m[3];
+    int e = make_byte_map(&m[0], a_codes, 1, a_rows, a_cols);
+    if (e == 0) e = make_byte_map(&m[1], b_codes, b_mats, b_rows, b_cols);
+    if (e == 0 && p.pair) e = make_bf16_out_map(&m[2], a.out, kind == BLOCK_WGRAD ? a.E : 1, a.M, a.N);
     if (e != 0) return static_cast<moe_status>(e);
-    return launched(block(kind, p, &am, &bm, &a, st, nullptr), "block-scaled product launch");
+    if (!p.pair) m[2] = m[0];
+    return launched(block(kind, p, m, &a, st), "block-scaled product launch");
 }
 
 BlockArgs block_args(const int32_t* offsets, int E, int rows, void* ws) {
