@@ -13,13 +13,14 @@
 // Its 128 x 256 partial sums take 256 clocks to read from TMEM and 256 to add (WGRAD, with
 // two scales a product, 512), on other pipes, but a slot is only refilled when all have
 // read it: what counts is the way from a slot's MMAs through a barrier, two reads and a
-// barrier back.  4096 tokens on 8 experts of 4096 x 14336: 418 us, 2.30 PFLOP/s, the tensor
-// pipe active in 54 % of the cycles; the same loop without reading the slots runs in 332 us,
-// without the additions in 383.  So a slot is freed as soon as a warp has its values in
+// barrier back.  4096 tokens on 8 experts of 4096 x 14336: 411 us, 2.34 PFLOP/s, the tensor
+// pipe active in 54 % of the cycles; the same loop without reading the slots runs in 332 us.  So a slot is freed as soon as a warp has its values in
 // registers, no arrival waits for memory, and scales come through shared memory (kept by the
 // epilogue's threads they cost spilled registers: 500 us).  Sixteen epilogue warps of 64
-// columns: 441 us; reads of 32 columns one ahead: 448 to 523.  WGRAD of the same sizes has
-// eight steps a tile: 0.6 us each and 2.5 us a tile, in which its rows are written.
+// columns: 441 for 420 us; reads of 32 columns one ahead: 448 to 523.  WGRAD of the same sizes
+// has eight steps a tile: about 0.6 us each and 2 us a tile around them.  Its rows leave as
+// tensor copies: both gradients 1020 us; as bulk copies of 256 bytes, 256 of them a tile,
+// 1075, as 64-byte pieces by the epilogue's own stores 1128 (FWD 430 so, 411 now).
 // With 128 rows an expert the weights' stream is the limit (4096 x 7168 x 2048 by 256 experts:
 // 728 us, 5.7 TB/s), and a warp whose 32 rows all lie behind the segment only frees its slots.
 //

@@ -109,11 +109,11 @@ long long row_tiles(const BlockArgs& a, int height) {
 //               its weights again: tiles win from 16 rows an expert on (7168 x 2048 14
 //               against 12), and 128 rows bound the turns of a batch that all goes to one.
 //   pairs       where an expert fills most of a 256-row tile: 4096 x 4096 x 14336 by 8
-//               experts (1024 rows each) 418, one-CTA tiles 450; at 128 rows each 112 and
-//               117, but 4096 x 7168 x 2048 by 256 experts (128 rows on average, ragged)
-//               817 and 728.  The weight gradient's tiles are all whole and its K is the
-//               rows: pairs from 512 rows an expert on (both gradients 4096^2 by 8 experts:
-//               512 rows 222 and 219, 1024 rows 334 and 353, 64 rows 117 and 100).
+//               experts (1024 rows each) 411, one-CTA tiles 450; at 128 rows each 119 both
+//               ways, but 4096 x 7168 x 2048 by 256 experts (128 rows on average, ragged)
+//               861 and 728, and 64 rows each 115 and 96.  The weight gradient's tiles are
+//               whole whatever the rows (both gradients 4096^2 by 8 experts: 64 rows 92 and
+//               100, 256 rows 133 and 162, 512 rows 197 and 217).
 //   128 x 256   else, where its tiles fill most of the GPU: 2048 x 768, 128 experts, 16384
 //               rows 61 against 65 for 128 x 128.
 //   128 x 128   else, with K in up to four parts while its tiles leave SMs idle: 7168 x 2048
@@ -134,7 +134,7 @@ BlockPlan plan_block(BlockKind kind, const BlockArgs& a) {
     if (kernel == 4 && kind != BLOCK_FWD) kernel = 1;
     if (kernel == 0) {
         const int mean = a.rows / a.E;
-        const bool high = kind == BLOCK_WGRAD ? a.M >= 160 && mean >= 512 : mean >= 160;
+        const bool high = (kind == BLOCK_WGRAD ? a.M : mean) >= 160;
         if (kind == BLOCK_FWD && (a.rows <= 8 || (mean <= 1 && a.rows <= 128))) kernel = 4;
         else if (high && tiles(2 * kBM, 256) >= 38) kernel = 3;
         else kernel = tiles(kBM, 256) >= 120 ? 2 : 1;
