@@ -592,7 +592,12 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
         if constexpr (C::BULK) bulk_wait();  // shared memory is given back, and the rows are written
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
-        if (warp == 0 || warp == 2) {  // copies: warp 0 A (it announces the stage's bytes), warp 2 B
+        // Copies: warp 0 A (it announces the stage's bytes), warp 2 B.  Each brings bytes of every
+        // stage, rows that exist or not: a stage that is complete without one of its copiers could
+        // be used up and filled again before that thread has seen it empty, which it then never
+        // does.  (Only the rows that exist, in boxes of 32, were no faster: 736 us both ways at
+        // 4096 x 7168 x 2048 by 256 experts.)
+        if (warp == 0 || warp == 2) {
             if (lane == 0) {
                 const bool is_a = warp == 0;
                 bool withhold = is_a && args.dbg && (*args.dbg & MOE_DBG_WITHHOLD_FIRST_LOAD) && blockIdx.x == 0;

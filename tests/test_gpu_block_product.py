@@ -209,6 +209,25 @@ def test_same_bits_every_time_and_in_a_graph(moe, monkeypatch, kernel):
     assert moe.read_device_error(wsp) == 0
 
 
+@pytest.mark.parametrize("kernel", ["1/1", "2", "3"])
+def test_many_calls_of_ragged_tiles(moe, monkeypatch, kernel):
+    """Tiles whose second half, last quarter or all but a row do not exist, in a long run of calls: no wait runs out and
+    every call gives the same bits."""
+    choose(monkeypatch, kernel)
+    counts, D, F = [130, 1, 100, 256, 31, 385, 0, 97, 128], 2064, 1040
+    off = offsets_of(counts)
+    xq, xs, wq, ws = forward_inputs(counts, D, F)
+    wsp = moe.workspace("combine")
+    first = moe.moe_grouped_linear_e4m3_block(xq, xs, wq, ws, expert_offsets=off, ws=wsp)
+    assert_within(first, *T.product(xq, xs, wq, ws, counts), "y")
+    y = torch.empty_like(first)
+    differs = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(1500):
+        moe.moe_grouped_linear_e4m3_block(xq, xs, wq, ws, expert_offsets=off, y=y, ws=wsp)
+        differs |= (y != first).any()
+    assert moe.read_device_error(wsp) == 0 and not differs
+
+
 def test_two_streams_at_once(moe):
     """Calls on two streams with a workspace each, many at a time."""
     sets = []
