@@ -118,7 +118,8 @@ quant_segments_kernel(const QuantSegArgs a) {
     // running sum of the segments' blocks (barriers would cost more)
     int carry = 0, first = -1, n = -1;  // first row, rows; n < 0: nothing here
     bool bad = false;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
+#pragma unroll 4
+    for (int e0 = 0; e0 < a.E; e0 += 32) {  // unrolled: the offsets' loads do not wait for one another
         const int e = e0 + lane;
         int lo = 0, len = 0;
         if (e < a.E) {
