@@ -13,14 +13,14 @@
 // Its 128 x 256 partial sums take 256 clocks to read from TMEM and 256 to add (WGRAD, with
 // two scales a product, 512), on other pipes, but a slot is only refilled when all have
 // read it: what counts is the way from a slot's MMAs through a barrier, two reads and a
-// barrier back.  4096 tokens on 8 experts of 4096 x 14336: 411 us, 2.34 PFLOP/s, the tensor
-// pipe active in 54 % of the cycles; the same loop without reading the slots runs in 332 us.  So a slot is freed as soon as a warp has its values in
+// barrier back.  4096 tokens on 8 experts of 4096 x 14336: 400 us, 2.40 PFLOP/s, the tensor
+// pipe active in 57 % of the cycles; the same loop without reading the slots runs in 332 us.  So a slot is freed as soon as a warp has its values in
 // registers, no arrival waits for memory, and scales come through shared memory (kept by the
 // epilogue's threads they cost spilled registers: 500 us).  Sixteen epilogue warps of 64
 // columns: 441 for 420 us; reads of 32 columns one ahead: 448 to 523.  WGRAD of the same sizes
 // has eight steps a tile: about 0.6 us each and 2 us a tile around them.  Its rows leave as
 // tensor copies: both gradients 1020 us; as bulk copies of 256 bytes, 256 of them a tile,
-// 1075, as 64-byte pieces by the epilogue's own stores 1128 (FWD 430 so, 411 now).
+// 1075, as 64-byte pieces by the epilogue's own stores 1128 (FWD 430 so, 411 with the copies).
 // With 128 rows an expert the weights' stream is the limit (4096 x 7168 x 2048 by 256 experts:
 // 728 us, 5.7 TB/s), and a warp whose 32 rows all lie behind the segment only frees its slots.
 //
@@ -148,9 +148,11 @@ __host__ __device__ constexpr uint32_t block_idesc(int M, int N) {
     return idesc_e4m3_f32(M, N) | (KIND == BLOCK_WGRAD ? 1u << 15 : 0u) | (KIND != BLOCK_FWD ? 1u << 16 : 0u);
 }
 
-// The MMA warp's walk over a ring of barriers, executed by all of its lanes.  A wait
-// on an mbarrier that is complete still takes about 200 clocks to answer, so the next
-// one is asked before this step's MMAs are issued.
+// A warp's walk over a ring of barriers, executed by all of its lanes.  A wait on an
+// mbarrier that is complete still takes about 200 clocks to answer, so a stage's is asked
+// before the MMAs of the one before are issued (AHEAD); a slot's, which is hardly ever
+// complete a step ahead, is not (403 for 408 us at 4096 x 4096 x 14336 by 8 experts).
+template <bool AHEAD>
 struct BarrierWalk {
     uint64_t* bar;
     int n, at;
@@ -164,7 +166,7 @@ struct BarrierWalk {
         if (!__all_sync(0xffffffffu, ok)) return false;
         __syncwarp();
         const int next = at + 1 == n ? 0 : at + 1;
-        ready = mbar_test_wait(&bar[next], next == 0 ? parity ^ 1u : parity);
+        ready = AHEAD && mbar_test_wait(&bar[next], next == 0 ? parity ^ 1u : parity);
         return true;
     }
     __device__ __forceinline__ void advance() {
@@ -644,7 +646,8 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
         } else if (warp == 1) {
             if (leader) {
                 constexpr uint32_t idesc = block_idesc<KIND>(C::ROWS, BN);
-                BarrierWalk stages(full, S, 0), slots(tempty, C::SLOTS, 1);
+                BarrierWalk<true> stages(full, S, 0);
+                BarrierWalk<false> slots(tempty, C::SLOTS, 1);
                 bool ok = true;
                 for (int t = first; ok && t < tiles; t += step) {
                     const BlockTile b = list.at<KIND>(t);
@@ -684,7 +687,7 @@ block_gemm_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_consta
         } else {
             // scales: rows 4 lane .. of this CTA, and the columns; loaded kAhead steps before their use
             constexpr int kAhead = 2, COLS4 = BN / 128;  // WGRAD: column quads of a lane
-            BarrierWalk slots(sempty, C::SLOTS, 1);
+            BarrierWalk<false> slots(sempty, C::SLOTS, 1);
             bool ok = true;
             const int nbs = (args.N + kBlock - 1) / kBlock;
             const int in_tile = (PAIR ? static_cast<int>(rank) * kBM : 0) + lane * 4;  // this lane's first row of the tile

@@ -109,9 +109,9 @@ long long row_tiles(const BlockArgs& a, int height) {
 //               its weights again: tiles win from 16 rows an expert on (7168 x 2048 14
 //               against 12), and 128 rows bound the turns of a batch that all goes to one.
 //   pairs       where an expert fills most of a 256-row tile: 4096 x 4096 x 14336 by 8
-//               experts (1024 rows each) 411, one-CTA tiles 450; at 128 rows each 119 both
+//               experts (1024 rows each) 404, one-CTA tiles 441; at 128 rows each 119 both
 //               ways, but 4096 x 7168 x 2048 by 256 experts (128 rows on average, ragged)
-//               861 and 728, and 64 rows each 115 and 96.  The weight gradient's tiles are
+//               872 and 729, and 64 rows each 115 and 96.  The weight gradient's tiles are
 //               whole whatever the rows (both gradients 4096^2 by 8 experts: 64 rows 92 and
 //               100, 256 rows 133 and 162, 512 rows 197 and 217).
 //   128 x 256   else, where its tiles fill most of the GPU: 2048 x 768, 128 experts, 16384
