@@ -109,6 +109,27 @@ def test_rows_behind_the_last_segment_stay(moe, monkeypatch, kernel):
     assert_within(dw, *want_dw, "dw")
 
 
+@pytest.mark.parametrize("kernel", KERNELS + [""])
+def test_no_rows_at_all(moe, monkeypatch, kernel):
+    """Rows that belong to no expert, and no rows: outputs stay, weight gradients are zero."""
+    choose(monkeypatch, kernel)
+    for rows in (5, 0):
+        off = torch.zeros(4, dtype=torch.int32, device="cuda")
+        xq, xs, wq, ws = forward_inputs([0, 0, 0], 144, 272, extra=rows)
+        y = torch.full((rows, 272), 7.0, dtype=torch.bfloat16, device="cuda")
+        moe.moe_grouped_linear_e4m3_block(xq, xs, wq, ws, expert_offsets=off, y=y)
+        (wq, ws), (dyq, dys), seg = backward_inputs(moe, [0, 0, 0], 144, 272, extra=rows)
+        dx = torch.full((rows, 144), 7.0, dtype=torch.bfloat16, device="cuda")
+        dw = torch.full((3, 272, 144), 7.0, dtype=torch.bfloat16, device="cuda")
+        wsp = moe.workspace("combine")
+        moe.moe_grouped_linear_e4m3_block_backward(wq, ws, dyq, dys, *seg, expert_offsets=off, dx=dx, dw=dw, ws=wsp)
+        assert moe.read_device_error(wsp) == 0
+        assert (y == 7).all() and (dx == 7).all() and (dw == 0).all()
+        src = torch.ones((rows, 144), dtype=torch.bfloat16, device="cuda")
+        q_seg = torch.full((moe.segment_rows(rows, 3), 144), 99, dtype=torch.uint8, device="cuda")
+        assert (moe.moe_quantize_e4m3_segments(src, off, both=False, q_seg=q_seg)[2] == 99).all()
+
+
 def test_dense_form_needs_no_offsets(moe):
     xq, xs, wq, ws = forward_inputs([37], 528, 272)
     a = moe.moe_grouped_linear_e4m3_block(xq, xs, wq, ws)
