@@ -943,9 +943,8 @@ def moe_combine_backward(dout, y_perm, inv_perm, topk_w, dy_perm=None, dtopk_w=N
     rows = _rows(y_perm, "y_perm")[0]
     if dy_perm is None:
         dy_perm, = _new(stream, ((rows, D), _BF16, dout.device))
-        if rows != N * K:
-            with torch.cuda.stream(stream):
-                dy_perm.zero_()
+        with torch.cuda.stream(stream):  # as many rows as assignments may still hold empty slots
+            dy_perm.zero_()
     if dtopk_w is None:
         dtopk_w, = _new(stream, ((N, K), _F32, dout.device))
     if ws is None:
@@ -1041,7 +1040,8 @@ def segment_rows(rows: int, E: int) -> int:
 def moe_quantize_e4m3_segments(src, expert_offsets, both: bool = True, q=None, scale=None, q_seg=None, scale_seg=None,
                                ws=None, stream=None):
     """e4m3 codes of src [rows, cols] along each expert's rows, as the weight gradient reads them, and (with both=True,
-    or where passed) along its columns: (q, scale, q_seg, scale_seg).  expert_offsets [E+1], or None for one segment."""
+    or where passed) along its columns: (q, scale, q_seg, scale_seg).  expert_offsets [E+1], or None for one segment.
+    Rows behind the last segment are not written."""
     rows, cols = _rows(src, "src")
     E = 1 if expert_offsets is None else expert_offsets.shape[0] - 1
     seg = segment_rows(rows, E)
@@ -1077,7 +1077,7 @@ def moe_grouped_linear_e4m3_block(xq, x_scale, wq, w_scale, expert_offsets=None,
                                   stream=None):
     """y = x w^T of each expert's rows, both in e4m3 with a scale for each block of 128 (as moe_quantize_e4m3_block makes
     them, or any fp32 scales): xq [rows, D], wq [E, F, D].  x_scale_index (perm_src) finds the row of x_scale; without
-    expert_offsets E is 1: a dense product."""
+    expert_offsets E is 1: a dense product.  Rows of y behind the last segment are not written."""
     rows, D = _rows(xq, "xq")
     E, F, _ = _weights(wq)
     n = _rows(x_scale, "x_scale")[0]
@@ -1100,7 +1100,8 @@ def moe_grouped_linear_e4m3_block(xq, x_scale, wq, w_scale, expert_offsets=None,
 def moe_grouped_linear_e4m3_block_backward(wq, w_scale, dyq, dy_scale, dyq_seg, dy_scale_seg, xq_seg, x_scale_seg,
                                            expert_offsets=None, dx=None, dw=None, ws=None, stream=None):
     """Gradients (dx, dw) of moe_grouped_linear_e4m3_block from quantised operands: the incoming gradient along its columns
-    (dyq, dy_scale) for dx and along its rows (dyq_seg, dy_scale_seg) for dw, x along its rows (xq_seg, x_scale_seg)."""
+    (dyq, dy_scale) for dx and along its rows (dyq_seg, dy_scale_seg) for dw, x along its rows (xq_seg, x_scale_seg).  Rows of dx
+    behind the last segment are not written; dw of an expert without rows is zero."""
     E, F, D = _weights(wq)
     rows = _rows(dyq, "dyq")[0]
     seg = segment_rows(rows, E)

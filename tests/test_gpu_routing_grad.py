@@ -138,6 +138,22 @@ def routed(g, N, D, E, K, sigmoid, duplicate=False):
     return x, wg, logits, ids, w.contiguous(), torch.randn((N, K), generator=g, device="cuda")
 
 
+def test_empty_slots_of_a_buffer_made_here_are_zero(moe):
+    """As many slots as assignments, some dropped and some empty: capacity factor one under a lopsided routing."""
+    N, D, E, K = 64, 256, 4, 2
+    cap = N * K // E
+    x = normal(gen(5), N, D)
+    ids = torch.tensor([0, 1], dtype=torch.int32, device="cuda").repeat(N, 1)
+    w = torch.rand((N, K), generator=gen(6), device="cuda")
+    _, kept, slot, x_pad = moe.moe_permute_padded(x, ids, E, cap)
+    assert kept.tolist() == [cap, cap, 0, 0] and (slot < 0).sum() == N * K - 2 * cap
+    ws = moe.workspace("combine")
+    held = [torch.full((E * cap, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(64)]
+    del held  # every free block of this size holds NaN
+    dy, _ = moe.moe_combine_backward(x, x_pad, slot, w, ws=ws)
+    assert (dy[2 * cap:] == 0).all() and torch.isfinite(dy).all()
+
+
 @pytest.mark.parametrize("N,D,E,K", [(1, 64, 8, 2), (3, 8, 4, 4), (100, 2048, 128, 8), (77, 520, 60, 6), (513, 256, 7, 3),
                                      (40, 136, 1024, 32), (300, 1032, 256, 8), (5, 64, 1, 1)])
 @pytest.mark.parametrize("sigmoid", [False, True])
