@@ -580,8 +580,10 @@ moe_status moe_quantize_e4m3_segments(const moe_bf16* src, const int32_t* expert
  *   expert_offsets [E+1] (checked as above) or NULL with E = 1: a dense product
  *   wq [E,F,D] codes, w_scale [E, ceil(F/128), ceil(D/128)] fp32
  *   y [total_rows, F] bf16 out; rows behind the last segment are left as they were
- * Each block's partial sum is scaled and added in fp32.  D and F are positive
- * multiples of 16, E <= 1024. */
+ * Each block's partial sum is scaled and added in fp32; the two scales are
+ * multiplied first, and where their product leaves fp32's range the result does too
+ * (0, inf, or NaN from a partial sum of 0).  D and F are positive multiples of 16,
+ * E <= 1024. */
 moe_status moe_grouped_linear_e4m3_block(const uint8_t* xq, const float* x_scale, const int32_t* x_scale_index,
                                          int x_scale_rows, const int32_t* expert_offsets, int total_rows,
                                          const uint8_t* wq, const float* w_scale, int E, int D, int F, moe_bf16* y,
